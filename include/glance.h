@@ -26,7 +26,10 @@
  * (glance_accept_commit_gated), one tree budget shared by a batch
  * (glance_build_tree_shared), and the target's dense layers around tree
  * attention (glance_dense_qkv, glance_dense_residual, glance_dense_swiglu,
- * glance_row_sumsq).
+ * glance_row_sumsq), query / key norm with rotary positions of several axes
+ * for any number of rows (glance_qk_norm_rope), and the round on K/V caches
+ * held in 4 bits (glance_kv4_write_rows, glance_kv4_read_rows,
+ * glance_kv4_tree_attention, glance_kv4_accept_commit).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -532,6 +535,164 @@ glance_status glance_dense_swiglu(const void* h, const void* W_gate, const void*
                                   int d, int inter, const float* in_sumsq, int n_sumsq, float eps,
                                   void* act, void* stream);
 
+/* ------------------------------------------------- query / key norm + rotary */
+
+/*
+ * Rotary positions as a host plan: for each of head_dim / 2 frequencies the
+ * angle per position and the position axis that turns it. Fill it with
+ * glance_rope_init once and pass it to glance_qk_norm_rope, which copies it.
+ */
+typedef struct {
+  int32_t head_dim;  /* 32, 64 or 128; every dim is rotated */
+  int32_t n_axes;    /* 1..4 position axes */
+  uint64_t turn[64]; /* frequency j per unit of position, in turns, the
+                        fraction of one turn times 2^64 */
+  uint8_t axis[64];  /* which axis turns frequency j */
+} glance_rope;
+
+/*
+ * Frequencies theta^(-2j / head_dim), j = 0 .. head_dim/2 - 1, shared out to
+ * n_axes position axes (text: one; an image or video token: time, height,
+ * width). sections (host int32 [n_axes], each >= 1, their sum head_dim / 2;
+ * nullable when n_axes is 1): how many frequencies each axis turns.
+ * interleaved 0: axis 0 has the first sections[0] frequencies, axis 1 the next
+ * and so on. interleaved 1: frequency j goes to axis j mod n_axes while that
+ * axis has had fewer than its section, else to axis 0 (every axis but 0 needs
+ * sections[a] <= (head_dim / 2 - a + n_axes - 1) / n_axes). theta: finite, > 0.
+ */
+glance_status glance_rope_init(glance_rope* rope, int head_dim, double theta, int n_axes,
+                               const int32_t* sections, int interleaved);
+
+/*
+ * Query and key rows made ready for attention in one pass, for any number of
+ * rows (a prompt's text and image tokens before the first round, or a round's
+ * tree rows where the projection was made elsewhere): per-head RMS norm of q
+ * and k, rotate-half rotary position, q to q_out, k and v into the caches.
+ * For request r of B (1 <= B <= 16) and row i of M (M >= 1), with row r M + i:
+ *   qkv    [B M] rows of (n_q_heads + 2 n_kv_heads) * head_dim elements (q
+ *          heads, k heads, v heads), row_stride elements apart;
+ *   y      = x / sqrt(mean x^2 + eps) * w for q heads (w = q_norm) and k heads
+ *          (w = k_norm); a null w leaves that kind as it is; v is copied;
+ *   dims j and j + head_dim/2 of y turn by pos[axis(j)][r M + i] * freq(j);
+ *   q_out  [B M][n_q_heads][head_dim];
+ *   k, v   to slots T + i of kv[r] (host array of B views, one geometry but
+ *          for t_cap and strides, T = *kv[r].t_len; T is not changed).
+ * pos: device int32 [n_axes][B M]. q_norm, k_norm: device float [head_dim].
+ * All arithmetic is fp32; angles are exact to 2^-32 of a turn at any int32
+ * position. dtype BF16 or F32 (that of kv); head_dim 32, 64 or 128. Arrays
+ * 16-byte aligned, strides multiples of 16 bytes; q_out must not overlap qkv.
+ * A request with T + M > t_cap sets device status 2 and none of its cache rows
+ * are written.
+ */
+glance_status glance_qk_norm_rope(const void* qkv, glance_dtype dtype, int B, int M,
+                                  int64_t row_stride, int n_q_heads, const float* q_norm,
+                                  const float* k_norm, float eps, const int32_t* pos,
+                                  const glance_rope* rope, void* q_out, const glance_kv* kv,
+                                  void* stream);
+
+/* ------------------------------------------------------------- 4-bit caches */
+
+/*
+ * One layer's K/V cache in 4 bits. Each slot of each kv head is head_dim codes
+ * of 4 bits and one scale of 8 bits per 16 elements. A code is a sign, two
+ * exponent bits and one fraction bit (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6);
+ * element 2i of a row is in the low half of byte i, element 2i + 1 in its high
+ * half. A scale is an e4m3 number >= 0; 0x7F (not a number) marks a group that
+ * held an infinity or NaN. An element stands for code * scale * global. Slot s
+ * of head h has its codes at k + (h * head_stride + s) * head_dim / 2 bytes and
+ * its scales at k_scale + (h * head_stride + s) * head_dim / 16 bytes; both
+ * arrays span n_kv_heads * head_stride slots. Slots past the committed prefix
+ * and the tree rows may hold anything.
+ */
+typedef struct {
+  void* k;             /* device, 16-byte aligned, like the three below */
+  void* k_scale;
+  void* v;
+  void* v_scale;
+  float k_global;      /* finite, 2^-60 .. 2^60 */
+  float v_global;
+  int32_t n_kv_heads;
+  int32_t head_dim;    /* 128 */
+  int32_t t_cap;       /* slots per head that may be used (<= 2^30) */
+  int64_t head_stride; /* slots between heads: >= t_cap, even */
+  int32_t* t_len;      /* device int32: T, the committed prefix length */
+} glance_kv4;
+
+/*
+ * glance_kv_write_rows for 4-bit caches: rows of K and V, quantised, to slots
+ * T .. T + rows - 1 of every layer in one launch (a prompt's rows, or a
+ * round's tree rows before attention reads them).
+ * src: device BF16 [n_layers][2][n_kv_heads][rows][128] (K before V),
+ * contiguous, 32-byte aligned. Per group of 16 elements x, in fp32:
+ * t = x / global; scale = max|t| / 6 rounded to e4m3 (nearest even, at most
+ * 448); code = t / scale rounded to nearest even, at most 6 (0 where the scale
+ * is 0). A group with a t that is not finite gets the scale 0x7F and codes 0.
+ * Each row is quantised by itself, so a row reads the same whether it was
+ * written alone, in a prompt or as a tree row.
+ * layers: host array with one t_len, geometry and pair of globals. If
+ * T + rows > t_cap the call sets device status 2 and writes nothing.
+ * Limits: 1 <= n_layers <= 128, rows >= 1.
+ */
+glance_status glance_kv4_write_rows(const void* src, const glance_kv4* layers, int n_layers,
+                                    int rows, void* stream);
+
+/*
+ * The values that slots first .. first + rows - 1 of every layer stand for, as
+ * BF16 [n_layers][2][n_kv_heads][rows][128] (dst, contiguous, 32-byte aligned;
+ * rounded once, nearest even): back to a 16-bit cache or to the host.
+ * 0 <= first, first + rows <= t_cap; T is not looked at. Otherwise as
+ * glance_kv4_write_rows.
+ */
+glance_status glance_kv4_read_rows(const glance_kv4* layers, int n_layers, int first, int rows,
+                                   void* dst, void* stream);
+
+/* Workspace bytes for glance_kv4_tree_attention (0 on bad sizes); depends on
+ * every request's t_cap, so pass the same kv array as to the call. */
+size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_heads,
+                                                 const glance_kv4* kv);
+
+/*
+ * glance_tree_attention over 4-bit caches, for B requests of one layer
+ * (1 <= B <= 16): q and out [B][N+1][n_q_heads][128] BF16; kv: host array [B],
+ * request r's cache (its own arrays, t_cap, head_stride, globals and t_len;
+ * n_kv_heads shared); trees: host array [B] of one N (0 <= N <= 255), of which
+ * anc is read. N = 0 is plain decoding: one row per request, which sees the
+ * prefix and its own slot T (anc may then be null: a row that sees itself).
+ * Row i sees the prefix slots 0..T-1 and the tree slots T + k for every k with
+ * anc bit (i, k). A row that sees no slot at all gives zeros. What a slot that
+ * a row does not see holds never reaches that row; a slot that it does see
+ * and that has a scale that is not a number makes the row NaN, all of it or
+ * the elements of that scale's group.
+ * n_q_heads / n_kv_heads in {1, 2, 4, 8}; scale finite and > 0; q, out 16-byte
+ * aligned and not overlapping, workspace 256-byte aligned. A request with
+ * T + N + 1 > t_cap sets device status 2 and its out is left as it was.
+ * The codes are widened to f16, which holds code * scale exactly; q is rounded
+ * to f16 after each row is scaled by a power of two; the softmax weights are
+ * rounded to f16; all sums are fp32.
+ */
+glance_status glance_kv4_tree_attention(const void* q, int n_q_heads, const glance_kv4* kv,
+                                        const glance_tree* trees, int B, float scale, void* out,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for glance_kv4_accept_commit (0 on bad sizes). */
+size_t glance_kv4_accept_commit_workspace_bytes(int B, int n_layers);
+
+/*
+ * glance_accept_commit_batched, or with gap and gated (both given, or both
+ * null) glance_accept_commit_gated_batched, on 4-bit caches; B = 1 for one
+ * request. The path rows' codes and scales move from slots T + path_i to slots
+ * T + i as they are (no requantisation), then T += a + 1. layers: host array
+ * [B][n_layers]; the layers of a request share t_len and geometry, no two
+ * requests share a t_len. Limits: 1 <= N <= 255, 1 <= n_layers <= 128,
+ * B * n_layers <= 960.
+ */
+glance_status glance_kv4_accept_commit(const glance_tree* trees, int B, const int32_t* argmax,
+                                       const float* gap, float gate_threshold,
+                                       const glance_kv4* layers, int n_layers,
+                                       int32_t* n_accepted, int32_t* accepted_tok,
+                                       int32_t* new_root, int32_t* gated, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ status */
 
 /* Text of the last host-side error on this thread ("" if none). */
@@ -556,7 +717,9 @@ glance_status glance_reset_device_status(void);
  * the work already there, copies of the status word of each kernel family
  * into status_out[1..5] (tree build, tree attention, LM head, walk + commit,
  * dense layers) and a one-thread kernel that stores the first non-zero of
- * them in status_out[0] (0 if none). status_out: GLANCE_STATUS_WORDS int32,
+ * them in status_out[0] (0 if none). The 4-bit attention reports with tree
+ * attention, the other 4-bit calls with walk + commit, glance_qk_norm_rope
+ * with the dense layers. status_out: GLANCE_STATUS_WORDS int32,
  * device memory or pinned / managed host memory (the caller reads it once
  * the stream has reached this point). No host or device-wide synchronisation,
  * so a serving loop can append it to every captured round. The words are not

@@ -10,6 +10,11 @@ The compute lives in ``libglance.so`` (CUDA kernels behind a C ABI declared in
 
 ``*_batched`` forms run B independent requests (ragged prefix lengths) in one
 launch per step; the LM head takes the B requests' rows stacked.
+
+* ``qk_norm_rope``  per-head RMS norm of q and k + rotary position (one axis,
+                    or several for image and video tokens), k and v cached
+* ``kv4_*``         the round on K/V caches held in 4 bits: rows written and
+                    read, tree attention (one row: decoding), walk + commit
 """
 from ._binding import (STATUS_WORDS, BF16, EXPORTS, F32, LIB_PATH, GlanceError, KVLayer, Tree, accept_commit,
                        accept_commit_batched, accept_commit_batched_workspace_bytes,
@@ -24,7 +29,9 @@ from ._binding import (STATUS_WORDS, BF16, EXPORTS, F32, LIB_PATH, GlanceError, 
                        lmhead_argmax_packed, lmhead_pack_w, lmhead_packed_w_bytes,
                        lmhead_argmax_workspace_bytes, reset_device_status, tree_attention,
                        tree_attention_timeout_check, tree_attention_batched, tree_attention_batched_workspace_bytes,
-                       tree_attention_workspace_bytes, version, workspace)
+                       tree_attention_workspace_bytes, version, workspace,
+                       KV4Layer, Rope, Views, kv4_accept_commit, kv4_accept_commit_workspace_bytes, kv4_read_rows,
+                       kv4_tree_attention, kv4_tree_attention_workspace_bytes, kv4_write_rows, qk_norm_rope)
 
 __all__ = ["STATUS_WORDS", "BF16", "EXPORTS", "F32", "LIB_PATH", "GlanceError", "KVLayer", "Tree",
            "accept_commit", "accept_commit_batched", "accept_commit_batched_workspace_bytes",
@@ -38,4 +45,5 @@ __all__ = ["STATUS_WORDS", "BF16", "EXPORTS", "F32", "LIB_PATH", "GlanceError", 
            "lmhead_argmax_packed", "lmhead_pack_w", "lmhead_packed_w_bytes",
            "reset_device_status", "tree_attention", "tree_attention_timeout_check", "tree_attention_batched",
            "tree_attention_batched_workspace_bytes", "tree_attention_workspace_bytes", "version",
-           "workspace"]
+           "workspace", "KV4Layer", "Rope", "Views", "kv4_accept_commit", "kv4_accept_commit_workspace_bytes",
+           "kv4_read_rows", "kv4_tree_attention", "kv4_tree_attention_workspace_bytes", "kv4_write_rows", "qk_norm_rope"]

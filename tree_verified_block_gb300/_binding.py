@@ -34,6 +34,10 @@ EXPORTS = [
     "glance_row_sumsq", "glance_dense_qkv",
     "glance_dense_residual", "glance_dense_swiglu",
     "glance_accept_commit_gated_batched",
+    "glance_rope_init", "glance_qk_norm_rope",
+    "glance_kv4_write_rows", "glance_kv4_read_rows",
+    "glance_kv4_tree_attention_workspace_bytes", "glance_kv4_tree_attention",
+    "glance_kv4_accept_commit_workspace_bytes", "glance_kv4_accept_commit",
     "glance_last_error", "glance_status_string", "glance_device_status",
     "glance_reset_device_status", "glance_get_status", "glance_kv_write_rows", "glance_clear_status", "glance_version",
 ]
@@ -57,6 +61,18 @@ class KVC(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("t_cap", ctypes.c_int32), ("head_stride", ctypes.c_int64),
                 ("row_stride", ctypes.c_int64), ("t_len", ctypes.c_void_p)]
+
+
+class KV4C(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_global", ctypes.c_float), ("v_global", ctypes.c_float),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("t_cap", ctypes.c_int32),
+                ("head_stride", ctypes.c_int64), ("t_len", ctypes.c_void_p)]
+
+
+class RopeC(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("turn", ctypes.c_uint64 * 64),
+                ("axis", ctypes.c_uint8 * 64)]
 
 
 _lib = None
@@ -144,6 +160,22 @@ def lib():
                                                      ctypes.c_float, ctypes.POINTER(KVC), i32, vp,
                                                      vp, vp, vp, vp, sz, vp]
     L.glance_accept_commit_gated_batched.restype = st
+    L.glance_rope_init.argtypes = [ctypes.POINTER(RopeC), i32, ctypes.c_double, i32, ctypes.POINTER(ctypes.c_int32), i32]
+    L.glance_rope_init.restype = st
+    L.glance_qk_norm_rope.argtypes = [vp, i32, i32, i32, ctypes.c_int64, i32, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp]
+    L.glance_qk_norm_rope.restype = st
+    L.glance_kv4_write_rows.argtypes = [vp, vp, i32, i32, vp]
+    L.glance_kv4_write_rows.restype = st
+    L.glance_kv4_read_rows.argtypes = [vp, i32, i32, i32, vp, vp]
+    L.glance_kv4_read_rows.restype = st
+    L.glance_kv4_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, vp]
+    L.glance_kv4_tree_attention_workspace_bytes.restype = sz
+    L.glance_kv4_tree_attention.argtypes = [vp, i32, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp]
+    L.glance_kv4_tree_attention.restype = st
+    L.glance_kv4_accept_commit_workspace_bytes.argtypes = [i32, i32]
+    L.glance_kv4_accept_commit_workspace_bytes.restype = sz
+    L.glance_kv4_accept_commit.argtypes = [vp, i32, vp, vp, ctypes.c_float, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.glance_kv4_accept_commit.restype = st
     L.glance_last_error.argtypes = []
     L.glance_last_error.restype = ctypes.c_char_p
     L.glance_status_string.argtypes = [st]
@@ -232,6 +264,74 @@ class KVLayer:
         Hkv, t_cap, D = k.shape
         self.c = KVC(_ptr(k).value, _ptr(v).value, _dtype_code(k), Hkv, D, t_cap,
                      k.stride(0), k.stride(1), _ptr(t_len).value)
+
+
+class KV4Layer:
+    """One layer's 4-bit cache view (include/glance.h, glance_kv4): codes k, v
+    uint8 [n_kv_heads][t_cap][64] and their scales uint8 (or float8_e4m3fn)
+    [n_kv_heads][t_cap][8], one factor for all of K and one for all of V."""
+
+    def __init__(self, k, k_scale, v, v_scale, t_len, k_global=1.0, v_global=1.0):
+        Hkv, t_cap, _ = k.shape
+        heads = {t.stride(0) // w for t, w in ((k, 64), (k_scale, 8), (v, 64), (v_scale, 8))} if Hkv > 1 else {t_cap + t_cap % 2}
+        for t, w in ((k, 64), (k_scale, 8), (v, 64), (v_scale, 8)):
+            if t.shape != (Hkv, t_cap, w) or t.element_size() != 1 or t.stride(2) != 1 or t.stride(1) != w or (
+                    Hkv > 1 and t.stride(0) % w):
+                raise ValueError("glance: a 4-bit cache has one-byte codes [n_kv_heads, t_cap, 64] and scales "
+                                 "[n_kv_heads, t_cap, 8] with whole rows next to each other")
+            if t.device != k.device:
+                raise ValueError("glance: codes and scales must be on one device")
+        if len(heads) != 1:
+            raise ValueError("glance: codes and scales need the same number of slots between heads")
+        if Hkv == 1 and t_cap % 2:
+            raise ValueError("glance: a 4-bit cache needs an even number of slots")
+        if t_len.dtype != torch.int32 or t_len.numel() != 1:
+            raise ValueError("glance: t_len must be one int32")
+        self.k, self.k_scale, self.v, self.v_scale, self.t_len = k, k_scale, v, v_scale, t_len
+        self.device = k.device
+        self.c = KV4C(_ptr(k).value, _ptr(k_scale).value, _ptr(v).value, _ptr(v_scale).value, float(k_global),
+                      float(v_global), Hkv, 128, t_cap, heads.pop(), _ptr(t_len).value)
+
+    @classmethod
+    def empty(cls, n_kv_heads, t_cap, t_len, k_global=1.0, v_global=1.0, device="cuda"):
+        """A zero-filled cache of t_cap slots (rounded up to an even number)."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        n = t_cap + t_cap % 2
+        return cls(torch.zeros((n_kv_heads, n, 64), **u8), torch.zeros((n_kv_heads, n, 8), **u8),
+                   torch.zeros((n_kv_heads, n, 64), **u8), torch.zeros((n_kv_heads, n, 8), **u8), t_len, k_global, v_global)
+
+
+class Views(list):
+    """A list of Tree, KVLayer or KV4Layer objects with their C array laid out
+    once: calls that take a list of them accept it without building the array
+    again. The list must not be changed afterwards."""
+
+    def __init__(self, items):
+        super().__init__(items)
+        if not self:
+            raise ValueError("glance: an empty list of views")
+        self.c = (type(self[0].c) * len(self))(*[x.c for x in self])
+
+
+def _views(x, kind):
+    """The C array of a Views, a list of views, or one view; its items checked."""
+    if not isinstance(x, Views):
+        x = Views(x if isinstance(x, (list, tuple)) else [x])
+    if not isinstance(x[0], kind):
+        raise TypeError(f"glance: expected {kind.__name__} views, got {type(x[0]).__name__}")
+    return x
+
+
+class Rope:
+    """Rotary positions as a plan (glance_rope_init): sections = how many of the
+    head_dim / 2 frequencies each position axis turns (None: one axis)."""
+
+    def __init__(self, head_dim, theta, sections=None, interleaved=False):
+        self.c = RopeC()
+        sec = list(sections) if sections is not None else [head_dim // 2]
+        _check(lib().glance_rope_init(ctypes.byref(self.c), head_dim, float(theta), len(sec),
+                                      (ctypes.c_int32 * len(sec))(*sec), int(bool(interleaved))))
+        self.head_dim, self.n_axes = head_dim, len(sec)
 
 
 # ------------------------------------------------------------------- calls
@@ -359,10 +459,14 @@ def accept_commit_gated(tree, argmax, gap, threshold, layers, n_accepted, accept
 # ------------------------------------------------------------ batched calls
 
 def _trees(trees):
+    if isinstance(trees, Views):
+        return trees.c
     return (TreeC * len(trees))(*[t.c for t in trees])
 
 
 def _kvs(kvs):
+    if isinstance(kvs, Views):
+        return kvs.c
     return (KVC * len(kvs))(*[k.c for k in kvs])
 
 
@@ -484,6 +588,141 @@ def dense_swiglu(h, W_gate, W_up, in_sumsq, eps, act, stream=None):
     _check(lib().glance_dense_swiglu(_ptr(h), _ptr(W_gate), _ptr(W_up), M, d, inter, _ptr(in_sumsq),
                                      _n_parts(in_sumsq, M), float(eps), _ptr(act),
                                      _stream(stream, h.device)))
+
+
+# ------------------------------------------- norm + rotary, 4-bit caches
+
+def _on(stream, *tensors):
+    """The stream to launch on: the given one, else the tensors' device's
+    current one. All tensors must be on the current device."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("glance: every array argument must be a CUDA tensor of one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("glance: the tensors are not on the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream
+
+
+def qk_norm_rope(qkv, n_q_heads, q_norm, k_norm, eps, pos, rope, q_out, kv, stream=None):
+    """qkv [B * M][(Hq + 2 Hkv) * D] (rows may be strided) -> per-head RMS norm
+    of q and k, rotary position, q to q_out [B * M][Hq][D], k and v to slots
+    T.. of kv (one KVLayer, or B of them). pos int32 [n_axes][B * M]."""
+    kv = _views(kv, KVLayer)
+    B, rows = len(kv), qkv.shape[0]
+    D, Hkv = kv[0].c.head_dim, kv[0].c.n_kv_heads
+    if (qkv.dim() != 2 or qkv.stride(1) != 1 or rows % B or qkv.shape[1] != (n_q_heads + 2 * Hkv) * D or rope.head_dim != D):
+        raise ValueError("glance: qkv must be [B * M, (n_q_heads + 2 * n_kv_heads) * head_dim], rope and kv of its head_dim")
+    if pos.dtype != torch.int32 or pos.shape[-1] != rows or pos.numel() != rope.n_axes * rows or not pos.is_contiguous():
+        raise ValueError("glance: pos must be contiguous int32 [n_axes, B * M]")
+    if q_out.dtype != qkv.dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
+        raise ValueError("glance: q_out must be contiguous [B * M, n_q_heads, head_dim] of qkv's dtype")
+    tensors = [qkv, pos, q_out, kv[0].k]
+    for w in (q_norm, k_norm):
+        if w is not None:
+            if w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous():
+                raise ValueError("glance: norm weights must be contiguous float32 [head_dim]")
+            tensors.append(w)
+    s = _on(stream, *tensors)
+    stride = qkv.stride(0) if rows > 1 else qkv.shape[1]
+    _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _dtype_code(qkv), B, rows // B, stride, n_q_heads,
+                                     None if q_norm is None else q_norm.data_ptr(),
+                                     None if k_norm is None else k_norm.data_ptr(), eps, pos.data_ptr(),
+                                     ctypes.addressof(rope.c), q_out.data_ptr(), ctypes.addressof(kv.c), s))
+
+
+def _rows16(x, n_layers, kv, rows):
+    if (x.dtype != torch.bfloat16 or not x.is_contiguous() or
+            tuple(x.shape) != (n_layers, 2, kv[0].c.n_kv_heads, rows, 128)):
+        raise ValueError("glance: rows must be contiguous bfloat16 [n_layers, 2, n_kv_heads, rows, 128]")
+
+
+def kv4_write_rows(src, layers, rows, stream=None):
+    """Quantise src [n_layers, 2, n_kv_heads, rows, 128] (bf16, K before V) into
+    every layer's 4-bit cache at slots T..T+rows-1 (T read on the device)."""
+    layers = _views(layers, KV4Layer)
+    _rows16(src, len(layers), layers, rows)
+    s = _on(stream, src, layers[0].k)
+    _check(lib().glance_kv4_write_rows(src.data_ptr(), ctypes.addressof(layers.c), len(layers), rows, s))
+
+
+def kv4_read_rows(layers, first, rows, dst, stream=None):
+    """dst [n_layers, 2, n_kv_heads, rows, 128] (bf16) = the values of slots
+    first .. first + rows - 1 of every layer's 4-bit cache."""
+    layers = _views(layers, KV4Layer)
+    _rows16(dst, len(layers), layers, rows)
+    s = _on(stream, dst, layers[0].k)
+    _check(lib().glance_kv4_read_rows(ctypes.addressof(layers.c), len(layers), first, rows, dst.data_ptr(), s))
+
+
+def kv4_tree_attention_workspace_bytes(rows, n_q_heads, kvs):
+    kvs = _views(kvs, KV4Layer)
+    return lib().glance_kv4_tree_attention_workspace_bytes(len(kvs), rows, n_q_heads, ctypes.addressof(kvs.c))
+
+
+_DECODE = {}
+
+
+def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
+    """Tree attention over 4-bit caches: q, out [B][N+1][Hq][128] bf16 (B = 1:
+    [N+1][Hq][128] too), kvs B KV4Layer views, trees B Tree objects. trees
+    None: plain decoding, one row per request that sees the prefix and itself."""
+    kvs = _views(kvs, KV4Layer)
+    B = len(kvs)
+    rows = q.shape[-3]
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or not q.is_contiguous() or not out.is_contiguous() \
+            or q.shape != out.shape or q.shape[-1] != 128 or q.numel() != B * rows * q.shape[-2] * 128:
+        raise ValueError("glance: q and out must be contiguous bfloat16 [B, N + 1, n_q_heads, 128]")
+    if trees is None:
+        c = _DECODE.get(B)
+        if c is None:
+            c = _DECODE[B] = (TreeC * B)(*[TreeC(0, 1, 1) for _ in range(B)])
+        if rows != 1:
+            raise ValueError("glance: without trees q has one row per request")
+    else:
+        trees = _views(trees, Tree)
+        if len(trees) != B or trees[0].rows != rows:
+            raise ValueError("glance: need one tree of q's N + 1 rows per request")
+        c = trees.c
+    s = _on(stream, q, out, ws, kvs[0].k)
+    _check(lib().glance_kv4_tree_attention(q.data_ptr(), q.shape[-2], ctypes.addressof(kvs.c), ctypes.addressof(c), B,
+                                           scale, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s))
+
+
+def kv4_accept_commit_workspace_bytes(B, n_layers):
+    return lib().glance_kv4_accept_commit_workspace_bytes(B, n_layers)
+
+
+def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root, ws, gap=None, gate_threshold=0.0,
+                      gated=None, stream=None):
+    """Walk + commit on 4-bit caches: trees B Tree objects (or one), layers the
+    B * n_layers KV4Layer views (request-major), argmax [B][N+1], outputs [B],
+    [B][L], [B]. With gap [B][N+1] and gated [B]: the tie-aware gate."""
+    trees, layers = _views(trees, Tree), _views(layers, KV4Layer)
+    B = len(trees)
+    t = trees[0]
+    if len(layers) % B:
+        raise ValueError("glance: layers must hold the same number of views for every request")
+    ints = ((argmax, B * t.rows), (n_accepted, B), (accepted_tok, B * t.L), (new_root, B)) + (
+        ((gated, B),) if gated is not None else ())
+    for x, n in ints:
+        if x.dtype != torch.int32 or x.numel() < n or not x.is_contiguous():
+            raise ValueError("glance: argmax, n_accepted, accepted_tok, new_root and gated must be contiguous int32 "
+                             "[B, N + 1], [B], [B, L], [B], [B]")
+    tensors = [x for x, _ in ints] + [ws, layers[0].k]
+    if gap is not None:
+        if gap.dtype != torch.float32 or gap.numel() < B * t.rows or not gap.is_contiguous():
+            raise ValueError("glance: gap must be contiguous float32 [B, N + 1]")
+        tensors.append(gap)
+    s = _on(stream, *tensors)
+    _check(lib().glance_kv4_accept_commit(ctypes.addressof(trees.c), B, argmax.data_ptr(),
+                                          None if gap is None else gap.data_ptr(), gate_threshold,
+                                          ctypes.addressof(layers.c), len(layers) // B, n_accepted.data_ptr(),
+                                          accepted_tok.data_ptr(), new_root.data_ptr(),
+                                          None if gated is None else gated.data_ptr(), ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), s))
 
 
 def device_status():

@@ -4,7 +4,7 @@
 
 #include <mutex>
 
-#include "glance_internal.cuh"
+#include "kv4_internal.cuh"
 
 namespace glance {
 
@@ -105,12 +105,19 @@ const char* glance_status_string(glance_status s) {
   return "GLANCE_UNKNOWN_STATUS";
 }
 
+// The families of status words, in the order of glance_get_status, and the
+// units that report with one of them (the family's index).
+constexpr int kStatusUnits = 5;
+constexpr int kStatusExtra = 3;
+static const int kExtraFamily[kStatusExtra] = {1, 3, 4};  // attention, walk + commit, dense layers
+
 static glance_status read_all_status(int32_t* code_out, bool reset) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return glance::cuda_fail(e, "glance_device_status");
   int first = 0;
-  cudaError_t (*fns[5])(int*, bool) = {glance::status_build_tree, glance::status_attention,
-                                       glance::status_lmhead, glance::status_commit, glance::status_dense};
+  cudaError_t (*fns[kStatusUnits + kStatusExtra])(int*, bool) = {
+      glance::status_build_tree, glance::status_attention, glance::status_lmhead, glance::status_commit,
+      glance::status_dense, glance::status_kv4_attention, glance::status_kv4, glance::status_rope};
   for (auto fn : fns) {
     int v = 0;
     e = fn(&v, reset);
@@ -127,8 +134,17 @@ glance_status glance_device_status(int32_t* code_out) { return read_all_status(c
 
 namespace {
 
-// out[0] = the first non-zero of out[1..n] (0 if none)
-__global__ void first_status_kernel(int32_t* out, int n) {
+// The status words of the units that report with a family.
+struct ExtraWords {
+  const int32_t* word[kStatusExtra];
+  int family[kStatusExtra];
+};
+
+// out[1 + family] = the extra word where the family's own is 0; out[0] = the
+// first non-zero of out[1..n] (0 if none)
+__global__ void first_status_kernel(int32_t* out, int n, ExtraWords extra) {
+  for (int i = 0; i < kStatusExtra; ++i)
+    if (out[1 + extra.family[i]] == 0) out[1 + extra.family[i]] = *extra.word[i];
   int first = 0;
   for (int i = 1; i <= n; ++i) {
     const int v = out[i];
@@ -137,7 +153,15 @@ __global__ void first_status_kernel(int32_t* out, int n) {
   out[0] = first;
 }
 
-constexpr int kStatusUnits = 5;
+cudaError_t extra_words(void* (&addr)[kStatusExtra]) {
+  cudaError_t (*fns[kStatusExtra])(void**) = {glance::status_kv4_attention_addr, glance::status_kv4_addr,
+                                              glance::status_rope_addr};
+  for (int i = 0; i < kStatusExtra; ++i) {
+    const cudaError_t e = fns[i](&addr[i]);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace
 
@@ -151,8 +175,16 @@ glance_status glance_get_status(int32_t* status_out, void* stream) {
     cudaError_t e = fns[i](status_out + 1 + i, s);
     if (e != cudaSuccess) return glance::cuda_fail(e, "glance_get_status");
   }
-  first_status_kernel<<<1, 1, 0, s>>>(status_out, kStatusUnits);
-  cudaError_t e = cudaGetLastError();
+  void* addr[kStatusExtra];
+  cudaError_t e = extra_words(addr);
+  if (e != cudaSuccess) return glance::cuda_fail(e, "glance_get_status");
+  ExtraWords extra;
+  for (int i = 0; i < kStatusExtra; ++i) {
+    extra.word[i] = static_cast<const int32_t*>(addr[i]);
+    extra.family[i] = kExtraFamily[i];
+  }
+  first_status_kernel<<<1, 1, 0, s>>>(status_out, kStatusUnits, extra);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return glance::cuda_fail(e, "glance_get_status");
   return GLANCE_OK;
 }
@@ -168,6 +200,10 @@ glance_status glance_clear_status(void* stream) {
     if (e == cudaSuccess) e = cudaMemsetAsync(a, 0, sizeof(int), s);
     if (e != cudaSuccess) return glance::cuda_fail(e, "glance_clear_status");
   }
+  void* addr[kStatusExtra];
+  cudaError_t e = extra_words(addr);
+  for (int i = 0; e == cudaSuccess && i < kStatusExtra; ++i) e = cudaMemsetAsync(addr[i], 0, sizeof(int), s);
+  if (e != cudaSuccess) return glance::cuda_fail(e, "glance_clear_status");
   return GLANCE_OK;
 }
 

@@ -1,0 +1,90 @@
+// Shared by the kernels on 4-bit K/V caches (glance_kv4): the row format, host
+// checks of a view, and the conversions between codes, scales and values.
+//
+// A row (one slot of one kv head of K or V) is 128 codes of 4 bits in 64 bytes
+// and 8 e4m3 scales, one per 16 elements. A code has 2 significant bits and a
+// scale 4, so code * scale has at most 6 and lies in [2^-10, 2688] or is 0:
+// f16 (and bf16) hold it exactly. Only the fp32 global factor needs rounding.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "glance_internal.cuh"
+
+namespace glance {
+
+// status words of the units added after the first five families; each one is
+// reported with a family (api.cu)
+GLANCE_DECLARE_STATUS_WORD(status_kv4)
+GLANCE_DECLARE_STATUS_WORD(status_kv4_attention)
+GLANCE_DECLARE_STATUS_WORD(status_rope)
+
+constexpr int kKv4D = 128;           // head_dim
+constexpr int kKv4CodeBytes = 64;    // codes of one row
+constexpr int kKv4ScaleBytes = 8;    // scales of one row
+constexpr int kKv4MaxCap = 1 << 30;  // slots per head
+
+// Checks of one view, shared by the 4-bit calls.
+inline glance_status check_kv4(const char* who, const glance_kv4& x, int rows, int index) {
+  if (!x.k || !x.k_scale || !x.v || !x.v_scale || !x.t_len)
+    return fail(GLANCE_ERR_INVALID_ARG, "%s: null array in view %d", who, index);
+  if (x.head_dim != kKv4D)
+    return fail(GLANCE_ERR_UNSUPPORTED, "%s: 4-bit caches need head_dim 128 (view %d)", who, index);
+  if (x.n_kv_heads < 1 || x.n_kv_heads > 1024 || x.t_cap < rows || x.head_stride < x.t_cap || (x.head_stride & 1))
+    return fail(GLANCE_ERR_INVALID_ARG,
+                "%s: need 1 <= n_kv_heads <= 1024, t_cap >= rows and an even head_stride >= t_cap (view %d)", who, index);
+  if (x.t_cap > kKv4MaxCap) return fail(GLANCE_ERR_UNSUPPORTED, "%s: t_cap too large (view %d)", who, index);
+  if (!aligned16(x.k) || !aligned16(x.k_scale) || !aligned16(x.v) || !aligned16(x.v_scale))
+    return fail(GLANCE_ERR_INVALID_ARG, "%s: codes and scales must be 16-byte aligned (view %d)", who, index);
+  const float lo = 8.6736174e-19f, hi = 1.1529215e18f;  // 2^-60, 2^60
+  if (!(x.k_global >= lo && x.k_global <= hi) || !(x.v_global >= lo && x.v_global <= hi))
+    return fail(GLANCE_ERR_INVALID_ARG, "%s: k_global and v_global must be in [2^-60, 2^60] (view %d)", who, index);
+  return GLANCE_OK;
+}
+
+}  // namespace glance
+
+namespace glance_dev {
+
+// Eight codes (one word, element 0 in the lowest bits) as four pairs of f16,
+// elements (0, 1), (2, 3), (4, 5), (6, 7): the hardware conversion, exact.
+__device__ __forceinline__ void codes8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two e4m3 scales (the low 16 bits of w, the first in the lower byte) as f16, exact.
+__device__ __forceinline__ uint32_t scales2_to_f16(uint32_t w) {
+  uint32_t h;
+  asm("{\n .reg .b16 t, u;\n mov.b32 {t, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Two fp32 values as codes (nearest even, at most 6 in magnitude), `lo` in the low half of the byte.
+__device__ __forceinline__ uint32_t code2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n .reg .b8 t, z;\n mov.b16 {z, t}, 0;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n mov.b32 %0, {t, z, z, z};\n}\n"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+// An fp32 value >= 0 as an e4m3 scale (nearest even, at most 448).
+__device__ __forceinline__ uint32_t scale1(float s) {
+  uint32_t r;
+  asm("{\n .reg .b16 t, z;\n mov.b16 z, 0;\n cvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n mov.b32 %0, {t, z};\n}\n"
+      : "=r"(r)
+      : "f"(s), "f"(0.f));
+  return r;
+}
+
+}  // namespace glance_dev
