@@ -624,8 +624,8 @@ typedef struct {
  * round's tree rows before attention reads them).
  * src: device BF16 [n_layers][2][n_kv_heads][rows][128] (K before V),
  * contiguous, 32-byte aligned. Per group of 16 elements x, in fp32:
- * t = x / global; scale = max|t| / 6 rounded to e4m3 (nearest even, at most
- * 448); code = t / scale rounded to nearest even, at most 6 (0 where the scale
+ * t = x * (1 / global), the reciprocal rounded first; scale = max|t| / 6
+ * rounded to e4m3 (nearest even, at most 448); code = t / scale rounded to nearest even, at most 6 (0 where the scale
  * is 0). A group with a t that is not finite gets the scale 0x7F and codes 0.
  * Each row is quantised by itself, so a row reads the same whether it was
  * written alone, in a prompt or as a tree row.

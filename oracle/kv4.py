@@ -4,8 +4,8 @@ A row is 128 codes of 4 bits (sign, two exponent bits, one fraction bit) and
 one e4m3 scale per 16 elements; an element stands for code * scale * global.
 Written from that definition: the grids of the two small formats are listed
 and a value goes to the nearest member, the one with an even bit pattern
-between two. Only the two quotients t = x / global and max|t| / 6 are taken in
-fp32, as the definition has them.
+between two. Only t = x * (1 / global) and max|t| / 6 are taken in fp32, as the
+definition has them.
 """
 import numpy as np
 
@@ -31,7 +31,7 @@ def quantise(x, g):
     """Rows x [..., 128] (float32 values) -> codes uint8 [..., 128], scale bits uint8 [..., 8]."""
     x = np.asarray(x, dtype=np.float32)
     with np.errstate(over="ignore", invalid="ignore"):
-        t = (x / np.float32(g)).astype(np.float32).reshape(*x.shape[:-1], -1, 16)
+        t = (x * (np.float32(1) / np.float32(g))).astype(np.float32).reshape(*x.shape[:-1], -1, 16)
     finite = np.isfinite(t).all(-1)
     t = np.where(finite[..., None], t, np.float32(0))
     s6 = (np.abs(t).max(-1) / np.float32(6)).astype(np.float32)

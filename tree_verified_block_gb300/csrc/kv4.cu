@@ -33,7 +33,6 @@ struct RowsParams {
   long long head_stride;         // slots
   int n_kv_heads, rows, t_cap;
   float global[2], inv_global[2];  // K, V; 1 / global rounded
-  int exact_inv[2];              // global is a power of two: x * inv_global is the quotient
 };
 
 // 32 bytes in one load / store.
@@ -48,18 +47,21 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
                : "memory");
 }
 
-// x / d rounded to nearest, from inv = 1 / d rounded: the product is off by
-// at most two units in the last place, and one step with the exact remainder
-// (a fused multiply-add) leaves an error of 2^-46 of the quotient before the
-// final rounding.
+// x / s rounded to nearest for a scale s of 4 significant bits, from inv =
+// 1 / s rounded: the product is off by at most two units in the last place, and
+// one step with the exact remainder (a fused multiply-add) leaves an error of
+// 2^-46 of the quotient before the final rounding. That rounding is the
+// quotient's: with s = m 2^e, m <= 15, the quotient is a multiple of 1 / m of a
+// unit, so no midpoint of two fp32 numbers is nearer than 1 / 30 of one. A tie
+// between two codes is exact this way and goes to the even one.
 __device__ __forceinline__ float quotient(float x, float d, float inv) {
   const float q = x * inv;
   return fmaf(fmaf(-q, d, x), inv, q);
 }
 
 // One group of 16 bf16 values (8 words) to 16 codes (2 words) and a scale.
-__device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float g, float inv_g, bool exact_inv,
-                                           uint32_t (&codes)[2], uint32_t& scale) {
+__device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float inv_g, uint32_t (&codes)[2],
+                                           uint32_t& scale) {
   float t[16];
   float amax = 0.f;
   bool finite = true;
@@ -70,7 +72,7 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float g, floa
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    t[i] = exact_inv ? t[i] * inv_g : quotient(t[i], g, inv_g);
+    t[i] *= inv_g;
     amax = fmaxf(amax, fabsf(t[i]));  // drops NaN
     finite = finite && fabsf(t[i]) < INFINITY;
   }
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_rows_kernel(const __gri
     const int row = row0 + u * kRowsPerPass;
     if (row >= p.rows || !GLANCE_IN_BOUNDS(T + row, p.t_cap)) continue;
     uint32_t codes[2], scale;
-    quantise16(x[u], p.global[is_v], p.inv_global[is_v], p.exact_inv[is_v] != 0, codes, scale);
+    quantise16(x[u], p.inv_global[is_v], codes, scale);
     const long long slot = slot0 + row;
     *reinterpret_cast<uint2*>(p.cache[lkv].codes + slot * glance::kKv4CodeBytes + grp * 8) = make_uint2(codes[0], codes[1]);
     p.cache[lkv].scales[slot * glance::kKv4ScaleBytes + grp] = static_cast<unsigned char>(scale);
@@ -173,10 +175,8 @@ glance_status launch_rows(const char* who, bool write, void* rows16, const glanc
   p.t_cap = l0.t_cap;
   const float gl[2] = {l0.k_global, l0.v_global};
   for (int i = 0; i < 2; ++i) {
-    int e;
     p.global[i] = gl[i];
     p.inv_global[i] = 1.f / gl[i];
-    p.exact_inv[i] = frexpf(gl[i], &e) == 0.5f;
   }
   for (int l = 0; l < n_layers; ++l) {
     p.cache[2 * l] = {static_cast<unsigned char*>(layers[l].k), static_cast<unsigned char*>(layers[l].k_scale)};
