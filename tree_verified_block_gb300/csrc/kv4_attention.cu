@@ -34,81 +34,9 @@ struct Params {
   float2* part_ml;  // its rows' (maximum in log2, sum of weights)
   uint32_t* count;  // [B][Hkv] blocks of a head that are done
   int B, rows, Hq, Hkv, G, W;
+  int n_qt;         // query tiles of 128 rows per kv head
   float scale_log2;
 };
-
-// One block per (request, row, head), one thread per output dim; keys one
-// block of 128 at a time.
-__global__ void __launch_bounds__(kD) kv4_attention_plain_kernel(const __grid_constant__ Params p) {
-  __shared__ float s_q[kD], s_p[kD], s_red[4];
-  pdl_wait_prior();
-  const int h = blockIdx.x % p.Hq, i = blockIdx.x / p.Hq % p.rows, r = blockIdx.x / p.Hq / p.rows;
-  const Request& rq = p.req[r];
-  const int t = threadIdx.x, T = *rq.t_len;
-  if (T < 0 || T > rq.t_cap - p.rows) {
-    if (i == 0 && h == 0 && t == 0) report(GLANCE_DEV_TREE_CAPACITY);
-    return;
-  }
-  const size_t qi = ((static_cast<size_t>(r) * p.rows + i) * p.Hq + h) * kD + t;
-  s_q[t] = __bfloat162float(p.q[qi]) * rq.k_global;
-  __syncthreads();
-  const long long head0 = static_cast<long long>(h / p.G) * rq.head_stride;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int c0 = 0; c0 < T + p.rows; c0 += kD) {
-    const int slot = c0 + t;
-    const int kr = slot - T;  // tree row
-    bool see = slot < T;
-    if (!see && kr < p.rows) see = rq.anc ? (rq.anc[i * p.W + (kr >> 6)] >> (kr & 63)) & 1 : kr == i;
-    float s = -INFINITY;
-    if (see && GLANCE_IN_BOUNDS(slot, rq.t_cap)) {
-      const unsigned char* kc = rq.k + (head0 + slot) * 64;
-      const unsigned char* ks = rq.k_scale + (head0 + slot) * 8;
-      float dot = 0.f;
-      for (int g = 0; g < 8; ++g) {
-        const float sc = f16x2_to_f32(scales2_to_f16(ks[g])).x;
-        float d = 0.f;
-        for (int w = 0; w < 2; ++w) {
-          uint32_t f[4];
-          codes8_to_f16(reinterpret_cast<const uint32_t*>(kc)[2 * g + w], f);
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = f16x2_to_f32(f[e]);
-            d = fmaf(s_q[16 * g + 8 * w + 2 * e], x.x, d);
-            d = fmaf(s_q[16 * g + 8 * w + 2 * e + 1], x.y, d);
-          }
-        }
-        dot = fmaf(d, sc, dot);
-      }
-      s = dot * p.scale_log2;
-    }
-    float cm = s;
-    for (int o = 16; o; o >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, o));
-    if ((t & 31) == 0) s_red[t >> 5] = cm;
-    __syncthreads();
-    cm = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    const float mn = fmaxf(m, cm);
-    const float mu = mn == -INFINITY ? 0.f : mn;
-    s_p[t] = see ? exp2f(s - mu) : 0.f;
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - mu);
-    m = mn;
-    l *= alpha;
-    acc *= alpha;
-    __syncthreads();
-    const int n = min(kD, T + p.rows - c0);
-    for (int j = 0; j < n; ++j) {
-      const float w = s_p[j];
-      if (w == 0.f) continue;
-      l += w;
-      const long long at = head0 + c0 + j;
-      const uint32_t b = rq.v[at * 64 + (t >> 1)] >> (4 * (t & 1)) & 15u;
-      uint32_t f[4];
-      codes8_to_f16(b, f);
-      acc = fmaf(w, f16x2_to_f32(f[0]).x * f16x2_to_f32(scales2_to_f16(rq.v_scale[at * 8 + (t >> 4)])).x, acc);
-    }
-    __syncthreads();
-  }
-  p.out[qi] = __float2bfloat16(l == 0.f ? 0.f : acc * rq.v_global / l);
-}
-
 
 // ------------------------------------------------- few query rows per kv head
 //
@@ -580,13 +508,751 @@ int few_grid(int B, int Hkv) {
 }
 size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv * 4 + 255) / 256 * 256; }
 
+// ------------------------------------------------ many query rows per kv head
+//
+// More than 16 query rows share a kv head: the products are worth the tensor
+// core's 128-row tiles. A block works on tiles of 128 query rows (head, packed
+// row) x 128 slots:
+//
+//   warps 12..15  codes and scales from global memory (one tile ahead in
+//                 registers) -> f16 K and V tiles in shared memory, in the
+//                 128-byte-swizzled layout of the tensor core, three stages
+//   warp 0        S = Q K^T into one of two tensor-memory buffers (the next
+//                 tile's before this tile's weights are ready), then O += P V
+//                 with P from tensor memory
+//   warps 4..11   softmax, two threads per row (64 slots each): mask, running
+//                 maximum, weights as f16 pairs to tensor memory; Q goes to
+//                 tensor memory once per segment, as f16 scaled per row
+//
+// Work: the slots of every (request, kv head, query tile) in units of 32. Where
+// each such group can be cut into equal parts that fill the grid, a block has
+// one part; else the list of all units is cut into equal runs and a block's
+// run may cross groups (a "segment" is its part in one group). The lengths are
+// read on the device. A group that one block has whole is written out there;
+// the others' parts are merged by a second kernel.
+
+constexpr int kWideThreads = 512;
+constexpr int kBM = 128, kBN = 128;
+constexpr int kWideStages = 3;
+constexpr uint32_t kHalfBytes = kBN * 128;     // 64 dims x 128 slots, f16
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // a K or V tile
+constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kWideRing = kWideStages * kStageBytes;
+constexpr uint32_t kWideMisc = 1024;
+constexpr uint32_t kWideSmem = 1024 + kWideRing + kWideMisc;
+constexpr int kMinUnits = 4;  // one tile
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+struct WidePlan {
+  int units[kMaxB];       // of one group of request r; 0: no room, no output
+  long long base[kMaxB];  // units of all groups before request r
+  long long total;
+  int tau;                // > 0: every group is cut into parts of tau units
+  int blocks0[kMaxB];     // tau > 0: blocks before request r's
+  int first_req;          // first request with units
+};
+
+struct WideMisc {
+  uint64_t k_full[kWideStages], v_full[kWideStages], kv_empty[kWideStages];
+  uint64_t q_ready, s_full[2], p_ready, o_done, drain;
+  uint32_t bad[kWideStages][4];  // slots of a tile whose V scales hold a NaN (tiles with tree slots)
+  uint32_t tmem;
+  int abort_flag;
+  WidePlan plan;
+};
+static_assert(sizeof(WideMisc) <= kWideMisc, "misc block");
+
+// The plan, by one warp; every block and the merge come to the same one.
+__device__ __forceinline__ void wide_plan(const Params& p, WidePlan* pl, int lane, int blocks) {
+  int units = 0;
+  if (lane < p.B) {
+    const int T = *p.req[lane].t_len;
+    if (T >= 0 && T <= p.req[lane].t_cap - p.rows) units = (T + p.rows + kUnit - 1) / kUnit;
+  }
+  const int gpr = p.Hkv * p.n_qt;
+  long long end = static_cast<long long>(units) * gpr;
+#pragma unroll
+  for (int o = 1; o < kMaxB; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, end, kMaxB - 1);
+  const int active = __popc(__ballot_sync(0xffffffffu, units > 0));
+  const int per_group = blocks / gpr;
+  int tau = 0;
+  if (per_group >= active && active > 0) {
+    int lo = kMinUnits, hi = max(kMinUnits, __reduce_max_sync(0xffffffffu, units));
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_group)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    // a run that crosses groups pays about kCrossUnits for each crossing
+    constexpr int kCrossUnits = 10;
+    if (lo <= total / blocks + kCrossUnits) tau = lo;
+  }
+  const int n = tau ? (units + tau - 1) / tau * gpr : 0;
+  int nb = n;
+#pragma unroll
+  for (int o = 1; o < kMaxB; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, nb, o);
+    if (lane >= o) nb += v;
+  }
+  if (lane < kMaxB) {
+    pl->units[lane] = units;
+    pl->base[lane] = end - static_cast<long long>(units) * gpr;
+    pl->blocks0[lane] = nb - n;
+  }
+  if (lane == 0) {
+    pl->total = total;
+    pl->tau = tau;
+  }
+}
+
+// First unit of block b's run (runs that may cross groups).
+__device__ __forceinline__ long long run_start(long long total, int b, int blocks) {
+  return total / blocks * b + total % blocks * b / blocks;
+}
+
+// A block's part in one group: units [a, a + n) of group g of request r.
+struct Segment {
+  int r, g, a, n;
+  int left;   // units of the run after this segment
+  int index;  // of the block's segments
+};
+
+__device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& pl, int b, int blocks, Segment& s) {
+  const int gpr = p.Hkv * p.n_qt;
+  s.index = 0;
+  int r = 0;
+  if (pl.tau) {
+    int n = 0, at = 0;
+    for (; r < p.B; ++r) {
+      n = (pl.units[r] + pl.tau - 1) / pl.tau;
+      at = b - pl.blocks0[r];
+      if (at < n * gpr) break;
+    }
+    if (r == p.B) return false;
+    s.r = r;
+    s.g = at / n;
+    s.a = at % n * pl.tau;
+    s.n = min(pl.tau, pl.units[r] - s.a);
+    s.left = 0;
+    return true;
+  }
+  const long long x = run_start(pl.total, b, blocks);
+  const int len = static_cast<int>(run_start(pl.total, b + 1, blocks) - x);
+  if (len == 0) return false;
+  while (r + 1 < p.B && x >= pl.base[r + 1]) ++r;  // requests without units share their base with the next
+  while (pl.units[r] == 0) --r;  // x lies before the end of the last request with units
+  const long long in = x - pl.base[r];
+  s.r = r;
+  s.g = static_cast<int>(in / pl.units[r]);
+  s.a = static_cast<int>(in % pl.units[r]);
+  s.n = min(len, pl.units[r] - s.a);
+  s.left = len - s.n;
+  return true;
+}
+__device__ __forceinline__ bool next_segment(const Params& p, const WidePlan& pl, Segment& s) {
+  if (s.left == 0) return false;
+  if (++s.g == p.Hkv * p.n_qt) {
+    s.g = 0;
+    do ++s.r;
+    while (pl.units[s.r] == 0);
+  }
+  s.a = 0;
+  s.n = min(s.left, pl.units[s.r]);
+  s.left -= s.n;
+  ++s.index;
+  return true;
+}
+
+// Slots of a segment: [k0, k1); its tiles start at k0, k0 + 128, ...
+struct Run {
+  int k0, k1, tiles;
+  __device__ __forceinline__ Run(const Segment& s, int n_keys) {
+    k0 = s.a * kUnit;
+    k1 = min(k0 + s.n * kUnit, n_keys);
+    tiles = (k1 - k0 + kBN - 1) / kBN;
+  }
+  __device__ __forceinline__ int key0(int j) const { return k0 + j * kBN; }
+  // columns of tile j that its products compute, a multiple of 32
+  __device__ __forceinline__ int cols(int j) const { return min(kBN, (k1 - key0(j) + 31) & ~31); }
+};
+
+__device__ __forceinline__ void wide_fail(WideMisc* ms) {
+  report(GLANCE_DEV_PIPELINE_TIMEOUT);
+  atomicExch(&ms->abort_flag, 1);
+}
+// Bounded wait that also gives up once another role has.
+__device__ __forceinline__ bool wide_wait(uint64_t* bar, uint32_t parity, WideMisc* ms) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) return false;
+      if (globaltimer_ns() - t0 > kWaitNs) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long pair_f2(float lo, float hi) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void split_f2(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma_f2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add_f2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// kind::f16 with f16 A and B, fp32 accumulator, 128 rows, N columns; B is
+// K-major (K tile) or MN-major (V tile).
+__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(kBM >> 4) << 24);
+}
+
+// Slots kb .. kb + 31 (tree index = slot - T) that row `prow` sees.
+__device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W, int rows, int kb) {
+  if (kb <= -32) return 0xFFFFFFFFu;
+  const uint32_t prefix = kb < 0 ? (1u << -kb) - 1u : 0u;
+  uint32_t tree;
+  if (kb < 0) {
+    tree = static_cast<uint32_t>(rq.anc[static_cast<size_t>(prow) * W] << -kb);
+  } else {
+    const int w = kb >> 6, o = kb & 63;
+    const uint64_t lo = w < W ? rq.anc[static_cast<size_t>(prow) * W + w] : 0ull;
+    const uint64_t hi = o && w + 1 < W ? rq.anc[static_cast<size_t>(prow) * W + w + 1] : 0ull;
+    tree = static_cast<uint32_t>(o ? (lo >> o) | (hi << (64 - o)) : lo);
+  }
+  const int lim = rows - kb;  // bits from lim on are past the last row
+  return prefix | (tree & (lim >= 32 ? 0xFFFFFFFFu : lim <= 0 ? 0u : (1u << lim) - 1u));
+}
+
+// Four rows' pieces of 32 dims (16 bytes of codes, two scales) of one tile.
+struct Raw {
+  uint4 codes[4];
+  uint32_t scales[4];
+};
+
+// Rows of the tile at key0: the thread's are warp * 32 + 8i + (lane & 7), dims
+// 32 (lane >> 3) ..: a warp's load is 8 whole rows. Rows from k1 on are zero.
+__device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, const unsigned char* scales, long long head0,
+                                         int key0, int k1, int row, int q, int t_cap) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int slot = key0 + row + 8 * i;
+    x.codes[i] = make_uint4(0, 0, 0, 0);
+    x.scales[i] = 0;
+    if (slot < k1 && GLANCE_IN_BOUNDS(slot, t_cap)) {
+      x.codes[i] = __ldg(reinterpret_cast<const uint4*>(codes + (head0 + slot) * 64) + q);
+      x.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + (head0 + slot) * 8) + q);
+    }
+  }
+}
+
+// ... as f16 into the tile: row r's 16-byte chunk c of a half is at
+// r * 128 + 16 (c ^ (r & 7)); the eight lanes of a store phase have eight rows.
+__device__ __forceinline__ void store_tile(const Raw& x, unsigned char* tile, int row, int q) {
+  unsigned char* base = tile + (q >> 1) * kHalfBytes + row * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t s = scales2_to_f16(x.scales[i]);
+    const uint32_t s0 = prmt(s, s, 0x1010), s1 = prmt(s, s, 0x3232);
+    const uint32_t w[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h[4];
+      codes8_to_f16(w[j], h);
+      const uint32_t sj = j < 2 ? s0 : s1;
+      const int chunk = ((q & 1) * 4 + j) ^ (row & 7);
+      *reinterpret_cast<uint4*>(base + i * 8 * 128 + chunk * 16) =
+          make_uint4(mul_f16x2(h[0], sj), mul_f16x2(h[1], sj), mul_f16x2(h[2], sj), mul_f16x2(h[3], sj));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  WideMisc* ms = reinterpret_cast<WideMisc*>(ring + kWideRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWideStages; ++s) {
+      mbar_init(&ms->k_full[s], 4);
+      mbar_init(&ms->v_full[s], 4);
+      mbar_init(&ms->kv_empty[s], 1);
+    }
+    mbar_init(&ms->q_ready, 256);
+    mbar_init(&ms->s_full[0], 1);
+    mbar_init(&ms->s_full[1], 1);
+    mbar_init(&ms->p_ready, 256);
+    mbar_init(&ms->o_done, 1);
+    mbar_init(&ms->drain, 1);
+    ms->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ms->tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait_prior();
+  pdl_launch_dependents();
+  if (warp == 2) wide_plan(p, &ms->plan, lane, blocks);
+  if (blockIdx.x == 0 && threadIdx.x < p.B) {
+    const int T = *p.req[threadIdx.x].t_len;
+    if (T < 0 || T > p.req[threadIdx.x].t_cap - p.rows) report(GLANCE_DEV_TREE_CAPACITY);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  const uint32_t tS = tmem, tO = tmem + 256, tP = tmem + 384, tQ = tmem + 448;
+  const WidePlan& pl = ms->plan;
+  Segment sg;
+  const bool any = first_segment(p, pl, blockIdx.x, blocks, sg);
+
+  if (warp == 0 && any) {
+    // --------------------------------------------------------------- products
+    if (lane == 0) {
+      int i = 0;  // tiles of the block so far
+      bool good = true;
+      Segment s = sg;
+      do {
+        const Run run(s, *p.req[s.r].t_len + p.rows);
+        const auto issue_s = [&](int j) {
+          const int t = i + j, st = t % kWideStages;
+          if (!wide_wait(&ms->k_full[st], (t / kWideStages) & 1, ms)) return false;
+          tc_fence_after();
+          const uint32_t k_addr = smem_u32(ring + st * kStageBytes);
+          const uint32_t idesc = idesc_f16(run.cols(j), false);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tS + (t & 1) * 128, tQ + kk * 8,
+                        sdesc_sw128(k_addr + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+          mma_commit(&ms->s_full[t & 1]);
+          return true;
+        };
+        good = wide_wait(&ms->q_ready, s.index & 1, ms);
+        if (good) {
+          tc_fence_after();
+          good = issue_s(0);
+        }
+        for (int j = 0; good && j < run.tiles; ++j) {
+          if (j + 1 < run.tiles && !issue_s(j + 1)) {
+            good = false;
+            break;
+          }
+          const int t = i + j, st = t % kWideStages;
+          if (!wide_wait(&ms->p_ready, t & 1, ms) || !wide_wait(&ms->v_full[st], (t / kWideStages) & 1, ms)) {
+            good = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t v_addr = smem_u32(ring + st * kStageBytes + kTileBytes);
+          const int steps = run.cols(j) / 16;
+          for (int kk = 0; kk < steps; ++kk)
+            mma_bf16_ts(tO, tP + kk * 8, sdesc_sw128(v_addr + kk * 2048, kHalfBytes, 1024), idesc_f16(kD, true),
+                        (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&ms->o_done);
+          mma_commit(&ms->kv_empty[st]);
+        }
+        i += run.tiles;
+      } while (good && next_segment(p, pl, s));
+      if (!good) wide_fail(ms);
+    }
+  } else if (warp >= 12 && any) {
+    // ----------------------------------------------------- codes to f16 tiles
+    const int row = (warp - 12) * 32 + (lane & 7), q = lane >> 3;
+    Segment s = sg;
+    int T = *p.req[s.r].t_len;
+    Run run(s, T + p.rows);
+    int j = 0, t = 0;
+    bool more = true, good = true;
+    Raw k, v;
+    const auto load = [&](bool of_v, Raw& x) {
+      const Request& rq = p.req[s.r];
+      load_raw(x, of_v ? rq.v : rq.k, of_v ? rq.v_scale : rq.k_scale, static_cast<long long>(s.g / p.n_qt) * rq.head_stride,
+               run.key0(j), run.k1, row, q, rq.t_cap);
+    };
+    load(false, k);
+    load(true, v);
+    while (more) {
+      const int st = t % kWideStages;
+      const bool tree = run.key0(j) + kBN > T;
+      if (t >= kWideStages) good = wide_wait(&ms->kv_empty[st], (t / kWideStages - 1) & 1, ms);
+      if (!__all_sync(0xffffffffu, good)) {
+        wide_fail(ms);
+        break;
+      }
+      unsigned char* tile = ring + st * kStageBytes;
+      if (tree) {
+        // a V row with a scale that is not a number is left out (0 * NaN would
+        // reach the rows that do not see it); its slot is marked instead
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool nan = (v.scales[i] & 0x7Fu) == 0x7Fu || (v.scales[i] & 0x7F00u) == 0x7F00u;
+          uint32_t b = __ballot_sync(0xffffffffu, nan);
+          b |= b >> 16;
+          b = (b | b >> 8) & 0xFFu;  // rows 8i .. 8i + 7
+          word |= b << (8 * i);
+          if (b >> (lane & 7) & 1u) {
+            v.codes[i] = make_uint4(0, 0, 0, 0);
+            v.scales[i] = 0;
+          }
+        }
+        if (lane == 0) ms->bad[st][warp - 12] = word;
+      }
+      store_tile(k, tile, row, q);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->k_full[st]);
+      // the next tile of this segment, or the first of the next one
+      Segment s2 = s;
+      if (++j == run.tiles) {
+        j = 0;
+        more = next_segment(p, pl, s2);
+      }
+      const Raw v_now = v;
+      if (more) {
+        if (j == 0) {
+          s = s2;
+          T = *p.req[s.r].t_len;
+          run = Run(s, T + p.rows);
+        }
+        load(false, k);
+        load(true, v);
+      }
+      store_tile(v_now, tile + kTileBytes, row, q);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->v_full[st]);
+      ++t;
+    }
+  } else if (warp >= 4 && warp < 12 && any) {
+    // ---------------------------------------------------------------- softmax
+    // Warp (quarter, sub) has rows 32 quarter + 16 sub + (lane & 15); lanes
+    // 0-15 slots / dims 0-63 of a tile, lanes 16-31 the other 64.
+    const int half = lane >> 4, quarter = warp & 3, sub = (warp - 4) >> 2;
+    const int lrow = quarter * 32 + sub * 16 + (lane & 15);
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32 + sub * 16) << 16;
+    const int R = p.G * p.rows;
+    bool ok = true;
+    int i = 0;
+    Segment s = sg;
+    do {
+      const Request& rq = p.req[s.r];
+      const int T = *rq.t_len, n_keys = T + p.rows;
+      const Run run(s, n_keys);
+      const int head = s.g / p.n_qt, qt = s.g % p.n_qt;
+      const int qrow = qt * kBM + lrow;
+      const bool valid = qrow < R;
+      const int prow = valid ? qrow % p.rows : 0;
+      const size_t q_at = ((static_cast<size_t>(s.r) * p.rows + prow) * p.Hq + head * p.G + (valid ? qrow / p.rows : 0)) * kD;
+      // Q row, this half's 64 dims, to tensor memory (the products that read
+      // the previous segment's have finished: their weights were written)
+      float sc;
+      {
+        uint4 x[8];
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at + 64 * half);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = valid ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+        uint32_t top = 0;  // the largest magnitude's bits: order of the absolute values
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
+        const float qf = query_factor(amax);
+        sc = score_factor(amax, qf, p.scale_log2, rq.k_global);
+        uint32_t h[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * qf, __uint_as_float(w[e] & 0xFFFF0000u) * qf);
+        tmem_st16x2<32>(tQ + lane_off, *reinterpret_cast<const uint32_t(*)[16]>(h));
+        tmem_st16x2<32>(tQ + lane_off + 16, *reinterpret_cast<const uint32_t(*)[16]>(h + 16));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&ms->q_ready);
+      }
+      float m = -INFINITY, lsum = 0.f;
+      for (int j = 0; j < run.tiles; ++j) {
+        const int t = i + j, key0 = run.key0(j);
+        const bool got_s = __all_sync(0xffffffffu, wide_wait(&ms->s_full[t & 1], (t >> 1) & 1, ms));
+        if (!got_s) {
+          wide_fail(ms);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[64];
+        tmem_ld32x2<64>(tS + (t & 1) * 128 + lane_off, *reinterpret_cast<uint32_t(*)[32]>(sr));
+        tmem_ld32x2<64>(tS + (t & 1) * 128 + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
+        tmem_ld_wait();
+        if (key0 + kBN > T || key0 + kBN > run.k1) {
+          uint32_t bad[2] = {0u, 0u};
+          if (key0 + kBN > T) {
+            // the marks were written before the K tile was handed over
+            if (!wide_wait(&ms->k_full[t % kWideStages], (t / kWideStages) & 1, ms)) wide_fail(ms);
+            bad[0] = ms->bad[t % kWideStages][2 * half];
+            bad[1] = ms->bad[t % kWideStages][2 * half + 1];
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int s0 = key0 + 64 * half + 32 * c;
+            uint32_t vis = valid ? visible32(rq, prow, p.W, p.rows, s0 - T) : 0u;
+            const int lim = run.k1 - s0;
+            if (lim < 32) vis &= lim <= 0 ? 0u : (1u << lim) - 1u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              sr[32 * c + e] = !(vis >> e & 1u) ? 0xFF800000u : (bad[c] >> e & 1u) ? 0x7FC00000u : sr[32 * c + e];
+          }
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+          mx0 = max3f(mx0, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+          mx1 = max3f(mx1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
+          mx2 = max3f(mx2, __uint_as_float(sr[e + 4]), __uint_as_float(sr[e + 5]));
+          mx3 = max3f(mx3, __uint_as_float(sr[e + 6]), __uint_as_float(sr[e + 7]));
+        }
+        float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sc;
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+        // the running maximum moves when some row of the warp grew by 8 (log2):
+        // a stale one keeps the weights below 2^8 and cancels between O and l
+        const bool grow = __any_sync(0xffffffffu, mt > m + 8.f);
+        const float m_new = grow ? fmaxf(m, mt) : m;
+        const float off = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - off);
+        uint32_t pk[32];
+        const unsigned long long sc2 = pair_f2(sc, sc), no2 = pair_f2(-off, -off);
+        unsigned long long l2 = pair_f2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float t0, t1;
+          split_f2(fma_f2(pair_f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, no2), t0, t1);
+          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+          l2 = add_f2(l2, pair_f2(p0, p1));
+          pk[e] = pack_f16x2(p0, p1);
+        }
+        float l0, l1;
+        split_f2(l2, l0, l1);
+        if (j > 0) {  // the product before this one has read P and written O
+          const bool got_o = __all_sync(0xffffffffu, wide_wait(&ms->o_done, (t - 1) & 1, ms));
+          if (!got_o) {
+            wide_fail(ms);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        tmem_st16x2<32>(tP + lane_off, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+        tmem_st16x2<32>(tP + lane_off + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            const uint32_t ta = tO + lane_off + 32 * c;
+            tmem_ld32x2<64>(ta, r);
+            tmem_ld_wait();
+            uint32_t x[16], y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              x[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              y[e] = __float_as_uint(__uint_as_float(r[16 + e]) * alpha);
+            }
+            tmem_st16x2<64>(ta, x);
+            tmem_st16x2<64>(ta + 16, y);
+          }
+        }
+        tmem_st_wait();
+        lsum = lsum * alpha + (l0 + l1);
+        m = m_new;
+        tc_fence_before();
+        mbar_arrive(&ms->p_ready);
+      }
+      if (ok) {
+        ok = __all_sync(0xffffffffu, wide_wait(&ms->o_done, (i + run.tiles - 1) & 1, ms));
+        if (!ok) wide_fail(ms);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      i += run.tiles;
+      float l = lsum + __shfl_xor_sync(0xffffffffu, lsum, 16);
+      const bool whole = s.n == pl.units[s.r];
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : rq.v_global / l;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld32x2<64>(tO + lane_off + 32 * c, r);
+          tmem_ld_wait();
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + q_at + 64 * half + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                w[f] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * f]) * inv, __uint_as_float(r[8 * e + 2 * f + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      } else {
+        // two slots per block: its first segment's and its last one's; [slot][dim quad][row]
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.index ? 1 : 0);
+        float4* po = p.part_o + slot * 32 * kBM + lrow;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld32x2<64>(tO + lane_off + 32 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            po[(16 * half + 8 * c + e) * kBM] =
+                make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                            __uint_as_float(r[4 * e + 3]));
+        }
+        if (half == 0) p.part_ml[slot * kBM + lrow] = make_float2(l != l ? 0.f : m, l);  // a NaN row stays one
+      }
+      tc_fence_before();  // O and Q are free for the next segment's products
+    } while (next_segment(p, pl, s));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(&ms->abort_flag) && any) {
+    // after a failed wait products may still be running
+    if (warp == 0 && lane == 0) {
+      mma_commit(&ms->drain);
+      (void)mbar_wait(&ms->drain, 0, 50000000ull);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The parts of the groups that several blocks had. Block (group, 4 rows):
+// thread = (slice of the parts, dim quad, row). The plan needs T only, which
+// nothing writes while this or the kernel before it runs.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 4;
+
+__global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(const __grid_constant__ Params p, int blocks) {
+  __shared__ WidePlan pl;
+  __shared__ float4 s_o[128];
+  __shared__ float2 s_ml[128];
+  if (threadIdx.x < 32) wide_plan(p, &pl, threadIdx.x, blocks);
+  __syncthreads();
+  const int gpr = p.Hkv * p.n_qt;
+  const int grp = blockIdx.x / (kBM / kMergeRows), rows0 = blockIdx.x % (kBM / kMergeRows) * kMergeRows;
+  const int r = grp / gpr, g = grp % gpr, units = pl.units[r];
+  const int qrow0 = g % p.n_qt * kBM + rows0;
+  pdl_wait_prior();  // in every block: this kernel ends after the one before it
+  pdl_launch_dependents();
+  if (units == 0 || qrow0 >= p.G * p.rows) return;
+  int first, n;           // the blocks that have a part of this group
+  bool late = false;      // the first of them has it as its last segment
+  if (pl.tau) {
+    n = (units + pl.tau - 1) / pl.tau;
+    first = pl.blocks0[r] + g * n;
+  } else {
+    const long long x0 = pl.base[r] + static_cast<long long>(g) * units, x1 = x0 + units;
+    first = static_cast<int>(x0 * blocks / pl.total);
+    while (run_start(pl.total, first + 1, blocks) <= x0) ++first;
+    while (run_start(pl.total, first, blocks) > x0) --first;
+    late = run_start(pl.total, first, blocks) < x0;
+    n = 1;
+    while (run_start(pl.total, first + n, blocks) < x1) ++n;
+  }
+  if (n == 1) return;  // written whole
+  const int row = threadIdx.x & (kMergeRows - 1), quad = threadIdx.x >> 2 & 31, slice = threadIdx.x >> 7;
+  const int lrow = rows0 + row;
+  const int per = (n + 1) / 2, b0 = slice * per, b1 = min(n, b0 + per);
+  const auto slot_of = [&](int b) { return 2 * static_cast<size_t>(first + b) + (b == 0 && late ? 1 : 0); };
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = b0; s0 < b1; s0 += 8) {
+    float4 v[8];
+    float2 ml[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = s0 + e < b1;
+      const size_t slot = slot_of(in ? s0 + e : b0);
+      ml[e] = in ? __ldcg(p.part_ml + slot * kBM + lrow) : make_float2(-INFINITY, 0.f);
+      v[e] = in ? __ldcg(p.part_o + (slot * 32 + quad) * kBM + lrow) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mx = M;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, ml[e].x);
+    const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+    M = mx;
+    L *= keep;
+    a.x *= keep;
+    a.y *= keep;
+    a.z *= keep;
+    a.w *= keep;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - mx);
+      L = fmaf(f, ml[e].y, L);
+      a.x = fmaf(f, v[e].x, a.x);
+      a.y = fmaf(f, v[e].y, a.y);
+      a.z = fmaf(f, v[e].z, a.z);
+      a.w = fmaf(f, v[e].w, a.w);
+    }
+  }
+  if (slice == 1) {
+    s_o[threadIdx.x - 128] = a;
+    s_ml[threadIdx.x - 128] = make_float2(M, L);
+  }
+  __syncthreads();
+  if (slice == 1) return;
+  const float4 b = s_o[threadIdx.x];
+  const float2 ml = s_ml[threadIdx.x];
+  const float mx = fmaxf(M, ml.x);
+  const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - mx), f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+  L = f0 * L + f1 * ml.y;
+  const float inv = L == 0.f ? 0.f : p.req[r].v_global / L;
+  const int qrow = qrow0 + row;
+  if (qrow >= p.G * p.rows) return;
+  const size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + g / p.n_qt * p.G + qrow / p.rows) * kD + quad * 4;
+  *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2((f0 * a.x + f1 * b.x) * inv, (f0 * a.y + f1 * b.y) * inv),
+                                                     pack_bf16x2((f0 * a.z + f1 * b.z) * inv, (f0 * a.w + f1 * b.w) * inv));
+}
+
 bool few_rows(int rows, int G) { return rows * G <= kFewRows; }
 
 size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
   const int Hkv = kv[0].n_kv_heads;
   if (few_rows(rows, Hq / Hkv))
     return few_counter_bytes(B, Hkv) + static_cast<size_t>(few_grid(B, Hkv)) * kFewRows * (kD * 4 + sizeof(float2));
-  return 256;
+  return 2 * static_cast<size_t>(glance::num_sms()) * kBM * (kD * 4 + sizeof(float2));
 }
 
 }  // namespace
@@ -649,6 +1315,7 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
   p.Hkv = Hkv;
   p.G = G;
   p.W = (rows + 63) / 64;
+  p.n_qt = (G * rows + kBM - 1) / kBM;
   p.scale_log2 = scale * kLog2e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -671,9 +1338,21 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     cfg.dynamicSmemBytes = kFewSmem;
     e = cudaLaunchKernelEx(&cfg, kv4_attention_few_kernel, p);
   } else {
-    cfg.gridDim = dim3(B * rows * n_q_heads);
-    cfg.blockDim = dim3(kD);
-    e = cudaLaunchKernelEx(&cfg, kv4_attention_plain_kernel, p);
+    const int grid = glance::num_sms();
+    p.count = nullptr;
+    p.part_o = reinterpret_cast<float4*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(grid) * kBM * 32);
+    e = glance::ensure_smem(reinterpret_cast<const void*>(kv4_attention_wide_kernel), kWideSmem);
+    if (e != cudaSuccess) return glance::cuda_fail(e, who);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = kWideSmem;
+    e = cudaLaunchKernelEx(&cfg, kv4_attention_wide_kernel, p);
+    if (e != cudaSuccess) return glance::cuda_fail(e, who);
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * Hkv * p.n_qt * (kBM / kMergeRows));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, kv4_attention_merge_kernel, p, grid);
   }
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
   return GLANCE_OK;
