@@ -30,11 +30,13 @@ struct Params {
   Request req[kMaxB];
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
-  float4* part_o;   // unnormalised partial O of a block
-  float2* part_ml;  // its rows' (maximum in log2, sum of weights)
+  float4* part_o;   // unnormalised partial O of a block (few rows)
+  float2* part_ml;  // a part's rows' (maximum in log2, sum of weights)
   uint32_t* count;  // [B][Hkv] blocks of a head that are done
   int B, rows, Hq, Hkv, G, W;
-  int n_qt;         // query tiles of 128 rows per kv head
+  int n_qt, n_qp;   // query tiles of 128 rows per kv head, and pairs of them
+  uint4* part;      // parts of 128 rows: O / l as f16, [16 octets][128 rows]
+  int2* group;      // [B][Hkv][n_qp] the first part's block segment and the number of parts
   float scale_log2;
 };
 
@@ -511,35 +513,47 @@ size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv 
 // ------------------------------------------------ many query rows per kv head
 //
 // More than 16 query rows share a kv head: the products are worth the tensor
-// core's 128-row tiles. A block works on tiles of 128 query rows (head, packed
-// row) x 128 slots:
+// core's 128-row tiles. A block has two softmax slots, each with its own S and
+// O in tensor memory, that take turns on the tensor core: while one slot's
+// warps turn S into weights, the other slot's products run.
 //
-//   warps 12..15  codes and scales from global memory (one tile ahead in
-//                 registers) -> f16 K and V tiles in shared memory, in the
-//                 128-byte-swizzled layout of the tensor core, three stages
-//   warp 0        S = Q K^T into one of two tensor-memory buffers (the next
-//                 tile's before this tile's weights are ready), then O += P V
-//                 with P from tensor memory
-//   warps 4..11   softmax, two threads per row (64 slots each): mask, running
-//                 maximum, weights as f16 pairs to tensor memory; Q goes to
-//                 tensor memory once per segment, as f16 scaled per row
+//   warp 2        bulk copies of codes and scales (half tiles, three in flight)
+//   warps 12..15  codes -> f16 K and V tiles in shared memory, in the
+//                 128-byte-swizzled layout of the tensor core, two stages
+//   warp 0        S = Q K^T (both from shared memory) and O += P V (P from
+//                 tensor memory, over the columns of its S)
+//   warps 4..7, 8..11  softmax of slot 0 and 1, one thread per query row: mask,
+//                 running maximum, weights as f16 pairs; Q as f16 scaled per
+//                 row at a segment's start; output at its end
 //
-// Work: the slots of every (request, kv head, query tile) in units of 32. Where
-// each such group can be cut into equal parts that fill the grid, a block has
-// one part; else the list of all units is cut into equal runs and a block's
-// run may cross groups (a "segment" is its part in one group). The lengths are
-// read on the device. A group that one block has whole is written out there;
-// the others' parts are merged by a second kernel.
+// Tiles are 128 query rows (head, packed row) x 128 slots. Two neighbouring
+// query tiles of a kv head go to the two slots and share every K and V tile
+// (codes are widened once for both). A last tile without a neighbour has both
+// slots: they take its slot tiles in turn and join at the end.
+//
+// Work: the slots of every (request, kv head, query tile pair) in units of 32.
+// Where each such group can be cut into equal parts that fill the grid, a
+// block has one part; else the list of all units is cut into equal runs and a
+// block's run may cross groups (a "segment" is its part in one group). The
+// lengths are read on the device. A group that one block has whole is written
+// out there; the others' parts are merged by a second kernel.
 
 constexpr int kWideThreads = 512;
+// Registers per thread: 128 at launch (65,536 for the block), then shared out
+// between products + copies, softmax and conversion.
+constexpr int kRegsFew = 64, kRegsSoftmax = 168, kRegsConvert = 104;
+static_assert(128 * kRegsFew + 256 * kRegsSoftmax + 128 * kRegsConvert <= kWideThreads * 128, "register shares");
 constexpr int kBM = 128, kBN = 128;
-constexpr int kWideStages = 3;
-constexpr uint32_t kHalfBytes = kBN * 128;     // 64 dims x 128 slots, f16
-constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // a K or V tile
-constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kWideRing = kWideStages * kStageBytes;
-constexpr uint32_t kWideMisc = 1024;
-constexpr uint32_t kWideSmem = 1024 + kWideRing + kWideMisc;
+constexpr int kStages = 2, kRawStages = 3;
+constexpr uint32_t kHalfBytes = kBN * 128;       // 64 dims x 128 rows, f16
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;  // a Q, K or V tile
+constexpr uint32_t kRawCodes = kBN * glance::kKv4CodeBytes, kRawScales = kBN * glance::kKv4ScaleBytes;
+constexpr uint32_t kRawBytes = kRawCodes + kRawScales;  // 9,216: codes and scales of a K or V tile
+constexpr uint32_t kOffK = 2 * kTileBytes, kOffV = kOffK + kStages * kTileBytes, kOffRaw = kOffV + kStages * kTileBytes;
+constexpr uint32_t kOffMisc = kOffRaw + kRawStages * kRawBytes;
+constexpr uint32_t kWideMisc = 6144;
+constexpr uint32_t kWideSmem = 1024 + kOffMisc + kWideMisc;
+static_assert(kWideSmem <= 227 * 1024, "shared memory");
 constexpr int kMinUnits = 4;  // one tile
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -549,27 +563,35 @@ struct WidePlan {
   long long total;
   int tau;                // > 0: every group is cut into parts of tau units
   int blocks0[kMaxB];     // tau > 0: blocks before request r's
-  int first_req;          // first request with units
+};
+
+// A block's part in one group: units [a, a + n) of group g of request r.
+struct Segment {
+  int r, g, a, n;
+  int left;   // units of the run after this segment
+  int index;  // of the block's segments
 };
 
 struct WideMisc {
-  uint64_t k_full[kWideStages], v_full[kWideStages], kv_empty[kWideStages];
-  uint64_t q_ready, s_full[2], p_ready, o_done, drain;
-  uint32_t bad[kWideStages][4];  // slots of a tile whose V scales hold a NaN (tiles with tree slots)
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
+  uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], drain;  // [slot]
   uint32_t tmem;
-  int abort_flag;
+  int abort_flag, any;
+  Segment seg;
   WidePlan plan;
+  float2 ml[2][2][kBM];  // [segment parity][slot][row], slots that share a query tile
 };
 static_assert(sizeof(WideMisc) <= kWideMisc, "misc block");
 
-// The plan, by one warp; every block and the merge come to the same one.
+// The plan, by one warp; every block comes to the same one.
 __device__ __forceinline__ void wide_plan(const Params& p, WidePlan* pl, int lane, int blocks) {
   int units = 0;
   if (lane < p.B) {
     const int T = *p.req[lane].t_len;
     if (T >= 0 && T <= p.req[lane].t_cap - p.rows) units = (T + p.rows + kUnit - 1) / kUnit;
   }
-  const int gpr = p.Hkv * p.n_qt;
+  const int gpr = p.Hkv * p.n_qp;
   long long end = static_cast<long long>(units) * gpr;
 #pragma unroll
   for (int o = 1; o < kMaxB; o <<= 1) {
@@ -616,15 +638,8 @@ __device__ __forceinline__ long long run_start(long long total, int b, int block
   return total / blocks * b + total % blocks * b / blocks;
 }
 
-// A block's part in one group: units [a, a + n) of group g of request r.
-struct Segment {
-  int r, g, a, n;
-  int left;   // units of the run after this segment
-  int index;  // of the block's segments
-};
-
 __device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& pl, int b, int blocks, Segment& s) {
-  const int gpr = p.Hkv * p.n_qt;
+  const int gpr = p.Hkv * p.n_qp;
   s.index = 0;
   int r = 0;
   if (pl.tau) {
@@ -657,7 +672,7 @@ __device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& p
 }
 __device__ __forceinline__ bool next_segment(const Params& p, const WidePlan& pl, Segment& s) {
   if (s.left == 0) return false;
-  if (++s.g == p.Hkv * p.n_qt) {
+  if (++s.g == p.Hkv * p.n_qp) {
     s.g = 0;
     do ++s.r;
     while (pl.units[s.r] == 0);
@@ -682,20 +697,20 @@ struct Run {
   __device__ __forceinline__ int cols(int j) const { return min(kBN, (k1 - key0(j) + 31) & ~31); }
 };
 
+
 __device__ __forceinline__ void wide_fail(WideMisc* ms) {
   report(GLANCE_DEV_PIPELINE_TIMEOUT);
   atomicExch(&ms->abort_flag, 1);
 }
-// Bounded wait that also gives up once another role has.
+// Bounded wait of a converged warp; gives up once another role has.
 __device__ __forceinline__ bool wide_wait(uint64_t* bar, uint32_t parity, WideMisc* ms) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*reinterpret_cast<volatile int*>(&ms->abort_flag)) return false;
-      if (globaltimer_ns() - t0 > kWaitNs) return false;
-    }
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 0 &&
+        __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ms->abort_flag) != 0 || globaltimer_ns() - t0 > kWaitNs))
+      return false;
   }
 }
 
@@ -730,6 +745,27 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
          (static_cast<uint32_t>(kBM >> 4) << 24);
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+
+// `steps` products of 16 along the inner dimension, issued by one lane of a
+// converged warp so that descriptors stay in uniform registers.
+__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint64_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+    mma_bf16_ss(d, q + off, k + off, idesc, kk > 0);
+  }
+}
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, int steps, bool fresh) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    if (kk < steps) mma_bf16_ts(d, p + kk * 8, v + ((kk * 2048) >> 4), idesc, kk > 0 || !fresh);
+}
+
 // Slots kb .. kb + 31 (tree index = slot - T) that row `prow` sees.
 __device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W, int rows, int kb) {
   if (kb <= -32) return 0xFFFFFFFFu;
@@ -747,67 +783,89 @@ __device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W
   return prefix | (tree & (lim >= 32 ? 0xFFFFFFFFu : lim <= 0 ? 0u : (1u << lim) - 1u));
 }
 
-// Four rows' pieces of 32 dims (16 bytes of codes, two scales) of one tile.
+// A thread's share of a tile: rows row + 8i (i = 0..3) of the 128, dims 32q ..
+// 32q + 31 (16 bytes of codes, two scales). A warp has 32 rows; lane = 4 (row
+// mod 8) + q, so that eight lanes read 128 consecutive bytes of codes.
 struct Raw {
   uint4 codes[4];
   uint32_t scales[4];
 };
-
-// Rows of the tile at key0: the thread's are warp * 32 + 8i + (lane & 7), dims
-// 32 (lane >> 3) ..: a warp's load is 8 whole rows. Rows from k1 on are zero.
-__device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, const unsigned char* scales, long long head0,
-                                         int key0, int k1, int row, int q, int t_cap) {
+__device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, const unsigned char* scales, int row, int q,
+                                         int left) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int slot = key0 + row + 8 * i;
-    x.codes[i] = make_uint4(0, 0, 0, 0);
-    x.scales[i] = 0;
-    if (slot < k1 && GLANCE_IN_BOUNDS(slot, t_cap)) {
-      x.codes[i] = __ldg(reinterpret_cast<const uint4*>(codes + (head0 + slot) * 64) + q);
-      x.scales[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + (head0 + slot) * 8) + q);
+    x.codes[i] = *reinterpret_cast<const uint4*>(codes + (row + 8 * i) * 64 + q * 16);
+    x.scales[i] = *reinterpret_cast<const uint16_t*>(scales + (row + 8 * i) * 8 + q * 2);
+    if (left < kBN && row + 8 * i >= left) {  // behind the run: zero, whatever is there
+      x.codes[i] = make_uint4(0, 0, 0, 0);
+      x.scales[i] = 0;
     }
   }
 }
 
-// ... as f16 into the tile: row r's 16-byte chunk c of a half is at
-// r * 128 + 16 (c ^ (r & 7)); the eight lanes of a store phase have eight rows.
+// ... as f16 into the tile: row r's 16-byte chunk c of a half (64 dims) is at
+// r * 128 + 16 (c ^ (r & 7)). Lanes of the upper half take their four chunks
+// in the order 2, 3, 0, 1: eight lanes (two rows, four q) then write eight
+// different 16-byte columns of the 128-byte rows, and no bank twice.
 __device__ __forceinline__ void store_tile(const Raw& x, unsigned char* tile, int row, int q) {
   unsigned char* base = tile + (q >> 1) * kHalfBytes + row * 128;
+  const bool up = q >= 2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t s = scales2_to_f16(x.scales[i]);
-    const uint32_t s0 = prmt(s, s, 0x1010), s1 = prmt(s, s, 0x3232);
-    const uint32_t w[4] = {x.codes[i].x, x.codes[i].y, x.codes[i].z, x.codes[i].w};
+    const uint32_t s0 = prmt(s, s, up ? 0x3232 : 0x1010), s1 = prmt(s, s, up ? 0x1010 : 0x3232);
+    const uint32_t w[4] = {up ? x.codes[i].z : x.codes[i].x, up ? x.codes[i].w : x.codes[i].y,
+                           up ? x.codes[i].x : x.codes[i].z, up ? x.codes[i].y : x.codes[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t h[4];
       codes8_to_f16(w[j], h);
       const uint32_t sj = j < 2 ? s0 : s1;
-      const int chunk = ((q & 1) * 4 + j) ^ (row & 7);
+      const int chunk = ((q & 1) * 4 + (j ^ (q & 2))) ^ (row & 7);
       *reinterpret_cast<uint4*>(base + i * 8 * 128 + chunk * 16) =
           make_uint4(mul_f16x2(h[0], sj), mul_f16x2(h[1], sj), mul_f16x2(h[2], sj), mul_f16x2(h[3], sj));
     }
   }
 }
 
+// Eight values of a row times f, as f16 and as bf16.
+__device__ __forceinline__ uint4 eight_f16(const uint32_t* r, float f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 eight_bf16(const uint32_t* r, float f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
-  WideMisc* ms = reinterpret_cast<WideMisc*>(ring + kWideRing);
+  WideMisc* ms = reinterpret_cast<WideMisc*>(smem + kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = gridDim.x;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kWideStages; ++s) {
+    for (int s = 0; s < kRawStages; ++s) {
+      mbar_init(&ms->raw_full[s], 1);
+      mbar_init(&ms->raw_empty[s], 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&ms->k_full[s], 4);
       mbar_init(&ms->v_full[s], 4);
-      mbar_init(&ms->kv_empty[s], 1);
+      mbar_init(&ms->k_empty[s], 1);
+      mbar_init(&ms->v_empty[s], 1);
     }
-    mbar_init(&ms->q_ready, 256);
-    mbar_init(&ms->s_full[0], 1);
-    mbar_init(&ms->s_full[1], 1);
-    mbar_init(&ms->p_ready, 256);
-    mbar_init(&ms->o_done, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&ms->q_ready[x], 128);
+      mbar_init(&ms->s_full[x], 1);
+      mbar_init(&ms->p_ready[x], 128);
+      mbar_init(&ms->o_done[x], 1);
+    }
     mbar_init(&ms->drain, 1);
     ms->abort_flag = 0;
     fence_barrier_init();
@@ -818,327 +876,432 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
   }
   pdl_wait_prior();
   pdl_launch_dependents();
-  if (warp == 2) wide_plan(p, &ms->plan, lane, blocks);
-  if (blockIdx.x == 0 && threadIdx.x < p.B) {
-    const int T = *p.req[threadIdx.x].t_len;
-    if (T < 0 || T > p.req[threadIdx.x].t_cap - p.rows) report(GLANCE_DEV_TREE_CAPACITY);
+  if (warp == 3) {
+    wide_plan(p, &ms->plan, lane, blocks);
+    __syncwarp();
+    if (lane == 0) ms->any = first_segment(p, ms->plan, blockIdx.x, blocks, ms->seg);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
-  const uint32_t tS = tmem, tO = tmem + 256, tP = tmem + 384, tQ = tmem + 448;
   const WidePlan& pl = ms->plan;
-  Segment sg;
-  const bool any = first_segment(p, pl, blockIdx.x, blocks, sg);
+  const bool any = ms->any != 0;
 
-  if (warp == 0 && any) {
-    // --------------------------------------------------------------- products
-    if (lane == 0) {
-      int i = 0;  // tiles of the block so far
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0 && any) {
+      // ------------------------------------------------------------- products
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + kOffK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + kOffV), kHalfBytes, 1024);
+      constexpr uint64_t kTileStep = kTileBytes >> 4;
+      Segment s = ms->seg;
+      int t0 = 0;                // slot tiles of the block before this segment
+      uint32_t n_q[2] = {0, 0};  // phases of q_ready and p_ready so far
+      uint32_t n_p[2] = {0, 0};
       bool good = true;
-      Segment s = sg;
       do {
         const Run run(s, *p.req[s.r].t_len + p.rows);
-        const auto issue_s = [&](int j) {
-          const int t = i + j, st = t % kWideStages;
-          if (!wide_wait(&ms->k_full[st], (t / kWideStages) & 1, ms)) return false;
+        const bool pair = 2 * (s.g % p.n_qp) + 1 < p.n_qt;
+        const int items = pair ? 2 * run.tiles : run.tiles;
+        // item k: slot k & 1, tile k / 2 of a pair or tile k
+        const auto issue_s = [&](int k) {
+          const int x = k & 1, j = pair ? k >> 1 : k, t = t0 + j, st = t & 1;
+          if (!wide_wait(&ms->k_full[st], (t >> 1) & 1, ms)) return false;
           tc_fence_after();
-          const uint32_t k_addr = smem_u32(ring + st * kStageBytes);
-          const uint32_t idesc = idesc_f16(run.cols(j), false);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tS + (t & 1) * 128, tQ + kk * 8,
-                        sdesc_sw128(k_addr + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
-          mma_commit(&ms->s_full[t & 1]);
+          if (elect_one()) {
+            issue_qk(tmem + x * 128, q_desc + (pair ? x * kTileStep : 0), k_desc + st * kTileStep,
+                     idesc_f16(run.cols(j), false));
+            mma_commit(&ms->s_full[x]);
+            if (!pair || x) mma_commit(&ms->k_empty[st]);
+          }
+          __syncwarp();
           return true;
         };
-        good = wide_wait(&ms->q_ready, s.index & 1, ms);
-        if (good) {
+        for (int x = 0; x < (pair ? 2 : 1) && good; ++x) good = wide_wait(&ms->q_ready[x], n_q[x]++ & 1, ms);
+        good = good && issue_s(0) && (items < 2 || issue_s(1));
+        for (int k = 0; good && k < items; ++k) {
+          const int x = k & 1, j = pair ? k >> 1 : k, t = t0 + j, st = t & 1;
+          good = wide_wait(&ms->p_ready[x], n_p[x]++ & 1, ms) && wide_wait(&ms->v_full[st], (t >> 1) & 1, ms);
+          if (!good) break;
           tc_fence_after();
-          good = issue_s(0);
-        }
-        for (int j = 0; good && j < run.tiles; ++j) {
-          if (j + 1 < run.tiles && !issue_s(j + 1)) {
-            good = false;
-            break;
+          if (elect_one()) {
+            issue_pv(tmem + 256 + x * 128, tmem + x * 128, v_desc + st * kTileStep, idesc_f16(kD, true),
+                     run.cols(j) / 16, k < 2);
+            if (!pair || x) mma_commit(&ms->v_empty[st]);
+            if (k + 2 >= items) mma_commit(&ms->o_done[x]);
           }
-          const int t = i + j, st = t % kWideStages;
-          if (!wide_wait(&ms->p_ready, t & 1, ms) || !wide_wait(&ms->v_full[st], (t / kWideStages) & 1, ms)) {
-            good = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t v_addr = smem_u32(ring + st * kStageBytes + kTileBytes);
-          const int steps = run.cols(j) / 16;
-          for (int kk = 0; kk < steps; ++kk)
-            mma_bf16_ts(tO, tP + kk * 8, sdesc_sw128(v_addr + kk * 2048, kHalfBytes, 1024), idesc_f16(kD, true),
-                        (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&ms->o_done);
-          mma_commit(&ms->kv_empty[st]);
+          __syncwarp();
+          // the slot's next S takes the columns of these weights: products run in the order of their issue
+          if (k + 2 < items) good = issue_s(k + 2);
         }
-        i += run.tiles;
+        t0 += run.tiles;
+      } while (good && next_segment(p, pl, s));
+      if (!good) wide_fail(ms);
+    } else if (warp == 2 && any) {
+      // ---------------------------------------------------------- bulk copies
+      Segment s = ms->seg;
+      int h = 0;  // half tiles so far: K, V, K, V, ...
+      bool good = true;
+      do {
+        const Request& rq = p.req[s.r];
+        const Run run(s, *rq.t_len + p.rows);
+        const long long head0 = static_cast<long long>(s.g / p.n_qp) * rq.head_stride;
+        for (int e = 0; e < 2 * run.tiles && good; ++e, ++h) {
+          const int st = h % kRawStages, key0 = run.key0(e >> 1);
+          if (h >= kRawStages) good = wide_wait(&ms->raw_empty[st], (h / kRawStages - 1) & 1, ms);
+          if (!good) break;
+          if (lane == 0) {
+            unsigned char* dst = smem + kOffRaw + st * kRawBytes;
+            const int n = min(kBN, (run.k1 - key0 + 1) & ~1);  // an even number: 16 bytes of scales
+            if (GLANCE_IN_BOUNDS(key0 + n - 1, rq.head_stride)) {
+              const long long at = head0 + key0;
+              mbar_arrive_expect_tx(&ms->raw_full[st], n * (glance::kKv4CodeBytes + glance::kKv4ScaleBytes));
+              bulk_copy_g2s(dst, (e & 1 ? rq.v : rq.k) + at * 64, n * 64, &ms->raw_full[st]);
+              bulk_copy_g2s(dst + kRawCodes, (e & 1 ? rq.v_scale : rq.k_scale) + at * 8, n * 8, &ms->raw_full[st]);
+            } else {
+              mbar_arrive(&ms->raw_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+      } while (good && next_segment(p, pl, s));
+      if (!good) {
+        wide_fail(ms);
+        for (int u = max(0, h - kRawStages); u < h; ++u)  // the copies in flight land before the block leaves
+          (void)mbar_wait(&ms->raw_full[u % kRawStages], (u / kRawStages) & 1, 50000000ull);
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------ which blocks have a group
+      // for the merge: by the block that has the group's first unit; requests
+      // without room have none
+      if (any) {
+        Segment s = ms->seg;
+        do {
+          if (s.a) continue;
+          int n = 1;
+          if (pl.tau) {
+            n = (pl.units[s.r] + pl.tau - 1) / pl.tau;
+          } else {
+            const long long end = pl.base[s.r] + (s.g + 1ll) * pl.units[s.r];
+            for (;; n += 32) {
+              const unsigned past = __ballot_sync(0xffffffffu, run_start(pl.total, blockIdx.x + n + lane, blocks) >= end);
+              if (past) {
+                n += __ffs(past) - 1;
+                break;
+              }
+            }
+          }
+          if (lane == 0) p.group[s.r * p.Hkv * p.n_qp + s.g] = make_int2(2 * blockIdx.x + (s.index ? 1 : 0), n);
+        } while (next_segment(p, pl, s));
+      }
+      if (blockIdx.x == 0)
+        for (int r = 0; r < p.B; ++r)
+          if (pl.units[r] == 0) {
+            if (lane == 0) report(GLANCE_DEV_TREE_CAPACITY);
+            for (int g = lane; g < p.Hkv * p.n_qp; g += 32) p.group[r * p.Hkv * p.n_qp + g] = make_int2(0, 0);
+          }
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    if (any) {
+      // --------------------------------------------------- codes to f16 tiles
+      const int row = (warp - 12) * 32 + (lane >> 2), q = lane & 3;
+      Segment s = ms->seg;
+      int h = 0;
+      bool good = true;
+      do {
+        const int T = *p.req[s.r].t_len;
+        const Run run(s, T + p.rows);
+        for (int e = 0; e < 2 * run.tiles; ++e, ++h) {
+          const int rs = h % kRawStages, t = h >> 1, st = t & 1, is_v = h & 1, key0 = run.key0(e >> 1);
+          good = wide_wait(&ms->raw_full[rs], (h / kRawStages) & 1, ms);
+          if (!good) break;
+          const unsigned char* src = smem + kOffRaw + rs * kRawBytes;
+          Raw x;
+          load_raw(x, src, src + kRawCodes, row, q, run.k1 - key0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->raw_empty[rs]);
+          if (is_v && key0 + kBN > T) {
+            // a V row with a scale that is not a number is left out: 0 * NaN
+            // would reach the rows that do not see it (the softmax marks the
+            // scores of those that do)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool nan = (x.scales[i] & 0x7Fu) == 0x7Fu || (x.scales[i] & 0x7F00u) == 0x7F00u;
+              if (__ballot_sync(0xffffffffu, nan) >> (lane & 28) & 15u) {
+                x.codes[i] = make_uint4(0, 0, 0, 0);
+                x.scales[i] = 0;
+              }
+            }
+          }
+          if (t >= kStages) good = wide_wait(is_v ? &ms->v_empty[st] : &ms->k_empty[st], ((t >> 1) - 1) & 1, ms);
+          if (!good) break;
+          store_tile(x, smem + (is_v ? kOffV : kOffK) + st * kTileBytes, row, q);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
+        }
       } while (good && next_segment(p, pl, s));
       if (!good) wide_fail(ms);
     }
-  } else if (warp >= 12 && any) {
-    // ----------------------------------------------------- codes to f16 tiles
-    const int row = (warp - 12) * 32 + (lane & 7), q = lane >> 3;
-    Segment s = sg;
-    int T = *p.req[s.r].t_len;
-    Run run(s, T + p.rows);
-    int j = 0, t = 0;
-    bool more = true, good = true;
-    Raw k, v;
-    const auto load = [&](bool of_v, Raw& x) {
-      const Request& rq = p.req[s.r];
-      load_raw(x, of_v ? rq.v : rq.k, of_v ? rq.v_scale : rq.k_scale, static_cast<long long>(s.g / p.n_qt) * rq.head_stride,
-               run.key0(j), run.k1, row, q, rq.t_cap);
-    };
-    load(false, k);
-    load(true, v);
-    while (more) {
-      const int st = t % kWideStages;
-      const bool tree = run.key0(j) + kBN > T;
-      if (t >= kWideStages) good = wide_wait(&ms->kv_empty[st], (t / kWideStages - 1) & 1, ms);
-      if (!__all_sync(0xffffffffu, good)) {
-        wide_fail(ms);
-        break;
-      }
-      unsigned char* tile = ring + st * kStageBytes;
-      if (tree) {
-        // a V row with a scale that is not a number is left out (0 * NaN would
-        // reach the rows that do not see it); its slot is marked instead
-        uint32_t word = 0;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if (any) {
+      // ------------------------------------------------------------- softmax
+      const int x = warp >= 8, lrow = (warp & 3) * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
+      const int R = p.G * p.rows;
+      uint32_t n_s = 0, n_o[2] = {0, 0};  // phases of s_full (this slot) and o_done so far
+      bool ok = true;
+      Segment s = ms->seg;
+      do {
+        const Request& rq = p.req[s.r];
+        const int T = *rq.t_len;
+        const Run run(s, T + p.rows);
+        const int head = s.g / p.n_qp, qt0 = 2 * (s.g % p.n_qp);
+        const bool pair = qt0 + 1 < p.n_qt;
+        // The thread's query row, worked out anew wherever it is needed: kept,
+        // it would cost registers while a row of S is in them.
+        const auto query = [&](bool& valid, int& prow) -> size_t {
+          int qrow = (pair ? qt0 + x : qt0) * kBM + lrow;
+          asm volatile("" : "+r"(qrow));
+          valid = qrow < R;
+          prow = valid ? qrow % p.rows : 0;
+          return ((static_cast<size_t>(s.r) * p.rows + prow) * p.Hq + head * p.G + (valid ? qrow / p.rows : 0)) * kD;
+        };
+        float sc;
+        {
+          bool valid;
+          int prow;
+          const size_t q_at = query(valid, prow);
+          // the row as f16; the products that read the previous segment's Q are done
+          uint4 v[16];
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool nan = (v.scales[i] & 0x7Fu) == 0x7Fu || (v.scales[i] & 0x7F00u) == 0x7F00u;
-          uint32_t b = __ballot_sync(0xffffffffu, nan);
-          b |= b >> 16;
-          b = (b | b >> 8) & 0xFFu;  // rows 8i .. 8i + 7
-          word |= b << (8 * i);
-          if (b >> (lane & 7) & 1u) {
-            v.codes[i] = make_uint4(0, 0, 0, 0);
-            v.scales[i] = 0;
-          }
-        }
-        if (lane == 0) ms->bad[st][warp - 12] = word;
-      }
-      store_tile(k, tile, row, q);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->k_full[st]);
-      // the next tile of this segment, or the first of the next one
-      Segment s2 = s;
-      if (++j == run.tiles) {
-        j = 0;
-        more = next_segment(p, pl, s2);
-      }
-      const Raw v_now = v;
-      if (more) {
-        if (j == 0) {
-          s = s2;
-          T = *p.req[s.r].t_len;
-          run = Run(s, T + p.rows);
-        }
-        load(false, k);
-        load(true, v);
-      }
-      store_tile(v_now, tile + kTileBytes, row, q);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->v_full[st]);
-      ++t;
-    }
-  } else if (warp >= 4 && warp < 12 && any) {
-    // ---------------------------------------------------------------- softmax
-    // Warp (quarter, sub) has rows 32 quarter + 16 sub + (lane & 15); lanes
-    // 0-15 slots / dims 0-63 of a tile, lanes 16-31 the other 64.
-    const int half = lane >> 4, quarter = warp & 3, sub = (warp - 4) >> 2;
-    const int lrow = quarter * 32 + sub * 16 + (lane & 15);
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32 + sub * 16) << 16;
-    const int R = p.G * p.rows;
-    bool ok = true;
-    int i = 0;
-    Segment s = sg;
-    do {
-      const Request& rq = p.req[s.r];
-      const int T = *rq.t_len, n_keys = T + p.rows;
-      const Run run(s, n_keys);
-      const int head = s.g / p.n_qt, qt = s.g % p.n_qt;
-      const int qrow = qt * kBM + lrow;
-      const bool valid = qrow < R;
-      const int prow = valid ? qrow % p.rows : 0;
-      const size_t q_at = ((static_cast<size_t>(s.r) * p.rows + prow) * p.Hq + head * p.G + (valid ? qrow / p.rows : 0)) * kD;
-      // Q row, this half's 64 dims, to tensor memory (the products that read
-      // the previous segment's have finished: their weights were written)
-      float sc;
-      {
-        uint4 x[8];
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at + 64 * half);
+          for (int e = 0; e < 16; ++e) v[e] = valid ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+          uint32_t top = 0;  // the largest magnitude's bits: in the order of the absolute values
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = valid ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-        uint32_t top = 0;  // the largest magnitude's bits: order of the absolute values
-#pragma unroll
-        for (int e = 0; e < 32; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
-        const float qf = query_factor(amax);
-        sc = score_factor(amax, qf, p.scale_log2, rq.k_global);
-        uint32_t h[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * qf, __uint_as_float(w[e] & 0xFFFF0000u) * qf);
-        tmem_st16x2<32>(tQ + lane_off, *reinterpret_cast<const uint32_t(*)[16]>(h));
-        tmem_st16x2<32>(tQ + lane_off + 16, *reinterpret_cast<const uint32_t(*)[16]>(h + 16));
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&ms->q_ready);
-      }
-      float m = -INFINITY, lsum = 0.f;
-      for (int j = 0; j < run.tiles; ++j) {
-        const int t = i + j, key0 = run.key0(j);
-        const bool got_s = __all_sync(0xffffffffu, wide_wait(&ms->s_full[t & 1], (t >> 1) & 1, ms));
-        if (!got_s) {
-          wide_fail(ms);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld32x2<64>(tS + (t & 1) * 128 + lane_off, *reinterpret_cast<uint32_t(*)[32]>(sr));
-        tmem_ld32x2<64>(tS + (t & 1) * 128 + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
-        tmem_ld_wait();
-        if (key0 + kBN > T || key0 + kBN > run.k1) {
-          uint32_t bad[2] = {0u, 0u};
-          if (key0 + kBN > T) {
-            // the marks were written before the K tile was handed over
-            if (!wide_wait(&ms->k_full[t % kWideStages], (t / kWideStages) & 1, ms)) wide_fail(ms);
-            bad[0] = ms->bad[t % kWideStages][2 * half];
-            bad[1] = ms->bad[t % kWideStages][2 * half + 1];
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int s0 = key0 + 64 * half + 32 * c;
-            uint32_t vis = valid ? visible32(rq, prow, p.W, p.rows, s0 - T) : 0u;
-            const int lim = run.k1 - s0;
-            if (lim < 32) vis &= lim <= 0 ? 0u : (1u << lim) - 1u;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              sr[32 * c + e] = !(vis >> e & 1u) ? 0xFF800000u : (bad[c] >> e & 1u) ? 0x7FC00000u : sr[32 * c + e];
-          }
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 64; e += 8) {
-          mx0 = max3f(mx0, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-          mx1 = max3f(mx1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
-          mx2 = max3f(mx2, __uint_as_float(sr[e + 4]), __uint_as_float(sr[e + 5]));
-          mx3 = max3f(mx3, __uint_as_float(sr[e + 6]), __uint_as_float(sr[e + 7]));
-        }
-        float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sc;
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-        // the running maximum moves when some row of the warp grew by 8 (log2):
-        // a stale one keeps the weights below 2^8 and cancels between O and l
-        const bool grow = __any_sync(0xffffffffu, mt > m + 8.f);
-        const float m_new = grow ? fmaxf(m, mt) : m;
-        const float off = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - off);
-        uint32_t pk[32];
-        const unsigned long long sc2 = pair_f2(sc, sc), no2 = pair_f2(-off, -off);
-        unsigned long long l2 = pair_f2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float t0, t1;
-          split_f2(fma_f2(pair_f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, no2), t0, t1);
-          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-          l2 = add_f2(l2, pair_f2(p0, p1));
-          pk[e] = pack_f16x2(p0, p1);
-        }
-        float l0, l1;
-        split_f2(l2, l0, l1);
-        if (j > 0) {  // the product before this one has read P and written O
-          const bool got_o = __all_sync(0xffffffffu, wide_wait(&ms->o_done, (t - 1) & 1, ms));
-          if (!got_o) {
-            wide_fail(ms);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-        }
-        tmem_st16x2<32>(tP + lane_off, *reinterpret_cast<const uint32_t(*)[16]>(pk));
-        tmem_st16x2<32>(tP + lane_off + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-            const uint32_t ta = tO + lane_off + 32 * c;
-            tmem_ld32x2<64>(ta, r);
-            tmem_ld_wait();
-            uint32_t x[16], y[16];
+          for (int e = 0; e < 16; ++e)
+            top = max(max(max(v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu) >> 16, max(v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu) >> 16),
+                      max(max(max(v[e].x & 0x7FFFu, v[e].y & 0x7FFFu), max(v[e].z & 0x7FFFu, v[e].w & 0x7FFFu)), top));
+          const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
+          const float qf = query_factor(amax);
+          sc = score_factor(amax, qf, p.scale_log2, rq.k_global);
+          if (pair || !x) {
+            unsigned char* dst = smem + (pair ? x * kTileBytes : 0) + lrow * 128;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              x[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-              y[e] = __float_as_uint(__uint_as_float(r[16 + e]) * alpha);
+              const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+              uint32_t f[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f[i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
+              *reinterpret_cast<uint4*>(dst + (e >> 3) * kHalfBytes + (((e & 7) ^ (lrow & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
             }
-            tmem_st16x2<64>(ta, x);
-            tmem_st16x2<64>(ta + 16, y);
+            fence_proxy_async_smem();
+            mbar_arrive(&ms->q_ready[x]);
           }
         }
-        tmem_st_wait();
-        lsum = lsum * alpha + (l0 + l1);
-        m = m_new;
-        tc_fence_before();
-        mbar_arrive(&ms->p_ready);
-      }
-      if (ok) {
-        ok = __all_sync(0xffffffffu, wide_wait(&ms->o_done, (i + run.tiles - 1) & 1, ms));
-        if (!ok) wide_fail(ms);
-        tc_fence_after();
-      }
-      if (!ok) break;
-      i += run.tiles;
-      float l = lsum + __shfl_xor_sync(0xffffffffu, lsum, 16);
-      const bool whole = s.n == pl.units[s.r];
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : rq.v_global / l;
+        float m = -INFINITY, l = 0.f;
+        const int step = pair ? 1 : 2, j0 = pair ? 0 : x;
+        for (int j = j0; j < run.tiles; j += step) {
+          const int key0 = run.key0(j);
+          const int nc = run.cols(j) / 32;
+          const bool tree = key0 + 32 * nc > T;
+          uint32_t bad[4] = {0u, 0u, 0u, 0u};  // slots with a V scale that is not a number
+          if (tree) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int slot = key0 + 32 * i + lane;
+              uint2 vs = make_uint2(0, 0);
+              if (slot < run.k1 && GLANCE_IN_BOUNDS(slot, rq.t_cap))
+                vs = __ldg(reinterpret_cast<const uint2*>(rq.v_scale) + static_cast<long long>(head) * rq.head_stride + slot);
+              const uint32_t nan = __vcmpeq4(vs.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(vs.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              bad[i] = __ballot_sync(0xffffffffu, nan != 0u);
+            }
+          }
+          ok = wide_wait(&ms->s_full[x], n_s++ & 1, ms);
+          if (!ok) break;
+          tc_fence_after();
+          if (tree) {
+            // masked in place, so that the rest is the same for every tile
+            bool valid;
+            int prow;
+            (void)query(valid, prow);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          tmem_ld32x2<64>(tO + lane_off + 32 * c, r);
-          tmem_ld_wait();
-          if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + q_at + 64 * half + 32 * c);
+            for (int c = 0; c < nc; ++c) {
+              const int s0 = key0 + 32 * c, lim = run.k1 - s0;
+              uint32_t vis = valid ? visible32(rq, prow, p.W, p.rows, s0 - T) : 0u;
+              if (lim < 32) vis &= (1u << lim) - 1u;
+              uint32_t r[32], y[16], z[16];
+              tmem_ld32(tS + 32 * c, r);
+              tmem_wait32(r);
+              const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                y[e] = !(vis >> e & 1u) ? 0xFF800000u : (b >> e & 1u) ? 0x7FC00000u : r[e];
+                z[e] = !(vis >> (16 + e) & 1u) ? 0xFF800000u : (b >> (16 + e) & 1u) ? 0x7FC00000u : r[16 + e];
+              }
+              tmem_st16(tS + 32 * c, y);
+              tmem_st16(tS + 32 * c + 16, z);
+            }
+            tmem_st_wait();
+          }
+          // 64 slots at a time: a whole row would not fit the registers
+#pragma unroll 1
+          for (int h = 0; 2 * h < nc; ++h) {
+            uint32_t sr[64];
+            tmem_row64(tS + 64 * h, sr);
+            const bool both = 2 * h + 1 < nc;  // the product has the second 32 slots
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (c == 0 || both) {
+#pragma unroll
+                for (int e = 32 * c; e < 32 * c + 32; e += 8)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    mx[i] = max3f(mx[i], __uint_as_float(sr[e + 2 * i]), __uint_as_float(sr[e + 2 * i + 1]));
+              }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            // the running maximum moves when some row of the warp grew by 8 (log2):
+            // a stale one keeps the weights below 2^8 and cancels between O and l
+            if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+              const float mn = fmaxf(m, mt);
+              const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+              m = mn;
+              l *= alpha;
+              // O is complete (S of this tile came after the product of the last)
+              // but for the weights of the row's first half
+              if (j > j0)
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t r[16];
+                  tmem_ld16(tO + 16 * c, r);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                  tmem_st16(tO + 16 * c, r);
+                }
+              if (h) {
+                tmem_st_wait();
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t r[16];
+                  tmem_ld16(tS + 16 * c, r);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const float2 f = f16x2_to_f32(r[e]);
+                    r[e] = pack_f16x2(f.x * alpha, f.y * alpha);
+                  }
+                  tmem_st16(tS + 16 * c, r);
+                }
+              }
+            }
+            const float off = m == -INFINITY ? 0.f : m;
+            const unsigned long long sc2 = pair_f2(sc, sc), no2 = pair_f2(-off, -off);
+            unsigned long long l2 = pair_f2(0.f, 0.f), l3 = l2;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (c == 0 || both) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  float u0, u1;
+                  split_f2(fma_f2(pair_f2(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sc2, no2),
+                           u0, u1);
+                  const float p0 = ex2_approx(u0), p1 = ex2_approx(u1);
+                  if (e & 1)
+                    l3 = add_f2(l3, pair_f2(p0, p1));
+                  else
+                    l2 = add_f2(l2, pair_f2(p0, p1));
+                  pk[e] = pack_f16x2(p0, p1);
+                }
+                tmem_st16(tS + 32 * h + 16 * c, pk);
+              }
+            float l0, l1;
+            split_f2(add_f2(l2, l3), l0, l1);
+            l += l0 + l1;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&ms->p_ready[x]);
+        }
+        if (!ok) break;
+        // ------------------------------------------------ the segment's output
+        const bool whole = s.n == pl.units[s.r];
+        bool valid;
+        int prow;
+        const size_t q_at = query(valid, prow);
+        // two parts per block: its first segment's and its last one's, each of
+        // two query tiles, O / l rounded to f16: half a step is 2^-12 of an
+        // element, a sixteenth of the output's, and halves the merge's bytes
+        const size_t part = 2 * (2 * static_cast<size_t>(blockIdx.x) + (s.index ? 1 : 0)) + (pair ? x : 0);
+        uint4* po = p.part + part * 16 * kBM + lrow;
+        if (l != l) m = 0.f;  // a NaN row stays one in every merge
+        if (pair) {
+          ok = wide_wait(&ms->o_done[x], n_o[x]++ & 1, ms);
+          if (!ok) break;
+          tc_fence_after();
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tO + 32 * c, r);
+            tmem_wait32(r);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                w[f] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * f]) * inv, __uint_as_float(r[8 * e + 2 * f + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              if (!whole)
+                po[(4 * c + e) * kBM] = eight_f16(r + 8 * e, inv);
+              else if (valid)
+                *reinterpret_cast<uint4*>(p.out + q_at + 32 * c + 8 * e) = eight_bf16(r + 8 * e, inv * rq.v_global);
             }
           }
-        }
-      } else {
-        // two slots per block: its first segment's and its last one's; [slot][dim quad][row]
-        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.index ? 1 : 0);
-        float4* po = p.part_o + slot * 32 * kBM + lrow;
+          if (!whole) p.part_ml[part * kBM + lrow] = make_float2(m, l);
+        } else {
+          // both slots have this query tile: slot x writes dims 64x .. 64x + 63
+          float2(*ml)[kBM] = ms->ml[s.index & 1];
+          ml[x][lrow] = make_float2(m, l);
+          ok = wide_wait(&ms->o_done[0], n_o[0]++ & 1, ms) && (run.tiles < 2 || wide_wait(&ms->o_done[1], n_o[1]++ & 1, ms));
+          ok = !named_bar_or(1, 256, !ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 a = ml[0][lrow], b = ml[1][lrow];
+          const float M = fmaxf(a.x, b.x);
+          const float fa = a.x == -INFINITY ? 0.f : ex2_approx(a.x - M), fb = b.x == -INFINITY ? 0.f : ex2_approx(b.x - M);
+          const float L = fa * a.y + fb * b.y, inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          tmem_ld32x2<64>(tO + lane_off + 32 * c, r);
-          tmem_ld_wait();
+          for (int c = 2 * x; c < 2 * x + 2; ++c) {
+            uint32_t r[32], r1[32];
+            tmem_ld32(tmem + lanes + 256 + 32 * c, r);
+            tmem_wait32(r);
+            if (run.tiles > 1) {
+              tmem_ld32(tmem + lanes + 384 + 32 * c, r1);
+              tmem_wait32(r1);
+            }
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            po[(16 * half + 8 * c + e) * kBM] =
-                make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
-                            __uint_as_float(r[4 * e + 3]));
+            for (int e = 0; e < 32; ++e) {
+              const float o1 = run.tiles > 1 ? fb * __uint_as_float(r1[e]) : 0.f;
+              r[e] = __float_as_uint(fmaf(fa, __uint_as_float(r[e]), o1));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!whole)
+                po[(4 * c + e) * kBM] = eight_f16(r + 8 * e, inv);
+              else if (valid)
+                *reinterpret_cast<uint4*>(p.out + q_at + 32 * c + 8 * e) = eight_bf16(r + 8 * e, inv * rq.v_global);
+            }
+          }
+          if (!whole && !x) p.part_ml[part * kBM + lrow] = make_float2(M, L);
+          tc_fence_before();
+          named_bar(1, 256);  // both have read both O before either slot's next product
         }
-        if (half == 0) p.part_ml[slot * kBM + lrow] = make_float2(l != l ? 0.f : m, l);  // a NaN row stays one
-      }
-      tc_fence_before();  // O and Q are free for the next segment's products
-    } while (next_segment(p, pl, s));
+        tc_fence_before();
+      } while (next_segment(p, pl, s));
+      if (!ok) wide_fail(ms);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1157,94 +1320,84 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
   }
 }
 
-// The parts of the groups that several blocks had. Block (group, 4 rows):
-// thread = (slice of the parts, dim quad, row). The plan needs T only, which
-// nothing writes while this or the kernel before it runs.
+// The parts of the groups that several blocks had. Block (query tile, 8 rows):
+// thread = (half of the parts, octet of dims, row).
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 4;
+constexpr int kMergeRows = 8;
 
-__global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(const __grid_constant__ Params p, int blocks) {
-  __shared__ WidePlan pl;
-  __shared__ float4 s_o[128];
+__global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(const __grid_constant__ Params p) {
+  __shared__ float s_o[8][128];
   __shared__ float2 s_ml[128];
-  if (threadIdx.x < 32) wide_plan(p, &pl, threadIdx.x, blocks);
-  __syncthreads();
-  const int gpr = p.Hkv * p.n_qt;
-  const int grp = blockIdx.x / (kBM / kMergeRows), rows0 = blockIdx.x % (kBM / kMergeRows) * kMergeRows;
-  const int r = grp / gpr, g = grp % gpr, units = pl.units[r];
-  const int qrow0 = g % p.n_qt * kBM + rows0;
+  const int tile = blockIdx.x / (kBM / kMergeRows), rows0 = blockIdx.x % (kBM / kMergeRows) * kMergeRows;
+  const int qt = tile % p.n_qt, rh = tile / p.n_qt;  // request * Hkv + head
+  const int row = threadIdx.x & 7, octet = threadIdx.x >> 3 & 15, half = threadIdx.x >> 7;
+  const int lrow = rows0 + row, qrow = qt * kBM + lrow;
   pdl_wait_prior();  // in every block: this kernel ends after the one before it
   pdl_launch_dependents();
-  if (units == 0 || qrow0 >= p.G * p.rows) return;
-  int first, n;           // the blocks that have a part of this group
-  bool late = false;      // the first of them has it as its last segment
-  if (pl.tau) {
-    n = (units + pl.tau - 1) / pl.tau;
-    first = pl.blocks0[r] + g * n;
-  } else {
-    const long long x0 = pl.base[r] + static_cast<long long>(g) * units, x1 = x0 + units;
-    first = static_cast<int>(x0 * blocks / pl.total);
-    while (run_start(pl.total, first + 1, blocks) <= x0) ++first;
-    while (run_start(pl.total, first, blocks) > x0) --first;
-    late = run_start(pl.total, first, blocks) < x0;
-    n = 1;
-    while (run_start(pl.total, first + n, blocks) < x1) ++n;
-  }
-  if (n == 1) return;  // written whole
-  const int row = threadIdx.x & (kMergeRows - 1), quad = threadIdx.x >> 2 & 31, slice = threadIdx.x >> 7;
-  const int lrow = rows0 + row;
-  const int per = (n + 1) / 2, b0 = slice * per, b1 = min(n, b0 + per);
-  const auto slot_of = [&](int b) { return 2 * static_cast<size_t>(first + b) + (b == 0 && late ? 1 : 0); };
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = b0; s0 < b1; s0 += 8) {
-    float4 v[8];
-    float2 ml[8];
+  if (qt * kBM + rows0 >= p.G * p.rows) return;
+  const int2 gi = __ldcg(p.group + rh * p.n_qp + qt / 2);
+  const int n = gi.y;
+  if (n < 2) return;  // written whole, or no output
+  // the first block's part is gi.x (its first or last segment), the others' their first segments
+  const auto part_of = [&](int b) { return 2 * static_cast<size_t>(b ? (gi.x & ~1) + 2 * b : gi.x) + (qt & 1); };
+  const int per = (n + 1) / 2, b0 = half * per, b1 = min(n, b0 + per);
+  float M = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = 10;
+  for (int s0 = b0; s0 < b1; s0 += kAhead) {
+    uint4 v[kAhead];
+    float2 ml[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kAhead; ++e) {
       const bool in = s0 + e < b1;
-      const size_t slot = slot_of(in ? s0 + e : b0);
-      ml[e] = in ? __ldcg(p.part_ml + slot * kBM + lrow) : make_float2(-INFINITY, 0.f);
-      v[e] = in ? __ldcg(p.part_o + (slot * 32 + quad) * kBM + lrow) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const size_t part = part_of(in ? s0 + e : b0);
+      ml[e] = in ? __ldcg(p.part_ml + part * kBM + lrow) : make_float2(-INFINITY, 0.f);
+      v[e] = in ? __ldcg(p.part + (part * 16 + octet) * kBM + lrow) : make_uint4(0, 0, 0, 0);
     }
     float mx = M;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, ml[e].x);
+    for (int e = 0; e < kAhead; ++e) mx = fmaxf(mx, ml[e].x);
     const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mx);
     M = mx;
     L *= keep;
-    a.x *= keep;
-    a.y *= keep;
-    a.z *= keep;
-    a.w *= keep;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - mx);
-      L = fmaf(f, ml[e].y, L);
-      a.x = fmaf(f, v[e].x, a.x);
-      a.y = fmaf(f, v[e].y, a.y);
-      a.z = fmaf(f, v[e].z, a.z);
-      a.w = fmaf(f, v[e].w, a.w);
+    for (int i = 0; i < 8; ++i) a[i] *= keep;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const float w = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - mx) * ml[e].y;
+      const uint32_t h[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+      L += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = f16x2_to_f32(h[i]);
+        a[2 * i] = fmaf(w, f.x, a[2 * i]);
+        a[2 * i + 1] = fmaf(w, f.y, a[2 * i + 1]);
+      }
     }
   }
-  if (slice == 1) {
-    s_o[threadIdx.x - 128] = a;
-    s_ml[threadIdx.x - 128] = make_float2(M, L);
+  const int t = threadIdx.x & 127;
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_o[i][t] = a[i];
+    s_ml[t] = make_float2(M, L);
   }
   __syncthreads();
-  if (slice == 1) return;
-  const float4 b = s_o[threadIdx.x];
-  const float2 ml = s_ml[threadIdx.x];
+  if (half || qrow >= p.G * p.rows) return;
+  const float2 ml = s_ml[t];
   const float mx = fmaxf(M, ml.x);
   const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - mx), f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
   L = f0 * L + f1 * ml.y;
+  const int r = rh / p.Hkv, head = rh % p.Hkv;
   const float inv = L == 0.f ? 0.f : p.req[r].v_global / L;
-  const int qrow = qrow0 + row;
-  if (qrow >= p.G * p.rows) return;
-  const size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + g / p.n_qt * p.G + qrow / p.rows) * kD + quad * 4;
-  *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2((f0 * a.x + f1 * b.x) * inv, (f0 * a.y + f1 * b.y) * inv),
-                                                     pack_bf16x2((f0 * a.z + f1 * b.z) * inv, (f0 * a.w + f1 * b.w) * inv));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = pack_bf16x2((f0 * a[2 * i] + f1 * s_o[2 * i][t]) * inv, (f0 * a[2 * i + 1] + f1 * s_o[2 * i + 1][t]) * inv);
+  const size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + head * p.G + qrow / p.rows) * kD + octet * 8;
+  *reinterpret_cast<uint4*>(p.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+size_t wide_group_bytes(int B, int Hkv, int n_qp) { return (static_cast<size_t>(B) * Hkv * n_qp * sizeof(int2) + 255) / 256 * 256; }
+size_t wide_parts() { return 4 * static_cast<size_t>(glance::num_sms()); }  // 128 rows each
 
 bool few_rows(int rows, int G) { return rows * G <= kFewRows; }
 
@@ -1252,7 +1405,8 @@ size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
   const int Hkv = kv[0].n_kv_heads;
   if (few_rows(rows, Hq / Hkv))
     return few_counter_bytes(B, Hkv) + static_cast<size_t>(few_grid(B, Hkv)) * kFewRows * (kD * 4 + sizeof(float2));
-  return 2 * static_cast<size_t>(glance::num_sms()) * kBM * (kD * 4 + sizeof(float2));
+  const int n_qp = (rows * (Hq / Hkv) + 2 * kBM - 1) / (2 * kBM);
+  return wide_group_bytes(B, Hkv, n_qp) + wide_parts() * kBM * (kD * 2 + sizeof(float2));
 }
 
 }  // namespace
@@ -1316,6 +1470,11 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
   p.G = G;
   p.W = (rows + 63) / 64;
   p.n_qt = (G * rows + kBM - 1) / kBM;
+  p.n_qp = (p.n_qt + 1) / 2;
+  p.part_o = nullptr;
+  p.part = nullptr;
+  p.group = nullptr;
+  p.count = nullptr;
   p.scale_log2 = scale * kLog2e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -1339,9 +1498,10 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     e = cudaLaunchKernelEx(&cfg, kv4_attention_few_kernel, p);
   } else {
     const int grid = glance::num_sms();
-    p.count = nullptr;
-    p.part_o = reinterpret_cast<float4*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(grid) * kBM * 32);
+    char* ws = static_cast<char*>(workspace);
+    p.group = reinterpret_cast<int2*>(ws);
+    p.part = reinterpret_cast<uint4*>(ws + wide_group_bytes(B, Hkv, p.n_qp));
+    p.part_ml = reinterpret_cast<float2*>(p.part + wide_parts() * kBM * 16);
     e = glance::ensure_smem(reinterpret_cast<const void*>(kv4_attention_wide_kernel), kWideSmem);
     if (e != cudaSuccess) return glance::cuda_fail(e, who);
     cfg.gridDim = dim3(grid);
@@ -1352,7 +1512,7 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     cfg.gridDim = dim3(static_cast<unsigned>(B) * Hkv * p.n_qt * (kBM / kMergeRows));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, kv4_attention_merge_kernel, p, grid);
+    e = cudaLaunchKernelEx(&cfg, kv4_attention_merge_kernel, p);
   }
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
   return GLANCE_OK;
