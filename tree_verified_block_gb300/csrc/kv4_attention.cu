@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ms->q_ready[x], 128);
       mbar_init(&ms->s_full[x], 1);
-      mbar_init(&ms->p_ready[x], 128);
+      mbar_init(&ms->p_ready[x], 4);
       mbar_init(&ms->o_done[x], 1);
     }
     mbar_init(&ms->drain, 1);
@@ -905,36 +905,43 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         const Run run(s, *p.req[s.r].t_len + p.rows);
         const bool pair = 2 * (s.g % p.n_qp) + 1 < p.n_qt;
         const int items = pair ? 2 * run.tiles : run.tiles;
-        // item k: slot k & 1, tile k / 2 of a pair or tile k
+        // Item k: slot k & 1, tile k / 2 of a pair or tile k. A K or V tile is
+        // waited for by its first item and let go by its last one. Tiles are
+        // waited for before the weights, which come last.
+        const auto tile_of = [&](int k) { return pair ? k >> 1 : k; };
+        const auto wait_tile = [&](uint64_t* full, int k) {
+          const int t = t0 + tile_of(k);
+          return (pair && (k & 1)) || wide_wait(&full[t & 1], (t >> 1) & 1, ms);
+        };
         const auto issue_s = [&](int k) {
-          const int x = k & 1, j = pair ? k >> 1 : k, t = t0 + j, st = t & 1;
-          if (!wide_wait(&ms->k_full[st], (t >> 1) & 1, ms)) return false;
-          tc_fence_after();
+          const int x = k & 1, j = tile_of(k), st = (t0 + j) & 1;
           if (elect_one()) {
-            issue_qk(tmem + x * 128, q_desc + (pair ? x * kTileStep : 0), k_desc + st * kTileStep,
-                     idesc_f16(run.cols(j), false));
+            issue_qk(tmem + x * 128, q_desc + (pair ? x * kTileStep : 0), k_desc + st * kTileStep, idesc_f16(run.cols(j), false));
             mma_commit(&ms->s_full[x]);
             if (!pair || x) mma_commit(&ms->k_empty[st]);
           }
           __syncwarp();
-          return true;
         };
         for (int x = 0; x < (pair ? 2 : 1) && good; ++x) good = wide_wait(&ms->q_ready[x], n_q[x]++ & 1, ms);
-        good = good && issue_s(0) && (items < 2 || issue_s(1));
+        for (int k = 0; k < 2 && k < items && good; ++k) {
+          good = wait_tile(ms->k_full, k);
+          tc_fence_after();
+          if (good) issue_s(k);
+        }
         for (int k = 0; good && k < items; ++k) {
-          const int x = k & 1, j = pair ? k >> 1 : k, t = t0 + j, st = t & 1;
-          good = wide_wait(&ms->p_ready[x], n_p[x]++ & 1, ms) && wide_wait(&ms->v_full[st], (t >> 1) & 1, ms);
+          const int x = k & 1, j = tile_of(k), st = (t0 + j) & 1;
+          good = wait_tile(ms->v_full, k) && (k + 2 >= items || wait_tile(ms->k_full, k + 2)) &&
+                 wide_wait(&ms->p_ready[x], n_p[x]++ & 1, ms);
           if (!good) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_pv(tmem + 256 + x * 128, tmem + x * 128, v_desc + st * kTileStep, idesc_f16(kD, true),
-                     run.cols(j) / 16, k < 2);
+            issue_pv(tmem + 256 + x * 128, tmem + x * 128, v_desc + st * kTileStep, idesc_f16(kD, true), run.cols(j) / 16, k < 2);
             if (!pair || x) mma_commit(&ms->v_empty[st]);
             if (k + 2 >= items) mma_commit(&ms->o_done[x]);
           }
           __syncwarp();
           // the slot's next S takes the columns of these weights: products run in the order of their issue
-          if (k + 2 < items) good = issue_s(k + 2);
+          if (k + 2 < items) issue_s(k + 2);
         }
         t0 += run.tiles;
       } while (good && next_segment(p, pl, s));
@@ -1156,17 +1163,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
             uint32_t sr[64];
             tmem_row64(tS + 64 * h, sr);
             const bool both = 2 * h + 1 < nc;  // the product has the second 32 slots
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[8];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (c == 0 || both) {
+            for (int i = 0; i < 8; ++i) mx[i] = max3f(__uint_as_float(sr[i]), __uint_as_float(sr[8 + i]), __uint_as_float(sr[16 + i]));
 #pragma unroll
-                for (int e = 32 * c; e < 32 * c + 32; e += 8)
+            for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], __uint_as_float(sr[24 + i]));
+            if (both) {
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    mx[i] = max3f(mx[i], __uint_as_float(sr[e + 2 * i]), __uint_as_float(sr[e + 2 * i + 1]));
+              for (int i = 0; i < 8; ++i) {
+                mx[i] = max3f(mx[i], __uint_as_float(sr[32 + i]), __uint_as_float(sr[40 + i]));
+                mx[i] = max3f(mx[i], __uint_as_float(sr[48 + i]), __uint_as_float(sr[56 + i]));
               }
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            }
+            const float mt = fmaxf(max3f(mx[0], mx[1], mx[2]), max3f(max3f(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sc;
             // the running maximum moves when some row of the warp grew by 8 (log2):
             // a stale one keeps the weights below 2^8 and cancels between O and l
             if (__any_sync(0xffffffffu, mt > m + 8.f)) {
@@ -1227,7 +1236,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           }
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&ms->p_ready[x]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->p_ready[x]);
         }
         if (!ok) break;
         // ------------------------------------------------ the segment's output
