@@ -523,8 +523,8 @@ size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv 
 //   warp 0        S = Q K^T (both from shared memory) and O += P V (P from
 //                 tensor memory, over the columns of its S)
 //   warps 4..7, 8..11  softmax of slot 0 and 1, one thread per query row: mask,
-//                 running maximum, weights as f16 pairs; Q as f16 scaled per
-//                 row at a segment's start; output at its end
+//                 running maximum, weights as f16 pairs; Q at a segment's start;
+//                 output at its end
 //
 // Tiles are 128 query rows (head, packed row) x 128 slots. Two neighbouring
 // query tiles of a kv head go to the two slots and share every K and V tile
@@ -533,9 +533,10 @@ size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv 
 //
 // Work: the slots of every (request, kv head, query tile pair) in units of 32.
 // Where each such group can be cut into equal parts that fill the grid, a
-// block has one part; else the list of all units is cut into equal runs and a
-// block's run may cross groups (a "segment" is its part in one group). The
-// lengths are read on the device. A group that one block has whole is written
+// block has one part; else the list of all groups is cut into equal runs and a
+// block's run may cross groups (a "segment" is its part in one group). In that
+// list a group counts kLead units more than it has, what starting and ending a
+// segment takes. The lengths are read on the device. A group that one block has whole is written
 // out there; the others' parts are merged by a second kernel.
 
 constexpr int kWideThreads = 512;
@@ -555,12 +556,15 @@ constexpr uint32_t kWideMisc = 6144;
 constexpr uint32_t kWideSmem = 1024 + kOffMisc + kWideMisc;
 static_assert(kWideSmem <= 227 * 1024, "shared memory");
 constexpr int kMinUnits = 4;  // one tile
+constexpr int kLead = 8;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 struct WidePlan {
+  int T[kMaxB];
   int units[kMaxB];       // of one group of request r; 0: no room, no output
-  long long base[kMaxB];  // units of all groups before request r
-  long long total;
+  long long base[kMaxB];  // length of the list before request r's groups
+  long long total;        // of the whole list
+  int runs;               // blocks that the list is cut for: none gets less than a tile and its lead
   int tau;                // > 0: every group is cut into parts of tau units
   int blocks0[kMaxB];     // tau > 0: blocks before request r's
 };
@@ -568,7 +572,7 @@ struct WidePlan {
 // A block's part in one group: units [a, a + n) of group g of request r.
 struct Segment {
   int r, g, a, n;
-  int left;   // units of the run after this segment
+  int left;   // length of the run after this segment
   int index;  // of the block's segments
 };
 
@@ -584,61 +588,94 @@ struct WideMisc {
 };
 static_assert(sizeof(WideMisc) <= kWideMisc, "misc block");
 
+// a / b for a run's arithmetic: 64-bit division only where it is needed.
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return a <= 0xFFFFFFFFll ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // The plan, by one warp; every block comes to the same one.
 __device__ __forceinline__ void wide_plan(const Params& p, WidePlan* pl, int lane, int blocks) {
-  int units = 0;
+  int units = 0, T = 0;
   if (lane < p.B) {
-    const int T = *p.req[lane].t_len;
+    T = *p.req[lane].t_len;
     if (T >= 0 && T <= p.req[lane].t_cap - p.rows) units = (T + p.rows + kUnit - 1) / kUnit;
   }
   const int gpr = p.Hkv * p.n_qp;
-  long long end = static_cast<long long>(units) * gpr;
-#pragma unroll
-  for (int o = 1; o < kMaxB; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end += v;
-  }
-  const long long total = __shfl_sync(0xffffffffu, end, kMaxB - 1);
+  const int sum = __reduce_add_sync(0xffffffffu, units);
+  const int length = units > 0 ? units + kLead : 0;
+  const long long total = static_cast<long long>(__reduce_add_sync(0xffffffffu, length)) * gpr;
   const int active = __popc(__ballot_sync(0xffffffffu, units > 0));
   const int per_group = blocks / gpr;
+  const int runs = static_cast<int>(min(static_cast<long long>(blocks), max(1ll, div_small(total, kMinUnits + kLead))));
   int tau = 0;
   if (per_group >= active && active > 0) {
-    int lo = kMinUnits, hi = max(kMinUnits, __reduce_max_sync(0xffffffffu, units));
+    // the least tau at which the groups' parts fit the grid: not under the mean,
+    // and at hi every request has one part
+    int lo = max(kMinUnits, (sum + per_group - 1) / per_group), hi = max(lo, __reduce_max_sync(0xffffffffu, units));
+    int mid = lo;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
       if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_group)
         hi = mid;
       else
         lo = mid + 1;
+      mid = (lo + hi) >> 1;
     }
-    // a run that crosses groups pays about kCrossUnits for each crossing
-    constexpr int kCrossUnits = 10;
-    if (lo <= total / blocks + kCrossUnits) tau = lo;
+    if (lo <= div_small(total, runs)) tau = lo;
   }
   const int n = tau ? (units + tau - 1) / tau * gpr : 0;
-  int nb = n;
-#pragma unroll
+  int before = length, nb = n;  // inclusive scans over the requests
+#pragma unroll 1
   for (int o = 1; o < kMaxB; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, nb, o);
-    if (lane >= o) nb += v;
+    const int u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_up_sync(0xffffffffu, nb, o);
+    if (lane >= o) {
+      before += u;
+      nb += v;
+    }
   }
   if (lane < kMaxB) {
+    pl->T[lane] = T;
     pl->units[lane] = units;
-    pl->base[lane] = end - static_cast<long long>(units) * gpr;
+    pl->base[lane] = static_cast<long long>(before - length) * gpr;
     pl->blocks0[lane] = nb - n;
   }
   if (lane == 0) {
     pl->total = total;
+    pl->runs = runs;
     pl->tau = tau;
   }
 }
 
 // First unit of block b's run (runs that may cross groups).
 __device__ __forceinline__ long long run_start(long long total, int b, int blocks) {
-  return total / blocks * b + total % blocks * b / blocks;
+  const long long q = div_small(total, blocks);
+  return q * b + div_small((total - q * blocks) * b, blocks);
 }
 
-__device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& pl, int b, int blocks, Segment& s) {
+__device__ __forceinline__ void step_group(const Params& p, const WidePlan& pl, Segment& s) {
+  if (++s.g == p.Hkv * p.n_qp) {
+    s.g = 0;
+    do ++s.r;
+    while (pl.units[s.r] == 0);
+  }
+}
+// The run's part from place `at` of the current group's stretch on, or of the
+// next group that it has units of.
+__device__ __forceinline__ bool take_segment(const Params& p, const WidePlan& pl, Segment& s, int at) {
+  for (;;) {
+    const int take = min(s.left, pl.units[s.r] + kLead - at), end = at + take - kLead;
+    s.left -= take;
+    s.a = max(at - kLead, 0);
+    s.n = end - s.a;
+    if (s.n > 0) {
+      ++s.index;
+      return true;
+    }
+    if (s.left == 0) return false;
+    step_group(p, pl, s);
+    at = 0;
+  }
+}
+__device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& pl, int b, Segment& s) {
   const int gpr = p.Hkv * p.n_qp;
   s.index = 0;
   int r = 0;
@@ -657,31 +694,22 @@ __device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& p
     s.left = 0;
     return true;
   }
-  const long long x = run_start(pl.total, b, blocks);
-  const int len = static_cast<int>(run_start(pl.total, b + 1, blocks) - x);
-  if (len == 0) return false;
+  if (b >= pl.runs || pl.total == 0) return false;
+  const long long x = run_start(pl.total, b, pl.runs);
+  const int len = static_cast<int>(run_start(pl.total, b + 1, pl.runs) - x);
   while (r + 1 < p.B && x >= pl.base[r + 1]) ++r;  // requests without units share their base with the next
-  while (pl.units[r] == 0) --r;  // x lies before the end of the last request with units
   const long long in = x - pl.base[r];
+  const int length = pl.units[r] + kLead;
   s.r = r;
-  s.g = static_cast<int>(in / pl.units[r]);
-  s.a = static_cast<int>(in % pl.units[r]);
-  s.n = min(len, pl.units[r] - s.a);
-  s.left = len - s.n;
-  return true;
+  s.g = static_cast<int>(div_small(in, length));
+  s.index = -1;
+  s.left = len;
+  return take_segment(p, pl, s, static_cast<int>(in - static_cast<long long>(s.g) * length));
 }
 __device__ __forceinline__ bool next_segment(const Params& p, const WidePlan& pl, Segment& s) {
   if (s.left == 0) return false;
-  if (++s.g == p.Hkv * p.n_qp) {
-    s.g = 0;
-    do ++s.r;
-    while (pl.units[s.r] == 0);
-  }
-  s.a = 0;
-  s.n = min(s.left, pl.units[s.r]);
-  s.left -= s.n;
-  ++s.index;
-  return true;
+  step_group(p, pl, s);
+  return take_segment(p, pl, s, 0);
 }
 
 // Slots of a segment: [k0, k1); its tiles start at k0, k0 + 128, ...
@@ -738,11 +766,10 @@ __device__ __forceinline__ unsigned long long add_f2(unsigned long long a, unsig
   return d;
 }
 
-// kind::f16 with f16 A and B, fp32 accumulator, 128 rows, N columns; B is
-// K-major (K tile) or MN-major (V tile).
-__host__ __device__ constexpr uint32_t idesc_f16(int N, bool b_mn_major) {
-  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(kBM >> 4) << 24);
+// kind::f16 with f16 A and B, fp32 accumulator, 128 rows, N columns, B MN-major
+// (the V tile).
+__host__ __device__ constexpr uint32_t idesc_f16(int N) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -784,46 +811,55 @@ __device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W
 }
 
 // A thread's share of a tile: rows row + 8i (i = 0..3) of the 128, dims 32q ..
-// 32q + 31 (16 bytes of codes, two scales). A warp has 32 rows; lane = 4 (row
-// mod 8) + q, so that eight lanes read 128 consecutive bytes of codes.
-struct Raw {
-  uint4 codes[4];
-  uint32_t scales[4];
-};
-__device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, const unsigned char* scales, int row, int q,
-                                         int left) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x.codes[i] = *reinterpret_cast<const uint4*>(codes + (row + 8 * i) * 64 + q * 16);
-    x.scales[i] = *reinterpret_cast<const uint16_t*>(scales + (row + 8 * i) * 8 + q * 2);
-    if (left < kBN && row + 8 * i >= left) {  // behind the run: zero, whatever is there
-      x.codes[i] = make_uint4(0, 0, 0, 0);
-      x.scales[i] = 0;
-    }
-  }
-}
-
-// ... as f16 into the tile: row r's 16-byte chunk c of a half (64 dims) is at
-// r * 128 + 16 (c ^ (r & 7)). Lanes of the upper half take their four chunks
-// in the order 2, 3, 0, 1: eight lanes (two rows, four q) then write eight
-// different 16-byte columns of the 128-byte rows, and no bank twice.
-__device__ __forceinline__ void store_tile(const Raw& x, unsigned char* tile, int row, int q) {
-  unsigned char* base = tile + (q >> 1) * kHalfBytes + row * 128;
+// 32q + 31 (16 bytes of codes, two scales) of each, as 16-bit values into the
+// tile: row r's 16-byte chunk c of a half (64 dims) is at r * 128 + 16 (c ^ (r
+// & 7)). lane = 4 (row mod 8) + q, so that eight lanes read 128 consecutive
+// bytes of codes; lanes of the upper half take their four chunks in the order
+// 2, 3, 0, 1, so that eight lanes (two rows, four q) write eight different
+// 16-byte columns: no bank twice, either way. Rows from `left` on are zero.
+// K becomes bf16, the type of q; V f16, the type of the weights: the products
+// are of one type each, and code * scale is exact in both.
+// The loop is not unrolled far: a block runs it a few times on a short prefix,
+// and fetching unrolled code costs more than running it.
+template <bool kIsV>
+__device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned char* tile, int row, int q, int left, bool tree,
+                                             int lane) {
   const bool up = q >= 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t s = scales2_to_f16(x.scales[i]);
-    const uint32_t s0 = prmt(s, s, up ? 0x3232 : 0x1010), s1 = prmt(s, s, up ? 0x1010 : 0x3232);
-    const uint32_t w[4] = {up ? x.codes[i].z : x.codes[i].x, up ? x.codes[i].w : x.codes[i].y,
-                           up ? x.codes[i].x : x.codes[i].z, up ? x.codes[i].y : x.codes[i].w};
+#pragma unroll 2
+  for (int i = 0; i < 4; ++i, row += 8) {
+    uint4 c = *reinterpret_cast<const uint4*>(raw + row * 64 + q * 16);
+    uint32_t sb = *reinterpret_cast<const uint16_t*>(raw + kRawCodes + row * 8 + q * 2);
+    bool keep = row < left;
+    if (kIsV && tree) {
+      // a V row with a scale that is not a number is left out: 0 * NaN would
+      // reach the rows that do not see it (the softmax marks the scores of
+      // those that do)
+      const bool nan = (sb & 0x7Fu) == 0x7Fu || (sb & 0x7F00u) == 0x7F00u;
+      const uint32_t row_nan = __ballot_sync(0xffffffffu, nan) >> (lane & 28) & 15u;  // every lane votes
+      keep = keep && row_nan == 0u;
+    }
+    if (!keep) {  // zero, whatever is there
+      c = make_uint4(0, 0, 0, 0);
+      sb = 0;
+    }
+    uint32_t s = scales2_to_f16(sb);
+    uint32_t s0 = prmt(s, s, up ? 0x3232 : 0x1010), s1 = prmt(s, s, up ? 0x1010 : 0x3232);
+    if (!kIsV) {  // times 2^112, as bf16
+      const float2 f0 = f16x2_to_f32(s0), f1 = f16x2_to_f32(s1);
+      s0 = pack_bf16x2(f0.x * 0x1p112f, f0.x * 0x1p112f);
+      s1 = pack_bf16x2(f1.x * 0x1p112f, f1.x * 0x1p112f);
+    }
+    const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+    unsigned char* dst = tile + (q >> 1) * kHalfBytes + row * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t h[4];
       codes8_to_f16(w[j], h);
       const uint32_t sj = j < 2 ? s0 : s1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = kIsV ? mul_f16x2(h[e], sj) : mul_bf16x2(f16_codes_to_bf16(h[e]), sj);
       const int chunk = ((q & 1) * 4 + (j ^ (q & 2))) ^ (row & 7);
-      *reinterpret_cast<uint4*>(base + i * 8 * 128 + chunk * 16) =
-          make_uint4(mul_f16x2(h[0], sj), mul_f16x2(h[1], sj), mul_f16x2(h[2], sj), mul_f16x2(h[3], sj));
+      *reinterpret_cast<uint4*>(dst + chunk * 16) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
 }
@@ -879,7 +915,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
   if (warp == 3) {
     wide_plan(p, &ms->plan, lane, blocks);
     __syncwarp();
-    if (lane == 0) ms->any = first_segment(p, ms->plan, blockIdx.x, blocks, ms->seg);
+    if (lane == 0) ms->any = first_segment(p, ms->plan, blockIdx.x, ms->seg);
   }
   tc_fence_before();
   __syncthreads();
@@ -902,7 +938,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       uint32_t n_p[2] = {0, 0};
       bool good = true;
       do {
-        const Run run(s, *p.req[s.r].t_len + p.rows);
+        const Run run(s, pl.T[s.r] + p.rows);
         const bool pair = 2 * (s.g % p.n_qp) + 1 < p.n_qt;
         const int items = pair ? 2 * run.tiles : run.tiles;
         // Item k: slot k & 1, tile k / 2 of a pair or tile k. A K or V tile is
@@ -916,7 +952,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         const auto issue_s = [&](int k) {
           const int x = k & 1, j = tile_of(k), st = (t0 + j) & 1;
           if (elect_one()) {
-            issue_qk(tmem + x * 128, q_desc + (pair ? x * kTileStep : 0), k_desc + st * kTileStep, idesc_f16(run.cols(j), false));
+            issue_qk(tmem + x * 128, q_desc + (pair ? x * kTileStep : 0), k_desc + st * kTileStep, idesc_bf16_f32(kBM, run.cols(j), false, false));
             mma_commit(&ms->s_full[x]);
             if (!pair || x) mma_commit(&ms->k_empty[st]);
           }
@@ -935,7 +971,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           if (!good) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_pv(tmem + 256 + x * 128, tmem + x * 128, v_desc + st * kTileStep, idesc_f16(kD, true), run.cols(j) / 16, k < 2);
+            issue_pv(tmem + 256 + x * 128, tmem + x * 128, v_desc + st * kTileStep, idesc_f16(kD), run.cols(j) / 16, k < 2);
             if (!pair || x) mma_commit(&ms->v_empty[st]);
             if (k + 2 >= items) mma_commit(&ms->o_done[x]);
           }
@@ -953,7 +989,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       bool good = true;
       do {
         const Request& rq = p.req[s.r];
-        const Run run(s, *rq.t_len + p.rows);
+        const Run run(s, pl.T[s.r] + p.rows);
         const long long head0 = static_cast<long long>(s.g / p.n_qp) * rq.head_stride;
         for (int e = 0; e < 2 * run.tiles && good; ++e, ++h) {
           const int st = h % kRawStages, key0 = run.key0(e >> 1);
@@ -991,9 +1027,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           if (pl.tau) {
             n = (pl.units[s.r] + pl.tau - 1) / pl.tau;
           } else {
-            const long long end = pl.base[s.r] + (s.g + 1ll) * pl.units[s.r];
+            const long long end = pl.base[s.r] + (s.g + 1ll) * (pl.units[s.r] + kLead);
             for (;; n += 32) {
-              const unsigned past = __ballot_sync(0xffffffffu, run_start(pl.total, blockIdx.x + n + lane, blocks) >= end);
+              const unsigned past = __ballot_sync(0xffffffffu, run_start(pl.total, blockIdx.x + n + lane, pl.runs) >= end);
               if (past) {
                 n += __ffs(past) - 1;
                 break;
@@ -1019,36 +1055,25 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       int h = 0;
       bool good = true;
       do {
-        const int T = *p.req[s.r].t_len;
+        const int T = pl.T[s.r];
         const Run run(s, T + p.rows);
         for (int e = 0; e < 2 * run.tiles; ++e, ++h) {
           const int rs = h % kRawStages, t = h >> 1, st = t & 1, is_v = h & 1, key0 = run.key0(e >> 1);
           good = wide_wait(&ms->raw_full[rs], (h / kRawStages) & 1, ms);
           if (!good) break;
-          const unsigned char* src = smem + kOffRaw + rs * kRawBytes;
-          Raw x;
-          load_raw(x, src, src + kRawCodes, row, q, run.k1 - key0);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms->raw_empty[rs]);
-          if (is_v && key0 + kBN > T) {
-            // a V row with a scale that is not a number is left out: 0 * NaN
-            // would reach the rows that do not see it (the softmax marks the
-            // scores of those that do)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool nan = (x.scales[i] & 0x7Fu) == 0x7Fu || (x.scales[i] & 0x7F00u) == 0x7F00u;
-              if (__ballot_sync(0xffffffffu, nan) >> (lane & 28) & 15u) {
-                x.codes[i] = make_uint4(0, 0, 0, 0);
-                x.scales[i] = 0;
-              }
-            }
-          }
           if (t >= kStages) good = wide_wait(is_v ? &ms->v_empty[st] : &ms->k_empty[st], ((t >> 1) - 1) & 1, ms);
           if (!good) break;
-          store_tile(x, smem + (is_v ? kOffV : kOffK) + st * kTileBytes, row, q);
+          const unsigned char* src = smem + kOffRaw + rs * kRawBytes;
+          if (is_v)
+            convert_tile<true>(src, smem + kOffV + st * kTileBytes, row, q, run.k1 - key0, key0 + kBN > T, lane);
+          else
+            convert_tile<false>(src, smem + kOffK + st * kTileBytes, row, q, run.k1 - key0, false, lane);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
+          if (lane == 0) {
+            mbar_arrive(&ms->raw_empty[rs]);
+            mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
+          }
         }
       } while (good && next_segment(p, pl, s));
       if (!good) wide_fail(ms);
@@ -1066,7 +1091,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       Segment s = ms->seg;
       do {
         const Request& rq = p.req[s.r];
-        const int T = *rq.t_len;
+        const int T = pl.T[s.r];
         const Run run(s, T + p.rows);
         const int head = s.g / p.n_qp, qt0 = 2 * (s.g % p.n_qp);
         const bool pair = qt0 + 1 < p.n_qt;
@@ -1079,38 +1104,31 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           prow = valid ? qrow % p.rows : 0;
           return ((static_cast<size_t>(s.r) * p.rows + prow) * p.Hq + head * p.G + (valid ? qrow / p.rows : 0)) * kD;
         };
-        float sc;
-        {
-          bool valid;
-          int prow;
-          const size_t q_at = query(valid, prow);
-          // the row as f16; the products that read the previous segment's Q are done
-          uint4 v[16];
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + q_at);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = valid ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
-          uint32_t top = 0;  // the largest magnitude's bits: in the order of the absolute values
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            top = max(max(max(v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu) >> 16, max(v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu) >> 16),
-                      max(max(max(v[e].x & 0x7FFFu, v[e].y & 0x7FFFu), max(v[e].z & 0x7FFFu, v[e].w & 0x7FFFu)), top));
-          const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
-          const float qf = query_factor(amax);
-          sc = score_factor(amax, qf, p.scale_log2, rq.k_global);
-          if (pair || !x) {
-            unsigned char* dst = smem + (pair ? x * kTileBytes : 0) + lrow * 128;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-              uint32_t f[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                f[i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
-              *reinterpret_cast<uint4*>(dst + (e >> 3) * kHalfBytes + (((e & 7) ^ (lrow & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+        // score factor, in log2; at least the least normal number: a score of -infinity stays one
+        const float sc = fmaxf(p.scale_log2 * rq.k_global, 1.17549435e-38f);
+        if (pair || !x) {
+          // Q into its tile, 16 bytes at a time (thread = chunk, 16 to a row; the
+          // products that read the previous segment's are done); rows behind the last are zero
+          const int th = (warp & 3) * 32 + lane, c = th & 15;
+          unsigned char* dst = smem + (pair ? x * kTileBytes : 0) + (c >> 3) * kHalfBytes;
+          int i = th >> 4, qr = (pair ? qt0 + x : qt0) * kBM + i;
+          int h = qr / p.rows, pr = qr - h * p.rows;  // query head of the group, packed row
+          const __nv_bfloat16* src = p.q + (static_cast<size_t>(s.r) * p.rows * p.Hq + head * p.G) * kD + c * 8;
+          dst += i * 128 + (((c & 7) ^ (i & 7)) << 4);  // i steps by 8: the swizzle stays
+#pragma unroll 2
+          for (; i < kBM; i += 8, qr += 8, pr += 8, dst += 8 * 128) {
+            while (pr >= p.rows) {
+              pr -= p.rows;
+              ++h;
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&ms->q_ready[x]);
+            if (qr < R)
+              copy16_async(dst, src + (static_cast<size_t>(pr) * p.Hq + h) * kD);
+            else
+              *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
           }
+          copy_async_wait();
+          fence_proxy_async_smem();
+          mbar_arrive(&ms->q_ready[x]);
         }
         float m = -INFINITY, l = 0.f;
         const int step = pair ? 1 : 2, j0 = pair ? 0 : x;
@@ -1239,7 +1257,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms->p_ready[x]);
         }
-        if (!ok) break;
+        if (!ok && pair) break;  // slots that share a query tile leave together, at the barrier below
         // ------------------------------------------------ the segment's output
         const bool whole = s.n == pl.units[s.r];
         bool valid;
@@ -1274,7 +1292,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           // both slots have this query tile: slot x writes dims 64x .. 64x + 63
           float2(*ml)[kBM] = ms->ml[s.index & 1];
           ml[x][lrow] = make_float2(m, l);
-          ok = wide_wait(&ms->o_done[0], n_o[0]++ & 1, ms) && (run.tiles < 2 || wide_wait(&ms->o_done[1], n_o[1]++ & 1, ms));
+          ok = ok && wide_wait(&ms->o_done[0], n_o[0]++ & 1, ms) && (run.tiles < 2 || wide_wait(&ms->o_done[1], n_o[1]++ & 1, ms));
           ok = !named_bar_or(1, 256, !ok);
           if (!ok) break;
           tc_fence_after();
@@ -1331,16 +1349,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
 }
 
 // The parts of the groups that several blocks had. Block (query tile, 8 rows):
-// thread = (half of the parts, octet of dims, row).
-constexpr int kMergeThreads = 256;
+// thread = (slice of the parts, octet of dims, row); five parts at a time. The
+// more blocks a group can have, the more slices share them.
 constexpr int kMergeRows = 8;
 
-__global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(const __grid_constant__ Params p) {
-  __shared__ float s_o[8][128];
-  __shared__ float2 s_ml[128];
+template <int kSlices>
+__global__ void __launch_bounds__(128 * kSlices) kv4_attention_merge_kernel(const __grid_constant__ Params p) {
+  __shared__ float s_o[kSlices][8][128];
+  __shared__ float2 s_ml[kSlices][128];
   const int tile = blockIdx.x / (kBM / kMergeRows), rows0 = blockIdx.x % (kBM / kMergeRows) * kMergeRows;
   const int qt = tile % p.n_qt, rh = tile / p.n_qt;  // request * Hkv + head
-  const int row = threadIdx.x & 7, octet = threadIdx.x >> 3 & 15, half = threadIdx.x >> 7;
+  const int t = threadIdx.x & 127, row = t & 7, octet = t >> 3, slice = threadIdx.x >> 7;
   const int lrow = rows0 + row, qrow = qt * kBM + lrow;
   pdl_wait_prior();  // in every block: this kernel ends after the one before it
   pdl_launch_dependents();
@@ -1350,9 +1369,10 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(cons
   if (n < 2) return;  // written whole, or no output
   // the first block's part is gi.x (its first or last segment), the others' their first segments
   const auto part_of = [&](int b) { return 2 * static_cast<size_t>(b ? (gi.x & ~1) + 2 * b : gi.x) + (qt & 1); };
-  const int per = (n + 1) / 2, b0 = half * per, b1 = min(n, b0 + per);
+  const int per = (n + kSlices - 1) / kSlices, b0 = slice * per, b1 = min(n, b0 + per);
   float M = -INFINITY, L = 0.f, a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  constexpr int kAhead = 10;
+  constexpr int kAhead = 5;
+#pragma unroll 1
   for (int s0 = b0; s0 < b1; s0 += kAhead) {
     uint4 v[kAhead];
     float2 ml[kAhead];
@@ -1384,24 +1404,36 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attention_merge_kernel(cons
       }
     }
   }
-  const int t = threadIdx.x & 127;
-  if (half) {
+  if (kSlices > 1) {
+    if (slice) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_o[i][t] = a[i];
-    s_ml[t] = make_float2(M, L);
+      for (int i = 0; i < 8; ++i) s_o[slice][i][t] = a[i];
+      s_ml[slice][t] = make_float2(M, L);
+    }
+    __syncthreads();
+    if (slice) return;
+    float mx = M;
+#pragma unroll
+    for (int y = 1; y < kSlices; ++y) mx = fmaxf(mx, s_ml[y][t].x);
+    const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+    L *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= f0;
+#pragma unroll
+    for (int y = 1; y < kSlices; ++y) {
+      const float2 ml = s_ml[y][t];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+      L = fmaf(f, ml.y, L);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = fmaf(f, s_o[y][i][t], a[i]);
+    }
   }
-  __syncthreads();
-  if (half || qrow >= p.G * p.rows) return;
-  const float2 ml = s_ml[t];
-  const float mx = fmaxf(M, ml.x);
-  const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - mx), f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-  L = f0 * L + f1 * ml.y;
+  if (qrow >= p.G * p.rows) return;
   const int r = rh / p.Hkv, head = rh % p.Hkv;
   const float inv = L == 0.f ? 0.f : p.req[r].v_global / L;
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = pack_bf16x2((f0 * a[2 * i] + f1 * s_o[2 * i][t]) * inv, (f0 * a[2 * i + 1] + f1 * s_o[2 * i + 1][t]) * inv);
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(a[2 * i] * inv, a[2 * i + 1] * inv);
   const size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + head * p.G + qrow / p.rows) * kD + octet * 8;
   *reinterpret_cast<uint4*>(p.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -1520,9 +1552,14 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     e = cudaLaunchKernelEx(&cfg, kv4_attention_wide_kernel, p);
     if (e != cudaSuccess) return glance::cuda_fail(e, who);
     cfg.gridDim = dim3(static_cast<unsigned>(B) * Hkv * p.n_qt * (kBM / kMergeRows));
-    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, kv4_attention_merge_kernel, p);
+    // blocks per group, where every group has as many
+    const int parts = grid / (B * Hkv * p.n_qp);
+    const int slices = parts > 10 ? 4 : parts > 5 ? 2 : 1;
+    cfg.blockDim = dim3(128 * slices);
+    e = cudaLaunchKernelEx(&cfg, slices == 4   ? kv4_attention_merge_kernel<4>
+                                 : slices == 2 ? kv4_attention_merge_kernel<2>
+                                               : kv4_attention_merge_kernel<1>, p);
   }
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
   return GLANCE_OK;
