@@ -811,55 +811,55 @@ __device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W
 }
 
 // A thread's share of a tile: rows row + 8i (i = 0..3) of the 128, dims 32q ..
-// 32q + 31 (16 bytes of codes, two scales) of each, as 16-bit values into the
-// tile: row r's 16-byte chunk c of a half (64 dims) is at r * 128 + 16 (c ^ (r
-// & 7)). lane = 4 (row mod 8) + q, so that eight lanes read 128 consecutive
-// bytes of codes; lanes of the upper half take their four chunks in the order
-// 2, 3, 0, 1, so that eight lanes (two rows, four q) write eight different
-// 16-byte columns: no bank twice, either way. Rows from `left` on are zero.
-// K becomes bf16, the type of q; V f16, the type of the weights: the products
-// are of one type each, and code * scale is exact in both.
-// The loop is not unrolled far: a block runs it a few times on a short prefix,
-// and fetching unrolled code costs more than running it.
+// 32q + 31 (16 bytes of codes, two scales). A warp has 32 rows; lane = 4 (row
+// mod 8) + q, so that eight lanes read 128 consecutive bytes of codes.
+struct Raw {
+  uint4 codes[4];
+  uint32_t scales[4];
+};
+__device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, const unsigned char* scales, int row, int q,
+                                         int left) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.codes[i] = *reinterpret_cast<const uint4*>(codes + (row + 8 * i) * 64 + q * 16);
+    x.scales[i] = *reinterpret_cast<const uint16_t*>(scales + (row + 8 * i) * 8 + q * 2);
+    if (left < kBN && row + 8 * i >= left) {  // behind the run: zero, whatever is there
+      x.codes[i] = make_uint4(0, 0, 0, 0);
+      x.scales[i] = 0;
+    }
+  }
+}
+
+// ... as 16-bit values into the tile (K as bf16, the type of q; V as f16, the
+// type of the weights: a product has one type, and code * scale is exact in both): row r's 16-byte chunk c of a half (64 dims) is at
+// r * 128 + 16 (c ^ (r & 7)). Lanes of the upper half take their four chunks
+// in the order 2, 3, 0, 1: eight lanes (two rows, four q) then write eight
+// different 16-byte columns of the 128-byte rows, and no bank twice.
 template <bool kIsV>
-__device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned char* tile, int row, int q, int left, bool tree,
-                                             int lane) {
+__device__ __forceinline__ void store_tile(const Raw& x, unsigned char* tile, int row, int q) {
+  unsigned char* base = tile + (q >> 1) * kHalfBytes + row * 128;
   const bool up = q >= 2;
-#pragma unroll 2
-  for (int i = 0; i < 4; ++i, row += 8) {
-    uint4 c = *reinterpret_cast<const uint4*>(raw + row * 64 + q * 16);
-    uint32_t sb = *reinterpret_cast<const uint16_t*>(raw + kRawCodes + row * 8 + q * 2);
-    bool keep = row < left;
-    if (kIsV && tree) {
-      // a V row with a scale that is not a number is left out: 0 * NaN would
-      // reach the rows that do not see it (the softmax marks the scores of
-      // those that do)
-      const bool nan = (sb & 0x7Fu) == 0x7Fu || (sb & 0x7F00u) == 0x7F00u;
-      const uint32_t row_nan = __ballot_sync(0xffffffffu, nan) >> (lane & 28) & 15u;  // every lane votes
-      keep = keep && row_nan == 0u;
-    }
-    if (!keep) {  // zero, whatever is there
-      c = make_uint4(0, 0, 0, 0);
-      sb = 0;
-    }
-    uint32_t s = scales2_to_f16(sb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t s = scales2_to_f16(x.scales[i]);
     uint32_t s0 = prmt(s, s, up ? 0x3232 : 0x1010), s1 = prmt(s, s, up ? 0x1010 : 0x3232);
     if (!kIsV) {  // times 2^112, as bf16
-      const float2 f0 = f16x2_to_f32(s0), f1 = f16x2_to_f32(s1);
-      s0 = pack_bf16x2(f0.x * 0x1p112f, f0.x * 0x1p112f);
-      s1 = pack_bf16x2(f1.x * 0x1p112f, f1.x * 0x1p112f);
+      const float2 f = f16x2_to_f32(prmt(s0, s1, 0x5410));
+      s0 = pack_bf16x2(f.x * 0x1p112f, f.x * 0x1p112f);
+      s1 = pack_bf16x2(f.y * 0x1p112f, f.y * 0x1p112f);
     }
-    const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
-    unsigned char* dst = tile + (q >> 1) * kHalfBytes + row * 128;
+    const uint32_t w[4] = {up ? x.codes[i].z : x.codes[i].x, up ? x.codes[i].w : x.codes[i].y,
+                           up ? x.codes[i].x : x.codes[i].z, up ? x.codes[i].y : x.codes[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t h[4];
       codes8_to_f16(w[j], h);
       const uint32_t sj = j < 2 ? s0 : s1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = kIsV ? mul_f16x2(h[e], sj) : mul_bf16x2(f16_codes_to_bf16(h[e]), sj);
       const int chunk = ((q & 1) * 4 + (j ^ (q & 2))) ^ (row & 7);
-      *reinterpret_cast<uint4*>(dst + chunk * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(base + i * 8 * 128 + chunk * 16) =
+          kIsV ? make_uint4(mul_f16x2(h[0], sj), mul_f16x2(h[1], sj), mul_f16x2(h[2], sj), mul_f16x2(h[3], sj))
+               : make_uint4(mul_bf16x2(f16_codes_to_bf16(h[0]), sj), mul_bf16x2(f16_codes_to_bf16(h[1]), sj),
+                            mul_bf16x2(f16_codes_to_bf16(h[2]), sj), mul_bf16x2(f16_codes_to_bf16(h[3]), sj));
     }
   }
 }
@@ -1061,19 +1061,33 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           const int rs = h % kRawStages, t = h >> 1, st = t & 1, is_v = h & 1, key0 = run.key0(e >> 1);
           good = wide_wait(&ms->raw_full[rs], (h / kRawStages) & 1, ms);
           if (!good) break;
+          const unsigned char* src = smem + kOffRaw + rs * kRawBytes;
+          Raw x;
+          load_raw(x, src, src + kRawCodes, row, q, run.k1 - key0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->raw_empty[rs]);
+          if (is_v && key0 + kBN > T) {
+            // a V row with a scale that is not a number is left out: 0 * NaN
+            // would reach the rows that do not see it (the softmax marks the
+            // scores of those that do)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool nan = (x.scales[i] & 0x7Fu) == 0x7Fu || (x.scales[i] & 0x7F00u) == 0x7F00u;
+              if (__ballot_sync(0xffffffffu, nan) >> (lane & 28) & 15u) {
+                x.codes[i] = make_uint4(0, 0, 0, 0);
+                x.scales[i] = 0;
+              }
+            }
+          }
           if (t >= kStages) good = wide_wait(is_v ? &ms->v_empty[st] : &ms->k_empty[st], ((t >> 1) - 1) & 1, ms);
           if (!good) break;
-          const unsigned char* src = smem + kOffRaw + rs * kRawBytes;
           if (is_v)
-            convert_tile<true>(src, smem + kOffV + st * kTileBytes, row, q, run.k1 - key0, key0 + kBN > T, lane);
+            store_tile<true>(x, smem + kOffV + st * kTileBytes, row, q);
           else
-            convert_tile<false>(src, smem + kOffK + st * kTileBytes, row, q, run.k1 - key0, false, lane);
+            store_tile<false>(x, smem + kOffK + st * kTileBytes, row, q);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ms->raw_empty[rs]);
-            mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
-          }
+          if (lane == 0) mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
         }
       } while (good && next_segment(p, pl, s));
       if (!good) wide_fail(ms);
