@@ -1128,17 +1128,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           int i = th >> 4, qr = (pair ? qt0 + x : qt0) * kBM + i;
           int h = qr / p.rows, pr = qr - h * p.rows;  // query head of the group, packed row
           const __nv_bfloat16* src = p.q + (static_cast<size_t>(s.r) * p.rows * p.Hq + head * p.G) * kD + c * 8;
+          int at = (pr * p.Hq + h) * kD;  // of the row's head in q
+          const int step = 8 * p.Hq * kD, wrap = kD - p.rows * p.Hq * kD;  // 8 packed rows on; the next head's first
           dst += i * 128 + (((c & 7) ^ (i & 7)) << 4);  // i steps by 8: the swizzle stays
-#pragma unroll 2
-          for (; i < kBM; i += 8, qr += 8, pr += 8, dst += 8 * 128) {
-            while (pr >= p.rows) {
-              pr -= p.rows;
-              ++h;
-            }
+#pragma unroll 4
+          for (; i < kBM; i += 8) {
             if (qr < R)
-              copy16_async(dst, src + (static_cast<size_t>(pr) * p.Hq + h) * kD);
+              copy16_async(dst, src + at);
             else
               *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            dst += 8 * 128;
+            qr += 8;
+            pr += 8;
+            at += step;
+            while (pr >= p.rows) {
+              pr -= p.rows;
+              at += wrap;
+            }
           }
           copy_async_wait();
           fence_proxy_async_smem();
