@@ -46,17 +46,18 @@ struct Params {
 // bound by reading the cache, 144 bytes per slot and kv head, so everything
 // else is kept off that path.
 //
-// * A warp takes 32 slots at a time and has three such pieces (4.6 KB each) in
+// * A warp takes 32 slots at a time and has two such pieces (4.6 KB each) in
 //   flight: bulk copies into its own ring, no other warp to wait for. Codes and
 //   scales of a head are contiguous, so a piece is four copies.
-// * Both products are m16n8k16 with the query rows as M. The codes become f16
-//   in registers, straight in fragment order, by choosing which element each
-//   fragment position stands for: a sum over dims (or slots) may take them in
-//   any order as long as both operands agree. For S a lane holds 32
-//   consecutive dims of one slot (one 16-byte load); for O a lane holds the 16
-//   dims of one scale group of four slots (four 8-byte loads), paired by slot.
-// * Softmax weights never leave registers: S's accumulator layout is P's
-//   operand layout.
+// * Both products are m16n8k16 with the query rows as N, eight or sixteen of
+//   them: S^T = K Q^T and O^T = V^T P^T. The codes become f16 in registers,
+//   straight in fragment order, by choosing which element each fragment position
+//   stands for: a sum over dims (or slots) may take them in any order as long as
+//   both operands agree. For S a lane holds 32 consecutive dims of a slot (one
+//   16-byte load) and of a query row; for O the 16 dims of one scale group of
+//   four slots (four 8-byte loads), paired by slot.
+// * Softmax weights never leave registers: an 8 x 8 transpose turns S^T's
+//   accumulator layout into P^T's operand layout.
 // The warps of a block are merged through shared memory, the blocks of a head
 // through the workspace by the block that finishes last.
 
@@ -64,23 +65,21 @@ constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewRows = 16;
 constexpr int kUnit = 32;    // slots of one piece
-constexpr int kFewStages = 3;
+constexpr int kFewStages = 2;
 constexpr uint32_t kUnitCodes = kUnit * glance::kKv4CodeBytes;    // 2048
 constexpr uint32_t kUnitScales = kUnit * glance::kKv4ScaleBytes;  // 256
 constexpr uint32_t kUnitBytes = 2 * (kUnitCodes + kUnitScales);
-constexpr uint32_t kFewRing = kFewWarps * kFewStages * kUnitBytes;  // 110,592
-constexpr uint32_t kFewQ = 8 * 32 * 16;                             // Q in fragment order
-constexpr uint32_t kFewMisc = 512;
-constexpr uint32_t kFewSmem = kFewRing + kFewQ + kFewMisc;
+constexpr uint32_t kFewRing = kFewWarps * kFewStages * kUnitBytes;  // 73,728
+constexpr uint32_t kFewMisc = 256;
+constexpr uint32_t kFewSmem = kFewRing + kFewMisc;
 constexpr uint32_t kWarpRing = kFewStages * kUnitBytes;
 constexpr uint32_t kWarpO = kFewRows * kD * 4;  // a finished warp's O, then its rows' maxima and sums, in its own ring
 static_assert(kWarpO + 2 * kFewRows * 4 <= kWarpRing, "a warp's result fits its ring");
-static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two blocks per SM");
+static_assert(3 * (kFewSmem + 1024) <= 228 * 1024, "three blocks per SM");
 
 struct FewMisc {
   uint64_t full[kFewWarps][kFewStages];
-  float row_scale[kFewRows];           // score factor of a row, in log2
-  int req, head, split, n_split, tau, first_block, last;
+  int req, head, split, n_split, tau, first_block, T, last;
 };
 static_assert(sizeof(FewMisc) <= kFewMisc, "misc block");
 
@@ -118,21 +117,22 @@ __device__ __forceinline__ float score_factor(float amax, float factor, float sc
 // grid; it comes from the prefix lengths themselves, which only the device
 // knows. Warp 0 computes it, lane r for request r.
 __device__ __forceinline__ void few_plan(const Params& p, FewMisc* ms, int lane) {
-  int units = 0;
+  int units = 0, T = 0;
   if (lane < p.B) {
-    const int T = *p.req[lane].t_len;
+    T = *p.req[lane].t_len;
     const bool room = T >= 0 && T <= p.req[lane].t_cap - p.rows;
     if (!room && blockIdx.x == 0) report(GLANCE_DEV_TREE_CAPACITY);
     units = room ? (T + p.rows + kUnit - 1) / kUnit : 0;
   }
   const int per_head = static_cast<int>(gridDim.x) / p.Hkv;  // blocks for one head of every request
-  int lo = kFewWarps, hi = max(kFewWarps, __reduce_max_sync(0xffffffffu, units));
-  while (lo < hi) {  // at hi every request has one block, and per_head >= B
-    const int mid = (lo + hi) >> 1;
+  const int sum = __reduce_add_sync(0xffffffffu, units);
+  int lo = max(kFewWarps, (sum + per_head - 1) / per_head), hi = max(lo, __reduce_max_sync(0xffffffffu, units)), mid = lo;
+  while (lo < hi) {  // not under the mean; at hi every request has one block, and per_head >= B
     if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_head)
       hi = mid;
     else
       lo = mid + 1;
+    mid = (lo + hi) >> 1;
   }
   const int n = (units + lo - 1) / lo;
   int end = n * p.Hkv;  // inclusive scan of the requests' blocks
@@ -145,7 +145,7 @@ __device__ __forceinline__ void few_plan(const Params& p, FewMisc* ms, int lane)
   const unsigned past = __ballot_sync(0xffffffffu, lane < p.B && at >= end);
   const int r = __popc(past);
   const int start = __shfl_sync(0xffffffffu, end - n * p.Hkv, r & 31);
-  const int nr = __shfl_sync(0xffffffffu, n, r & 31);
+  const int nr = __shfl_sync(0xffffffffu, n, r & 31), Tr = __shfl_sync(0xffffffffu, T, r & 31);
   if (lane == 0) {
     const bool any = r < p.B && nr > 0;
     ms->req = any ? r : -1;
@@ -153,6 +153,7 @@ __device__ __forceinline__ void few_plan(const Params& p, FewMisc* ms, int lane)
     ms->split = any ? (at - start) % nr : 0;
     ms->n_split = nr;
     ms->tau = lo;
+    ms->T = Tr;
     ms->first_block = any ? at - (at - start) % nr : 0;
   }
 }
@@ -173,11 +174,18 @@ __device__ __forceinline__ void few_copy(const Request& rq, long long head0, int
   bulk_copy_g2s(st + 2 * kUnitCodes + kUnitScales, rq.v_scale + at * 8, n * 8, bar);
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+
+// kN: groups of eight query rows.
+template <int kN>
 __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem;
-  uint4* sq = reinterpret_cast<uint4*>(smem + kFewRing);
-  FewMisc* ms = reinterpret_cast<FewMisc*>(smem + kFewRing + kFewQ);
+  FewMisc* ms = reinterpret_cast<FewMisc*>(smem + kFewRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
     for (int s = 0; s < kFewStages; ++s) mbar_init(&ms->full[warp][s], 1);
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   if (ms->req < 0) return;
   const Request& rq = p.req[ms->req];
   const int head = ms->head, n_split = ms->n_split;
-  const int T = *rq.t_len, n_keys = T + p.rows;
+  const int T = ms->T, n_keys = T + p.rows;
   const int n_units = (n_keys + kUnit - 1) / kUnit;
   const int u0 = ms->split * ms->tau, u1 = min(u0 + ms->tau, n_units);
   const long long head0 = static_cast<long long>(head) * rq.head_stride;
@@ -201,49 +209,61 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + s * kUnitBytes, &ms->full[warp][s]);
   const int R = p.G * p.rows;
   const size_t q_base = static_cast<size_t>(ms->req) * p.rows * p.Hq + head * p.G;
-  {
-    // Q into fragment order: thread (row, e) has dims 8e .. 8e + 7
-    const int row = threadIdx.x >> 4, e = threadIdx.x & 15;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (row < R)
-      x = *reinterpret_cast<const uint4*>(p.q + (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + e * 8);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float f[8], amax = 0.f;
-    bool bad = false;
+  // Fragments: lane = 4 r + c. K: slots r (and r + 8) of sixteen, in the order
+  // below, dims 32c ..; Q: row r, dims 32c ..; a lane's scores and O are of
+  // query rows 2c and 2c + 1 (of each eight).
+  const int r = lane >> 2, c = lane & 3;
+  uint32_t q[kN][16];
+  float sc[kN][2];
+  uint32_t seen[kN][2];  // visible tree rows (at most 16)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-      bad = bad || !(fabsf(f[2 * i]) < INFINITY) || !(fabsf(f[2 * i + 1]) < INFINITY);
+  for (int n = 0; n < kN; ++n) {
+    const int row = 8 * n + r;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + 32 * c);
+    uint4 v[4];
+    uint32_t top = 0;  // the largest magnitude's bits: in the order of the absolute values
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = row < R ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      top = max(top, max(max(v[e].x & 0x7FFFu, v[e].y & 0x7FFFu), max(v[e].z & 0x7FFFu, v[e].w & 0x7FFFu)));
+      top = max(top, max(max(v[e].x & 0x7FFF0000u, v[e].y & 0x7FFF0000u), max(v[e].z & 0x7FFF0000u, v[e].w & 0x7FFF0000u)) >> 16);
     }
-    if (bad) amax = INFINITY;
-#pragma unroll
-    for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
     const float qf = query_factor(amax);
-    if (e == 0) ms->row_scale[row] = score_factor(amax, qf, p.scale_log2, rq.k_global);
-    uint32_t* s32 = reinterpret_cast<uint32_t*>(sq);
+    const float factor = score_factor(amax, qf, p.scale_log2, rq.k_global);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // dims 8e + 2i, + 1: c = e / 4, step, half of the step
-      const int step = (e & 3) * 2 + (i >> 1);
-      s32[(step * 32 + (row & 7) * 4 + (e >> 2)) * 4 + (row >> 3) + 2 * (i & 1)] = pack_f16x2(f[2 * i] * qf, f[2 * i + 1] * qf);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[n][4 * e + i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[n][h] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + h));
+      const int qr = 8 * n + 2 * c + h, i = qr % p.rows;
+      seen[n][h] = qr >= R ? 0u : rq.anc ? static_cast<uint32_t>(rq.anc[i * p.W]) : 1u << i;
+      seen[n][h] &= (1u << p.rows) - 1u;  // rows <= 16
     }
   }
-  __syncthreads();
-  const int r0 = lane >> 2, c = lane & 3;
-  const float sc[2] = {ms->row_scale[r0], ms->row_scale[r0 + 8]};
-  // visible tree rows (at most 16) of this lane's two query rows
-  uint32_t seen[2];
+  float o[8][kN][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int qr = r0 + 8 * h, i = qr % p.rows;
-    seen[h] = qr >= R ? 0u : rq.anc ? static_cast<uint32_t>(rq.anc[i * p.W]) : 1u << i;
-    if (p.rows < 32) seen[h] &= (1u << p.rows) - 1u;
+  for (int t = 0; t < 8; ++t)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+  float m[kN][2], l[kN][2];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
   }
-  float o[16][4];
-#pragma unroll
-  for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // position j of sixteen slots is slot 4 (j & 1) + (j >> 1 & 3) + (j & 8): the
+  // four slots of a lane's V fragment are then 4 apart and the four lanes' next
+  // to each other, which loads without bank conflicts
+  const int k_slot = 4 * (r & 1) + (r >> 1);
   int stage = 0;
   uint32_t parity = 0;
   for (int u = u0 + warp; u < u1; u += kFewWarps) {
@@ -256,36 +276,38 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       break;
     }
     const int key0 = u * kUnit;
-    float s[4][4];
+    float s[2][kN][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
-    {
-      // S: lane (n = r0, c) has slot 8b + 4 (n & 1) + (n >> 1), dims 32c ..
-      const int slot = 4 * (r0 & 1) + (r0 >> 1);
-      uint4 kw[4];
-      uint32_t ks[4][2];
+    for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        kw[b] = *reinterpret_cast<const uint4*>(st + (8 * b + slot) * 64 + c * 16);
-        const uint32_t x = scales2_to_f16(*reinterpret_cast<const uint16_t*>(st + 2 * kUnitCodes + (8 * b + slot) * 8 + 2 * c));
+      for (int n = 0; n < kN; ++n) s[kt][n][0] = s[kt][n][1] = s[kt][n][2] = s[kt][n][3] = 0.f;
+      uint4 kw[2];
+      uint32_t ks[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int slot = 16 * kt + 8 * b + k_slot;
+        kw[b] = *reinterpret_cast<const uint4*>(st + slot * 64 + c * 16);
+        const uint32_t x = scales2_to_f16(*reinterpret_cast<const uint16_t*>(st + 2 * kUnitCodes + slot * 8 + 2 * c));
         ks[b][0] = prmt(x, x, 0x1010);
         ks[b][1] = prmt(x, x, 0x3232);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 a = sq[(2 * j) * 32 + lane], a2 = sq[(2 * j + 1) * 32 + lane];
+        uint32_t h[2][4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t h[4];
-          codes8_to_f16(j == 0 ? kw[b].x : j == 1 ? kw[b].y : j == 2 ? kw[b].z : kw[b].w, h);
+        for (int b = 0; b < 2; ++b) {
+          codes8_to_f16(j == 0 ? kw[b].x : j == 1 ? kw[b].y : j == 2 ? kw[b].z : kw[b].w, h[b]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = mul_f16x2(h[i], ks[b][j >> 1]);
-          mma16816(s[b], a.x, a.y, a.z, a.w, h[0], h[1]);
-          mma16816(s[b], a2.x, a2.y, a2.z, a2.w, h[2], h[3]);
+          for (int i = 0; i < 4; ++i) h[b][i] = mul_f16x2(h[b][i], ks[b][j >> 1]);
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          mma16816(s[kt][n], h[0][0], h[1][0], h[0][1], h[1][1], q[n][4 * j], q[n][4 * j + 1]);
+          mma16816(s[kt][n], h[0][2], h[1][2], h[0][3], h[1][3], q[n][4 * j + 2], q[n][4 * j + 3]);
         }
       }
     }
-    // slot of s[b][e]: 8b + 4 (e & 1) + c, row r0 + 8 (e >> 1)
+    // s[kt][n][e]: slot 16 kt + 8 (e >> 1) + k_slot, query row 8n + 2c + (e & 1)
     uint32_t zero_v = 0u;  // slots whose V must not be multiplied
     if (key0 + kUnit > T) {
       // tree slots: a row sees its ancestors. What the other rows hold must not
@@ -299,73 +321,77 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       zero_v = bad | past;
       const int pre = T - key0;  // prefix slots of the piece
 #pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t vis = ~past & (pre >= 32 ? 0xFFFFFFFFu
+                                        : pre >= 0 ? ((1u << pre) - 1u) | (seen[n][h] << pre)
+                                                   : (-pre < 32 ? seen[n][h] >> -pre : 0u));
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int k = 16 * kt + 8 * b + k_slot;
+              float& x = s[kt][n][2 * b + h];
+              x = !(vis >> k & 1u) ? -INFINITY : (bad >> k & 1u) ? __uint_as_float(0x7FC00000u) : x;
+            }
+        }
+    }
+    uint32_t pb[2][kN][2];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float w[2][2][2];  // [query row][kt][half]
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t vis = pre >= 32 ? 0xFFFFFFFFu
-                             : pre >= 0 ? ((1u << pre) - 1u) | (seen[h] << pre)
-                                        : (-pre < 32 ? seen[h] >> -pre : 0u);
+        float mx = fmaxf(fmaxf(s[0][n][h], s[0][n][2 + h]), fmaxf(s[1][n][h], s[1][n][2 + h]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sc[n][h];  // sc > 0, or NaN (then mx is of no account)
+        // the running maximum moves only when it has grown by 8 (in log2): until
+        // then the weights stay below 2^8 and nothing is rescaled
+        const bool grow = mx > m[n][h] + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mx : m[n][h];
+          const float alpha = m[n][h] == -INFINITY ? 0.f : ex2_approx(m[n][h] - mn);
+          m[n][h] = mn;
+          l[n][h] *= alpha;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+          for (int t = 0; t < 8; ++t) {
+            o[t][n][h] *= alpha;
+            o[t][n][2 + h] *= alpha;
+          }
+        }
+        const float off = m[n][h] == -INFINITY ? 0.f : m[n][h];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = 8 * b + 4 * e + c;
-            float& x = s[b][2 * h + e];
-            x = !((vis & ~past) >> k & 1u) ? -INFINITY : (bad >> k & 1u) ? __uint_as_float(0x7FC00000u) : x;
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            w[h][kt][b] = ex2_approx(fmaf(s[kt][n][2 * b + h], sc[n][h], -off));
+            l[n][h] += w[h][kt][b];
           }
       }
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) pb[kt][n][b] = transpose8x8(pack_f16x2(w[0][kt][b], w[1][kt][b]));
     }
-    uint32_t pa[2][4];
+    // O^T: lane (r, c) has slots 16 kt + 4i + c, dims 16r .. 16r + 15; rows r and
+    // r + 8 of tile t are dims 16r + 2t and 16r + 2t + 1
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = fmaxf(fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])),
-                       fmaxf(fmaxf(s[2][2 * h], s[2][2 * h + 1]), fmaxf(s[3][2 * h], s[3][2 * h + 1])));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sc[h];  // sc > 0, or NaN (then mx is of no account)
-      // the running maximum moves only when it has grown by 8 (in log2): until
-      // then the weights stay below 2^8 and nothing is rescaled
-      const bool grow = mx > m[h] + 8.f;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? mx : m[h];
-        const float alpha = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mn);
-        m[h] = mn;
-        l[h] *= alpha;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          o[t][2 * h] *= alpha;
-          o[t][2 * h + 1] *= alpha;
-        }
-      }
-      const float off = m[h] == -INFINITY ? 0.f : m[h];
-      float w[4][2];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[b][e] = ex2_approx(fmaf(s[b][2 * h + e], sc[h], -off));
-          l[h] += w[b][e];
-        }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        pa[kb][h] = pack_f16x2(w[2 * kb][0], w[2 * kb][1]);
-        pa[kb][2 + h] = pack_f16x2(w[2 * kb + 1][0], w[2 * kb + 1][1]);
-      }
-    }
-    // O: lane (n = r0, c) has slots 16 kb + 4i + c, dims 16n .. 16n + 15; the
-    // product's column n of tile t is dim 16n + t
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kt = 0; kt < 2; ++kt) {
       uint2 vw[4];
       uint32_t sb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int slot = 16 * kb + 4 * i + c;
-        vw[i] = *reinterpret_cast<const uint2*>(st + kUnitCodes + slot * 64 + r0 * 8);
-        sb[i] = st[2 * kUnitCodes + kUnitScales + slot * 8 + r0];
+        const int slot = 16 * kt + 4 * i + c;
+        vw[i] = *reinterpret_cast<const uint2*>(st + kUnitCodes + slot * 64 + r * 8);
+        sb[i] = st[2 * kUnitCodes + kUnitScales + slot * 8 + r];
       }
       uint32_t vs[2] = {scales2_to_f16(sb[0] | sb[1] << 8), scales2_to_f16(sb[2] | sb[3] << 8)};
       if (zero_v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (zero_v >> (16 * kb + 4 * i + c) & 1u) {
+          if (zero_v >> (16 * kt + 4 * i + c) & 1u) {
             vw[i] = make_uint2(0u, 0u);
             vs[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
           }
@@ -376,13 +402,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
 #pragma unroll
         for (int i = 0; i < 4; ++i) codes8_to_f16(w ? vw[i].y : vw[i].x, h[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = mul_f16x2(prmt(h[0][i], h[1][i], 0x5410), vs[0]), a1 = mul_f16x2(prmt(h[0][i], h[1][i], 0x7632), vs[0]);
+          const uint32_t a2 = mul_f16x2(prmt(h[2][i], h[3][i], 0x5410), vs[1]), a3 = mul_f16x2(prmt(h[2][i], h[3][i], 0x7632), vs[1]);
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const uint32_t sel = z ? 0x7632 : 0x5410;
-            mma16816(o[8 * w + 2 * i + z], pa[kb][0], pa[kb][1], pa[kb][2], pa[kb][3],
-                     mul_f16x2(prmt(h[0][i], h[1][i], sel), vs[0]), mul_f16x2(prmt(h[2][i], h[3][i], sel), vs[1]));
-          }
+          for (int n = 0; n < kN; ++n) mma16816(o[4 * w + i][n], a0, a1, a2, a3, pb[kt][n][0], pb[kt][n][1]);
+        }
       }
     }
     __syncwarp();  // every lane has read the piece
@@ -397,33 +422,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   const auto warp_m = [&](int w) { return reinterpret_cast<float*>(ring + w * kWarpRing + kWarpO); };
   // the block's rows: maxima first, then every warp's O relative to them
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    if (l[h] != l[h]) m[h] = 0.f;  // a NaN row stays one in every merge
-    if (c == 0) {
-      warp_m(warp)[r0 + 8 * h] = m[h];
-      warp_m(warp)[kFewRows + r0 + 8 * h] = l[h];
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], x);
+      if (l[n][h] != l[n][h]) m[n][h] = 0.f;  // a NaN row stays one in every merge
+      if (r == 0) {
+        warp_m(warp)[8 * n + 2 * c + h] = m[n][h];
+        warp_m(warp)[kFewRows + 8 * n + 2 * c + h] = l[n][h];
+      }
     }
-  }
   __syncthreads();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = r0 + 8 * h;
-    if (row < R) {
-      float M = -INFINITY;
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, warp_m(w)[row]);
-      const float f = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - M);
-      float4* dst = warp_o(warp) + row * 32;  // 4-dim pieces rotated by the row, against bank conflicts
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * n + 2 * c + h;
+      if (row < R) {
+        float M = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+        for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, warp_m(w)[row]);
+        const float f = m[n][h] == -INFINITY ? 0.f : ex2_approx(m[n][h] - M);
+        float4* dst = warp_o(warp) + row * 32;  // 4-dim pieces rotated by the row, against bank conflicts
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          dst[(8 * c + 4 * e + t + row) & 31] = make_float4(o[4 * t][2 * h + e] * f, o[4 * t + 1][2 * h + e] * f,
-                                                            o[4 * t + 2][2 * h + e] * f, o[4 * t + 3][2 * h + e] * f);
+          dst[(4 * r + t + row) & 31] = make_float4(o[2 * t][n][h] * f, o[2 * t][n][2 + h] * f, o[2 * t + 1][n][h] * f,
+                                                    o[2 * t + 1][n][2 + h] * f);
+      }
     }
-  }
   __syncthreads();
   float4* out_part = p.part_o + static_cast<size_t>(blockIdx.x) * kFewRows * 32;
   for (int i = threadIdx.x; i < R * 32; i += kFewThreads) {
@@ -462,49 +489,68 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   }
   __syncthreads();
   if (!ms->last) return;
-  const int b0 = ms->first_block;
-  for (int i = threadIdx.x; i < R * 32; i += kFewThreads) {
-    const int row = i >> 5, x = i & 31;
+  // thread = (slice of the parts, row, dim quad): few rows leave threads for
+  // several slices, which meet in the ring
+  const int b0 = ms->first_block, items = R * 32, slices = max(1, kFewThreads / items);
+  float4* s_o = reinterpret_cast<float4*>(ring);
+  float2* s_ml = reinterpret_cast<float2*>(ring + kFewThreads * 16);
+  for (int i0 = 0; i0 < items; i0 += kFewThreads) {
+    const int slice = threadIdx.x / items, i = i0 + threadIdx.x - slice * items, row = i >> 5, x = i & 31;
     float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < n_split; s0 += 8) {
-      float4 v[8];
-      float2 ml[8];
+    if (slice < slices && i < items) {
+      constexpr int kAhead = 10;
+#pragma unroll 1
+      for (int s0 = slice; s0 < n_split; s0 += kAhead * slices) {
+        float4 v[kAhead];
+        float2 ml[kAhead];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const bool in = s0 + s < n_split;
-        ml[s] = in ? __ldcg(p.part_ml + (b0 + s0 + s) * kFewRows + row) : make_float2(-INFINITY, 0.f);
-        v[s] = in ? __ldcg(p.part_o + (static_cast<size_t>(b0 + s0 + s) * kFewRows + row) * 32 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float mx = M;
+        for (int e = 0; e < kAhead; ++e) {
+          const int b = s0 + e * slices;
+          const bool in = b < n_split;
+          ml[e] = in ? __ldcg(p.part_ml + (b0 + b) * kFewRows + row) : make_float2(-INFINITY, 0.f);
+          v[e] = in ? __ldcg(p.part_o + (static_cast<size_t>(b0 + b) * kFewRows + row) * 32 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mx = M;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) mx = fmaxf(mx, ml[s].x);
-      const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mx);
-      M = mx;
-      L *= keep;
-      a.x *= keep;
-      a.y *= keep;
-      a.z *= keep;
-      a.w *= keep;
+        for (int e = 0; e < kAhead; ++e) mx = fmaxf(mx, ml[e].x);
+        const float keep = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+        M = mx;
+        L *= keep;
+        a = make_float4(a.x * keep, a.y * keep, a.z * keep, a.w * keep);
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const float f = ml[s].x == -INFINITY ? 0.f : ex2_approx(ml[s].x - mx);
-        L = fmaf(f, ml[s].y, L);
-        a.x = fmaf(f, v[s].x, a.x);
-        a.y = fmaf(f, v[s].y, a.y);
-        a.z = fmaf(f, v[s].z, a.z);
-        a.w = fmaf(f, v[s].w, a.w);
+        for (int e = 0; e < kAhead; ++e) {
+          const float f = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - mx);
+          L = fmaf(f, ml[e].y, L);
+          a = make_float4(fmaf(f, v[e].x, a.x), fmaf(f, v[e].y, a.y), fmaf(f, v[e].z, a.z), fmaf(f, v[e].w, a.w));
+        }
       }
     }
+    if (slices > 1) {  // then the rows fit the block at once
+      s_o[threadIdx.x] = a;
+      s_ml[threadIdx.x] = make_float2(M, L);
+      __syncthreads();
+      if (slice) return;
+      for (int y = 1; y < slices; ++y) {
+        const float4 b = s_o[y * items + i];
+        const float2 ml = s_ml[y * items + i];
+        const float mx = fmaxf(M, ml.x);
+        const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - mx), f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+        M = mx;
+        L = f0 * L + f1 * ml.y;
+        a = make_float4(f0 * a.x + f1 * b.x, f0 * a.y + f1 * b.y, f0 * a.z + f1 * b.z, f0 * a.w + f1 * b.w);
+      }
+    }
+    if (slice || i >= items) continue;
     const float inv = L == 0.f ? 0.f : rq.v_global / L;
     const size_t at = (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + x * 4;
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
   }
 }
 
-// Blocks of the few-rows kernel: two per SM, or one per kv head of every
-// request where that is more.
-int few_grid(int B, int Hkv) {
+// Blocks of the few-rows kernel: as many as fit the SMs, or one per kv head of
+// every request where that is more.
+int few_grid(int B, int Hkv, int R) {
   const int n = 2 * glance::num_sms();
   return n < B * Hkv ? B * Hkv : n / Hkv * Hkv;
 }
@@ -1466,7 +1512,7 @@ bool few_rows(int rows, int G) { return rows * G <= kFewRows; }
 size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
   const int Hkv = kv[0].n_kv_heads;
   if (few_rows(rows, Hq / Hkv))
-    return few_counter_bytes(B, Hkv) + static_cast<size_t>(few_grid(B, Hkv)) * kFewRows * (kD * 4 + sizeof(float2));
+    return few_counter_bytes(B, Hkv) + static_cast<size_t>(few_grid(B, Hkv, rows * (Hq / Hkv))) * kFewRows * (kD * 4 + sizeof(float2));
   const int n_qp = (rows * (Hq / Hkv) + 2 * kBM - 1) / (2 * kBM);
   return wide_group_bytes(B, Hkv, n_qp) + wide_parts() * kBM * (kD * 2 + sizeof(float2));
 }
@@ -1547,17 +1593,18 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
   cfg.numAttrs = 1;
   cudaError_t e;
   if (few_rows(rows, G)) {
-    const int grid = few_grid(B, Hkv);
+    const int grid = few_grid(B, Hkv, rows * G);
+    const auto kernel = rows * G <= 8 ? kv4_attention_few_kernel<1> : kv4_attention_few_kernel<2>;
     char* ws = static_cast<char*>(workspace);
     p.count = reinterpret_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float4*>(ws + few_counter_bytes(B, Hkv));
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(grid) * kFewRows * 32);
-    e = glance::ensure_smem(reinterpret_cast<const void*>(kv4_attention_few_kernel), kFewSmem);
+    e = glance::ensure_smem(reinterpret_cast<const void*>(kernel), kFewSmem);
     if (e != cudaSuccess) return glance::cuda_fail(e, who);
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = kFewSmem;
-    e = cudaLaunchKernelEx(&cfg, kv4_attention_few_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
   } else {
     const int grid = glance::num_sms();
     char* ws = static_cast<char*>(workspace);
