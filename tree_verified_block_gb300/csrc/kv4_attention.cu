@@ -40,6 +40,162 @@ struct Params {
   float scale_log2;
 };
 
+// --------------------------------------------------------- work for a block
+//
+// The slots of every group (request, kv head, query tile pair) are counted in
+// units of 32. Where each group can be cut into equal parts that fill the grid,
+// a block has one part; else the list of all groups is cut into equal runs and
+// a block's run may cross groups (a "segment" is its part in one group). In that
+// list a group counts kLead units more than it has, what starting and ending a
+// segment takes. The lengths are read on the device: only it knows them.
+
+constexpr int kUnit = 32;
+
+struct Plan {
+  int T[kMaxB];
+  int units[kMaxB];       // of one group of request r; 0: no room, no output
+  long long base[kMaxB];  // length of the list before request r's groups
+  long long total;        // of the whole list
+  int runs;               // blocks that the list is cut for: none gets less than a tile and its lead
+  int tau;                // > 0: every group is cut into parts of tau units
+  int blocks0[kMaxB];     // tau > 0: blocks before request r's
+};
+
+// A block's part in one group: units [a, a + n) of group g of request r.
+struct Segment {
+  int r, g, a, n;
+  int left;   // length of the run after this segment
+  int index;  // of the block's segments
+};
+
+// a / b for a run's arithmetic: 64-bit division only where it is needed.
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return a <= 0xFFFFFFFFll ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// The plan, by one warp; every block comes to the same one.
+template <int kMinUnits, int kLead>
+__device__ __forceinline__ void make_plan(const Params& p, Plan* pl, int lane, int blocks) {
+  int units = 0, T = 0;
+  if (lane < p.B) {
+    T = *p.req[lane].t_len;
+    if (T >= 0 && T <= p.req[lane].t_cap - p.rows) units = (T + p.rows + kUnit - 1) / kUnit;
+  }
+  const int gpr = p.Hkv * p.n_qp;
+  const int sum = __reduce_add_sync(0xffffffffu, units);
+  const int length = units > 0 ? units + kLead : 0;
+  const long long total = static_cast<long long>(__reduce_add_sync(0xffffffffu, length)) * gpr;
+  const int active = __popc(__ballot_sync(0xffffffffu, units > 0));
+  const int per_group = blocks / gpr;
+  const int runs = static_cast<int>(min(static_cast<long long>(blocks), max(1ll, div_small(total, kMinUnits + kLead))));
+  int tau = 0;
+  if (per_group >= active && active > 0) {
+    // the least tau at which the groups' parts fit the grid: not under the mean,
+    // and at hi every request has one part
+    int lo = max(kMinUnits, (sum + per_group - 1) / per_group), hi = max(lo, __reduce_max_sync(0xffffffffu, units));
+    int mid = lo;
+    while (lo < hi) {
+      if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_group)
+        hi = mid;
+      else
+        lo = mid + 1;
+      mid = (lo + hi) >> 1;
+    }
+    if (lo <= div_small(total, runs)) tau = lo;
+  }
+  const int n = tau ? (units + tau - 1) / tau * gpr : 0;
+  int before = length, nb = n;  // inclusive scans over the requests
+#pragma unroll 1
+  for (int o = 1; o < kMaxB; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_up_sync(0xffffffffu, nb, o);
+    if (lane >= o) {
+      before += u;
+      nb += v;
+    }
+  }
+  if (lane < kMaxB) {
+    pl->T[lane] = T;
+    pl->units[lane] = units;
+    pl->base[lane] = static_cast<long long>(before - length) * gpr;
+    pl->blocks0[lane] = nb - n;
+  }
+  if (lane == 0) {
+    pl->total = total;
+    pl->runs = runs;
+    pl->tau = tau;
+  }
+}
+
+// First unit of block b's run (runs that may cross groups).
+__device__ __forceinline__ long long run_start(long long total, int b, int blocks) {
+  const long long q = div_small(total, blocks);
+  return q * b + div_small((total - q * blocks) * b, blocks);
+}
+
+__device__ __forceinline__ void step_group(const Params& p, const Plan& pl, Segment& s) {
+  if (++s.g == p.Hkv * p.n_qp) {
+    s.g = 0;
+    do ++s.r;
+    while (pl.units[s.r] == 0);
+  }
+}
+// The run's part from place `at` of the current group's stretch on, or of the
+// next group that it has units of.
+template <int kLead>
+__device__ __forceinline__ bool take_segment(const Params& p, const Plan& pl, Segment& s, int at) {
+  for (;;) {
+    const int take = min(s.left, pl.units[s.r] + kLead - at), end = at + take - kLead;
+    s.left -= take;
+    s.a = max(at - kLead, 0);
+    s.n = end - s.a;
+    if (s.n > 0) {
+      ++s.index;
+      return true;
+    }
+    if (s.left == 0) return false;
+    step_group(p, pl, s);
+    at = 0;
+  }
+}
+template <int kLead>
+__device__ __forceinline__ bool first_segment(const Params& p, const Plan& pl, int b, Segment& s) {
+  const int gpr = p.Hkv * p.n_qp;
+  s.index = 0;
+  int r = 0;
+  if (pl.tau) {
+    int n = 0, at = 0;
+    for (; r < p.B; ++r) {
+      n = (pl.units[r] + pl.tau - 1) / pl.tau;
+      at = b - pl.blocks0[r];
+      if (at < n * gpr) break;
+    }
+    if (r == p.B) return false;
+    s.r = r;
+    s.g = at / n;
+    s.a = at % n * pl.tau;
+    s.n = min(pl.tau, pl.units[r] - s.a);
+    s.left = 0;
+    return true;
+  }
+  if (b >= pl.runs || pl.total == 0) return false;
+  const long long x = run_start(pl.total, b, pl.runs);
+  const int len = static_cast<int>(run_start(pl.total, b + 1, pl.runs) - x);
+  while (r + 1 < p.B && x >= pl.base[r + 1]) ++r;  // requests without units share their base with the next
+  const long long in = x - pl.base[r];
+  const int length = pl.units[r] + kLead;
+  s.r = r;
+  s.g = static_cast<int>(div_small(in, length));
+  s.index = -1;
+  s.left = len;
+  return take_segment<kLead>(p, pl, s, static_cast<int>(in - static_cast<long long>(s.g) * length));
+}
+template <int kLead>
+__device__ __forceinline__ bool next_segment(const Params& p, const Plan& pl, Segment& s) {
+  if (s.left == 0) return false;
+  step_group(p, pl, s);
+  return take_segment<kLead>(p, pl, s, 0);
+}
+
 // ------------------------------------------------- few query rows per kv head
 //
 // At most 16 query rows share a kv head (decoding, small trees): the call is
@@ -64,22 +220,27 @@ struct Params {
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewRows = 16;
-constexpr int kUnit = 32;    // slots of one piece
 constexpr int kFewStages = 2;
 constexpr uint32_t kUnitCodes = kUnit * glance::kKv4CodeBytes;    // 2048
 constexpr uint32_t kUnitScales = kUnit * glance::kKv4ScaleBytes;  // 256
 constexpr uint32_t kUnitBytes = 2 * (kUnitCodes + kUnitScales);
 constexpr uint32_t kFewRing = kFewWarps * kFewStages * kUnitBytes;  // 73,728
-constexpr uint32_t kFewMisc = 256;
+constexpr uint32_t kFewMisc = 1024;
 constexpr uint32_t kFewSmem = kFewRing + kFewMisc;
 constexpr uint32_t kWarpRing = kFewStages * kUnitBytes;
 constexpr uint32_t kWarpO = kFewRows * kD * 4;  // a finished warp's O, then its rows' maxima and sums, in its own ring
 static_assert(kWarpO + 2 * kFewRows * 4 <= kWarpRing, "a warp's result fits its ring");
-static_assert(3 * (kFewSmem + 1024) <= 228 * 1024, "three blocks per SM");
+static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two blocks per SM");
+
+constexpr int kFewMin = kFewWarps, kFewLead = 12;  // a part has a piece for every warp
 
 struct FewMisc {
   uint64_t full[kFewWarps][kFewStages];
-  int req, head, split, n_split, tau, first_block, T, last;
+  Segment seg;
+  Plan plan;
+  int any;
+  int first_part, n_parts;  // of the segment's group: 2 * block + (the block's first or last segment)
+  int last;
 };
 static_assert(sizeof(FewMisc) <= kFewMisc, "misc block");
 
@@ -111,51 +272,35 @@ __device__ __forceinline__ float score_factor(float amax, float factor, float sc
   return amax < INFINITY ? fmaxf(scale_log2 * k_global * (1.f / factor), 1.17549435e-38f) : __uint_as_float(0x7FC00000u);
 }
 
-// Which part of which request's slots this block has: head `head` of request
-// `req`, units [split * tau, (split + 1) * tau). tau is the smallest number of
-// units per block (at least one per warp) at which every head's blocks fit the
-// grid; it comes from the prefix lengths themselves, which only the device
-// knows. Warp 0 computes it, lane r for request r.
-__device__ __forceinline__ void few_plan(const Params& p, FewMisc* ms, int lane) {
-  int units = 0, T = 0;
-  if (lane < p.B) {
-    T = *p.req[lane].t_len;
-    const bool room = T >= 0 && T <= p.req[lane].t_cap - p.rows;
-    if (!room && blockIdx.x == 0) report(GLANCE_DEV_TREE_CAPACITY);
-    units = room ? (T + p.rows + kUnit - 1) / kUnit : 0;
+// Which parts the group of a segment (not a whole group) has: their number and
+// the first one's place; by one warp.
+__device__ __forceinline__ void few_parts(const Plan& pl, const Segment& s, int lane, int& first_part, int& n) {
+  const int b = blockIdx.x;
+  if (pl.tau) {
+    n = (pl.units[s.r] + pl.tau - 1) / pl.tau;
+    first_part = 2 * (b - s.a / pl.tau);
+    return;
   }
-  const int per_head = static_cast<int>(gridDim.x) / p.Hkv;  // blocks for one head of every request
-  const int sum = __reduce_add_sync(0xffffffffu, units);
-  int lo = max(kFewWarps, (sum + per_head - 1) / per_head), hi = max(lo, __reduce_max_sync(0xffffffffu, units)), mid = lo;
-  while (lo < hi) {  // not under the mean; at hi every request has one block, and per_head >= B
-    if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_head)
-      hi = mid;
-    else
-      lo = mid + 1;
-    mid = (lo + hi) >> 1;
+  const int stretch = pl.units[s.r] + kFewLead;
+  const long long start = pl.base[s.r] + static_cast<long long>(s.g) * stretch;
+  int first = b;
+  bool late = s.index > 0;
+  if (s.a) {  // back to the block that has the group's first unit
+    for (;;) {
+      const unsigned before = __ballot_sync(0xffffffffu, run_start(pl.total, max(first - 1 - lane, 0), pl.runs) <= start + kFewLead);
+      first = max(first - (before ? __ffs(before) : 32), 0);
+      if (before || first == 0) break;
+    }
+    late = run_start(pl.total, first, pl.runs) < start;
   }
-  const int n = (units + lo - 1) / lo;
-  int end = n * p.Hkv;  // inclusive scan of the requests' blocks
-#pragma unroll
-  for (int o = 1; o < kMaxB; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end += v;
+  for (n = b + 1 - first;; n += 32) {  // on to the block whose run ends behind the group
+    const unsigned past = __ballot_sync(0xffffffffu, run_start(pl.total, min(first + n + lane, pl.runs), pl.runs) >= start + stretch);
+    if (past) {
+      n += __ffs(past) - 1;
+      break;
+    }
   }
-  const int at = blockIdx.x;
-  const unsigned past = __ballot_sync(0xffffffffu, lane < p.B && at >= end);
-  const int r = __popc(past);
-  const int start = __shfl_sync(0xffffffffu, end - n * p.Hkv, r & 31);
-  const int nr = __shfl_sync(0xffffffffu, n, r & 31), Tr = __shfl_sync(0xffffffffu, T, r & 31);
-  if (lane == 0) {
-    const bool any = r < p.B && nr > 0;
-    ms->req = any ? r : -1;
-    ms->head = any ? (at - start) / nr : 0;
-    ms->split = any ? (at - start) % nr : 0;
-    ms->n_split = nr;
-    ms->tau = lo;
-    ms->T = Tr;
-    ms->first_block = any ? at - (at - start) % nr : 0;
-  }
+  first_part = 2 * first + (late ? 1 : 0);
 }
 
 __device__ __forceinline__ void few_copy(const Request& rq, long long head0, int unit, int n_keys, unsigned char* st,
@@ -193,22 +338,32 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   }
   pdl_wait_prior();
   pdl_launch_dependents();
-  if (warp == 0) few_plan(p, ms, lane);
+  if (warp == 0) {
+    make_plan<kFewMin, kFewLead>(p, &ms->plan, lane, gridDim.x);
+    __syncwarp();
+    if (lane == 0) ms->any = first_segment<kFewLead>(p, ms->plan, blockIdx.x, ms->seg);
+  }
   __syncthreads();
-  if (ms->req < 0) return;
-  const Request& rq = p.req[ms->req];
-  const int head = ms->head, n_split = ms->n_split;
-  const int T = ms->T, n_keys = T + p.rows;
-  const int n_units = (n_keys + kUnit - 1) / kUnit;
-  const int u0 = ms->split * ms->tau, u1 = min(u0 + ms->tau, n_units);
-  const long long head0 = static_cast<long long>(head) * rq.head_stride;
+  const Plan& pl = ms->plan;
+  if (blockIdx.x == 0 && threadIdx.x < p.B && pl.units[threadIdx.x] == 0) report(GLANCE_DEV_TREE_CAPACITY);
+  if (!ms->any) return;
+  Segment sg = ms->seg;
   unsigned char* my_ring = ring + warp * kWarpRing;
+  int stage = 0;
+  uint32_t parity = 0;
+  do {
+  const Request& rq = p.req[sg.r];
+  const int head = sg.g, T = pl.T[sg.r], n_keys = T + p.rows;
+  const int u0 = sg.a, u1 = sg.a + sg.n;
+  const bool whole = sg.n == pl.units[sg.r];
+  const long long head0 = static_cast<long long>(head) * rq.head_stride;
   if (lane == 0)
     for (int s = 0; s < kFewStages; ++s)
       if (u0 + warp + s * kFewWarps < u1)
-        few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + s * kUnitBytes, &ms->full[warp][s]);
+        few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + (stage + s) % kFewStages * kUnitBytes,
+                 &ms->full[warp][(stage + s) % kFewStages]);
   const int R = p.G * p.rows;
-  const size_t q_base = static_cast<size_t>(ms->req) * p.rows * p.Hq + head * p.G;
+  const size_t q_base = static_cast<size_t>(sg.r) * p.rows * p.Hq + head * p.G;
   // Fragments: lane = 4 r + c. K: slots r (and r + 8) of sixteen, in the order
   // below, dims 32c ..; Q: row r, dims 32c ..; a lane's scores and O are of
   // query rows 2c and 2c + 1 (of each eight).
@@ -264,8 +419,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   // four slots of a lane's V fragment are then 4 apart and the four lanes' next
   // to each other, which loads without bank conflicts
   const int k_slot = 4 * (r & 1) + (r >> 1);
-  int stage = 0;
-  uint32_t parity = 0;
   for (int u = u0 + warp; u < u1; u += kFewWarps) {
     unsigned char* st = my_ring + stage * kUnitBytes;
     if (!__all_sync(0xffffffffu, mbar_wait(&ms->full[warp][stage], parity))) {
@@ -452,7 +605,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       }
     }
   __syncthreads();
-  float4* out_part = p.part_o + static_cast<size_t>(blockIdx.x) * kFewRows * 32;
+  const int part = 2 * blockIdx.x + (sg.index ? 1 : 0);  // two per block: its first segment's and its last one's
+  float4* out_part = p.part_o + static_cast<size_t>(part) * kFewRows * 32;
   for (int i = threadIdx.x; i < R * 32; i += kFewThreads) {
     const int row = i >> 5, x = i & 31;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -469,29 +623,37 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       a.z += v.z;
       a.w += v.w;
     }
-    if (n_split == 1) {
+    if (whole) {
       const float inv = L == 0.f ? 0.f : rq.v_global / L;
       const size_t at = (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + x * 4;
       *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     } else {
       out_part[i] = a;
-      if (x == 0) p.part_ml[blockIdx.x * kFewRows + row] = make_float2(M, L);
+      if (x == 0) p.part_ml[part * kFewRows + row] = make_float2(M, L);
     }
   }
-  if (n_split == 1) return;
-  // the last block of the head merges: its add acquires the others' partials
+  if (!whole && warp == 0) {
+    int first_part, n_parts;
+    few_parts(pl, sg, lane, first_part, n_parts);
+    if (lane == 0) {
+      ms->first_part = first_part;
+      ms->n_parts = n_parts;
+    }
+  }
+  // the last block of the group merges: its add acquires the others' partials
   __syncthreads();
+  if (!whole) {
   if (threadIdx.x == 0) {
-    uint32_t* count = p.count + ms->req * p.Hkv + head;
-    const bool last = atom_add_acq_rel_gpu(count, 1u) == static_cast<uint32_t>(n_split - 1);
+    uint32_t* count = p.count + sg.r * p.Hkv + head;
+    const bool last = atom_add_acq_rel_gpu(count, 1u) == static_cast<uint32_t>(ms->n_parts - 1);
     if (last) *count = 0u;
     ms->last = last;
   }
   __syncthreads();
-  if (!ms->last) return;
+  if (ms->last) {
   // thread = (slice of the parts, row, dim quad): few rows leave threads for
   // several slices, which meet in the ring
-  const int b0 = ms->first_block, items = R * 32, slices = max(1, kFewThreads / items);
+  const int n_split = ms->n_parts, part0 = ms->first_part, items = R * 32, slices = max(1, kFewThreads / items);
   float4* s_o = reinterpret_cast<float4*>(ring);
   float2* s_ml = reinterpret_cast<float2*>(ring + kFewThreads * 16);
   for (int i0 = 0; i0 < items; i0 += kFewThreads) {
@@ -508,8 +670,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         for (int e = 0; e < kAhead; ++e) {
           const int b = s0 + e * slices;
           const bool in = b < n_split;
-          ml[e] = in ? __ldcg(p.part_ml + (b0 + b) * kFewRows + row) : make_float2(-INFINITY, 0.f);
-          v[e] = in ? __ldcg(p.part_o + (static_cast<size_t>(b0 + b) * kFewRows + row) * 32 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const int part_b = b ? (part0 & ~1) + 2 * b : part0;
+          ml[e] = in ? __ldcg(p.part_ml + part_b * kFewRows + row) : make_float2(-INFINITY, 0.f);
+          v[e] = in ? __ldcg(p.part_o + (static_cast<size_t>(part_b) * kFewRows + row) * 32 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mx = M;
 #pragma unroll
@@ -530,8 +693,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       s_o[threadIdx.x] = a;
       s_ml[threadIdx.x] = make_float2(M, L);
       __syncthreads();
-      if (slice) return;
-      for (int y = 1; y < slices; ++y) {
+      for (int y = 1; y < slices && !slice; ++y) {
         const float4 b = s_o[y * items + i];
         const float2 ml = s_ml[y * items + i];
         const float mx = fmaxf(M, ml.x);
@@ -546,14 +708,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
     const size_t at = (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + x * 4;
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
   }
+  }
+  }
+  // the ring is the copies' again
+  fence_proxy_async_smem();
+  __syncthreads();
+  } while (next_segment<kFewLead>(p, pl, sg));
 }
 
-// Blocks of the few-rows kernel: as many as fit the SMs, or one per kv head of
-// every request where that is more.
-int few_grid(int B, int Hkv, int R) {
-  const int n = 2 * glance::num_sms();
-  return n < B * Hkv ? B * Hkv : n / Hkv * Hkv;
-}
+int few_grid() { return 2 * glance::num_sms(); }  // as many blocks as fit
 size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv * 4 + 255) / 256 * 256; }
 
 // ------------------------------------------------ many query rows per kv head
@@ -577,13 +740,8 @@ size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv 
 // (codes are widened once for both). A last tile without a neighbour has both
 // slots: they take its slot tiles in turn and join at the end.
 //
-// Work: the slots of every (request, kv head, query tile pair) in units of 32.
-// Where each such group can be cut into equal parts that fill the grid, a
-// block has one part; else the list of all groups is cut into equal runs and a
-// block's run may cross groups (a "segment" is its part in one group). In that
-// list a group counts kLead units more than it has, what starting and ending a
-// segment takes. The lengths are read on the device. A group that one block has whole is written
-// out there; the others' parts are merged by a second kernel.
+// A group that one block has whole is written out there; the others' parts are
+// merged by a second kernel.
 
 constexpr int kWideThreads = 512;
 // Registers per thread: 128 at launch (65,536 for the block), then shared out
@@ -601,26 +759,8 @@ constexpr uint32_t kOffMisc = kOffRaw + kRawStages * kRawBytes;
 constexpr uint32_t kWideMisc = 6144;
 constexpr uint32_t kWideSmem = 1024 + kOffMisc + kWideMisc;
 static_assert(kWideSmem <= 227 * 1024, "shared memory");
-constexpr int kMinUnits = 4;  // one tile
-constexpr int kLead = 8;
+constexpr int kWideMin = 4, kWideLead = 8;  // a part has a tile or more
 constexpr unsigned long long kWaitNs = 2000000000ull;
-
-struct WidePlan {
-  int T[kMaxB];
-  int units[kMaxB];       // of one group of request r; 0: no room, no output
-  long long base[kMaxB];  // length of the list before request r's groups
-  long long total;        // of the whole list
-  int runs;               // blocks that the list is cut for: none gets less than a tile and its lead
-  int tau;                // > 0: every group is cut into parts of tau units
-  int blocks0[kMaxB];     // tau > 0: blocks before request r's
-};
-
-// A block's part in one group: units [a, a + n) of group g of request r.
-struct Segment {
-  int r, g, a, n;
-  int left;   // length of the run after this segment
-  int index;  // of the block's segments
-};
 
 struct WideMisc {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
@@ -629,134 +769,10 @@ struct WideMisc {
   uint32_t tmem;
   int abort_flag, any;
   Segment seg;
-  WidePlan plan;
+  Plan plan;
   float2 ml[2][2][kBM];  // [segment parity][slot][row], slots that share a query tile
 };
 static_assert(sizeof(WideMisc) <= kWideMisc, "misc block");
-
-// a / b for a run's arithmetic: 64-bit division only where it is needed.
-__device__ __forceinline__ long long div_small(long long a, int b) {
-  return a <= 0xFFFFFFFFll ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
-
-// The plan, by one warp; every block comes to the same one.
-__device__ __forceinline__ void wide_plan(const Params& p, WidePlan* pl, int lane, int blocks) {
-  int units = 0, T = 0;
-  if (lane < p.B) {
-    T = *p.req[lane].t_len;
-    if (T >= 0 && T <= p.req[lane].t_cap - p.rows) units = (T + p.rows + kUnit - 1) / kUnit;
-  }
-  const int gpr = p.Hkv * p.n_qp;
-  const int sum = __reduce_add_sync(0xffffffffu, units);
-  const int length = units > 0 ? units + kLead : 0;
-  const long long total = static_cast<long long>(__reduce_add_sync(0xffffffffu, length)) * gpr;
-  const int active = __popc(__ballot_sync(0xffffffffu, units > 0));
-  const int per_group = blocks / gpr;
-  const int runs = static_cast<int>(min(static_cast<long long>(blocks), max(1ll, div_small(total, kMinUnits + kLead))));
-  int tau = 0;
-  if (per_group >= active && active > 0) {
-    // the least tau at which the groups' parts fit the grid: not under the mean,
-    // and at hi every request has one part
-    int lo = max(kMinUnits, (sum + per_group - 1) / per_group), hi = max(lo, __reduce_max_sync(0xffffffffu, units));
-    int mid = lo;
-    while (lo < hi) {
-      if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_group)
-        hi = mid;
-      else
-        lo = mid + 1;
-      mid = (lo + hi) >> 1;
-    }
-    if (lo <= div_small(total, runs)) tau = lo;
-  }
-  const int n = tau ? (units + tau - 1) / tau * gpr : 0;
-  int before = length, nb = n;  // inclusive scans over the requests
-#pragma unroll 1
-  for (int o = 1; o < kMaxB; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_up_sync(0xffffffffu, nb, o);
-    if (lane >= o) {
-      before += u;
-      nb += v;
-    }
-  }
-  if (lane < kMaxB) {
-    pl->T[lane] = T;
-    pl->units[lane] = units;
-    pl->base[lane] = static_cast<long long>(before - length) * gpr;
-    pl->blocks0[lane] = nb - n;
-  }
-  if (lane == 0) {
-    pl->total = total;
-    pl->runs = runs;
-    pl->tau = tau;
-  }
-}
-
-// First unit of block b's run (runs that may cross groups).
-__device__ __forceinline__ long long run_start(long long total, int b, int blocks) {
-  const long long q = div_small(total, blocks);
-  return q * b + div_small((total - q * blocks) * b, blocks);
-}
-
-__device__ __forceinline__ void step_group(const Params& p, const WidePlan& pl, Segment& s) {
-  if (++s.g == p.Hkv * p.n_qp) {
-    s.g = 0;
-    do ++s.r;
-    while (pl.units[s.r] == 0);
-  }
-}
-// The run's part from place `at` of the current group's stretch on, or of the
-// next group that it has units of.
-__device__ __forceinline__ bool take_segment(const Params& p, const WidePlan& pl, Segment& s, int at) {
-  for (;;) {
-    const int take = min(s.left, pl.units[s.r] + kLead - at), end = at + take - kLead;
-    s.left -= take;
-    s.a = max(at - kLead, 0);
-    s.n = end - s.a;
-    if (s.n > 0) {
-      ++s.index;
-      return true;
-    }
-    if (s.left == 0) return false;
-    step_group(p, pl, s);
-    at = 0;
-  }
-}
-__device__ __forceinline__ bool first_segment(const Params& p, const WidePlan& pl, int b, Segment& s) {
-  const int gpr = p.Hkv * p.n_qp;
-  s.index = 0;
-  int r = 0;
-  if (pl.tau) {
-    int n = 0, at = 0;
-    for (; r < p.B; ++r) {
-      n = (pl.units[r] + pl.tau - 1) / pl.tau;
-      at = b - pl.blocks0[r];
-      if (at < n * gpr) break;
-    }
-    if (r == p.B) return false;
-    s.r = r;
-    s.g = at / n;
-    s.a = at % n * pl.tau;
-    s.n = min(pl.tau, pl.units[r] - s.a);
-    s.left = 0;
-    return true;
-  }
-  if (b >= pl.runs || pl.total == 0) return false;
-  const long long x = run_start(pl.total, b, pl.runs);
-  const int len = static_cast<int>(run_start(pl.total, b + 1, pl.runs) - x);
-  while (r + 1 < p.B && x >= pl.base[r + 1]) ++r;  // requests without units share their base with the next
-  const long long in = x - pl.base[r];
-  const int length = pl.units[r] + kLead;
-  s.r = r;
-  s.g = static_cast<int>(div_small(in, length));
-  s.index = -1;
-  s.left = len;
-  return take_segment(p, pl, s, static_cast<int>(in - static_cast<long long>(s.g) * length));
-}
-__device__ __forceinline__ bool next_segment(const Params& p, const WidePlan& pl, Segment& s) {
-  if (s.left == 0) return false;
-  step_group(p, pl, s);
-  return take_segment(p, pl, s, 0);
-}
 
 // Slots of a segment: [k0, k1); its tiles start at k0, k0 + 128, ...
 struct Run {
@@ -959,15 +975,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == 3) {
-    wide_plan(p, &ms->plan, lane, blocks);
+    make_plan<kWideMin, kWideLead>(p, &ms->plan, lane, blocks);
     __syncwarp();
-    if (lane == 0) ms->any = first_segment(p, ms->plan, blockIdx.x, ms->seg);
+    if (lane == 0) ms->any = first_segment<kWideLead>(p, ms->plan, blockIdx.x, ms->seg);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
-  const WidePlan& pl = ms->plan;
+  const Plan& pl = ms->plan;
   const bool any = ms->any != 0;
 
   if (warp < 4) {
@@ -1026,7 +1042,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           if (k + 2 < items) issue_s(k + 2);
         }
         t0 += run.tiles;
-      } while (good && next_segment(p, pl, s));
+      } while (good && next_segment<kWideLead>(p, pl, s));
       if (!good) wide_fail(ms);
     } else if (warp == 2 && any) {
       // ---------------------------------------------------------- bulk copies
@@ -1055,7 +1071,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           }
           __syncwarp();
         }
-      } while (good && next_segment(p, pl, s));
+      } while (good && next_segment<kWideLead>(p, pl, s));
       if (!good) {
         wide_fail(ms);
         for (int u = max(0, h - kRawStages); u < h; ++u)  // the copies in flight land before the block leaves
@@ -1073,7 +1089,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           if (pl.tau) {
             n = (pl.units[s.r] + pl.tau - 1) / pl.tau;
           } else {
-            const long long end = pl.base[s.r] + (s.g + 1ll) * (pl.units[s.r] + kLead);
+            const long long end = pl.base[s.r] + (s.g + 1ll) * (pl.units[s.r] + kWideLead);
             for (;; n += 32) {
               const unsigned past = __ballot_sync(0xffffffffu, run_start(pl.total, blockIdx.x + n + lane, pl.runs) >= end);
               if (past) {
@@ -1083,7 +1099,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
             }
           }
           if (lane == 0) p.group[s.r * p.Hkv * p.n_qp + s.g] = make_int2(2 * blockIdx.x + (s.index ? 1 : 0), n);
-        } while (next_segment(p, pl, s));
+        } while (next_segment<kWideLead>(p, pl, s));
       }
       if (blockIdx.x == 0)
         for (int r = 0; r < p.B; ++r)
@@ -1135,7 +1151,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           __syncwarp();
           if (lane == 0) mbar_arrive(is_v ? &ms->v_full[st] : &ms->k_full[st]);
         }
-      } while (good && next_segment(p, pl, s));
+      } while (good && next_segment<kWideLead>(p, pl, s));
       if (!good) wide_fail(ms);
     }
   } else {
@@ -1393,7 +1409,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           named_bar(1, 256);  // both have read both O before either slot's next product
         }
         tc_fence_before();
-      } while (next_segment(p, pl, s));
+      } while (next_segment<kWideLead>(p, pl, s));
       if (!ok) wide_fail(ms);
     }
   }
@@ -1512,7 +1528,7 @@ bool few_rows(int rows, int G) { return rows * G <= kFewRows; }
 size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
   const int Hkv = kv[0].n_kv_heads;
   if (few_rows(rows, Hq / Hkv))
-    return few_counter_bytes(B, Hkv) + static_cast<size_t>(few_grid(B, Hkv, rows * (Hq / Hkv))) * kFewRows * (kD * 4 + sizeof(float2));
+    return few_counter_bytes(B, Hkv) + 2 * static_cast<size_t>(few_grid()) * kFewRows * (kD * 4 + sizeof(float2));
   const int n_qp = (rows * (Hq / Hkv) + 2 * kBM - 1) / (2 * kBM);
   return wide_group_bytes(B, Hkv, n_qp) + wide_parts() * kBM * (kD * 2 + sizeof(float2));
 }
@@ -1593,12 +1609,12 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
   cfg.numAttrs = 1;
   cudaError_t e;
   if (few_rows(rows, G)) {
-    const int grid = few_grid(B, Hkv, rows * G);
+    const int grid = few_grid();
     const auto kernel = rows * G <= 8 ? kv4_attention_few_kernel<1> : kv4_attention_few_kernel<2>;
     char* ws = static_cast<char*>(workspace);
     p.count = reinterpret_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float4*>(ws + few_counter_bytes(B, Hkv));
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(grid) * kFewRows * 32);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(grid) * kFewRows * 32);
     e = glance::ensure_smem(reinterpret_cast<const void*>(kernel), kFewSmem);
     if (e != cudaSuccess) return glance::cuda_fail(e, who);
     cfg.gridDim = dim3(grid);
