@@ -226,7 +226,8 @@ constexpr uint32_t kUnitScales = kUnit * glance::kKv4ScaleBytes;  // 256
 constexpr uint32_t kUnitBytes = 2 * (kUnitCodes + kUnitScales);
 constexpr uint32_t kFewRing = kFewWarps * kFewStages * kUnitBytes;  // 73,728
 constexpr uint32_t kFewMisc = 1024;
-constexpr uint32_t kFewSmem = kFewRing + kFewMisc;
+constexpr uint32_t kFewQ = 2 * 4 * 32 * 16;  // sixteen rows' Q fragments
+constexpr uint32_t kFewSmem = kFewRing + kFewMisc + kFewQ;
 constexpr uint32_t kWarpRing = kFewStages * kUnitBytes;
 constexpr uint32_t kWarpO = kFewRows * kD * 4;  // a finished warp's O, then its rows' maxima and sums, in its own ring
 static_assert(kWarpO + 2 * kFewRows * 4 <= kWarpRing, "a warp's result fits its ring");
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem;
   FewMisc* ms = reinterpret_cast<FewMisc*>(smem + kFewRing);
+  uint4* sq = reinterpret_cast<uint4*>(smem + kFewRing + kFewMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
     for (int s = 0; s < kFewStages; ++s) mbar_init(&ms->full[warp][s], 1);
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   // below, dims 32c ..; Q: row r, dims 32c ..; a lane's scores and O are of
   // query rows 2c and 2c + 1 (of each eight).
   const int r = lane >> 2, c = lane & 3;
-  uint32_t q[kN][16];
+  uint32_t q[16];  // of eight rows; of sixteen in shared memory, for want of registers
   float sc[kN][2];
   uint32_t seen[kN][2];  // visible tree rows (at most 16)
 #pragma unroll
@@ -394,7 +396,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        q[n][4 * e + i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
+        q[4 * e + i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
+    }
+    if (kN > 1 && warp == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sq[(4 * n + e) * 32 + lane] = make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -404,6 +410,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       seen[n][h] &= (1u << p.rows) - 1u;  // rows <= 16
     }
   }
+  if (kN > 1) __syncthreads();
   float o[8][kN][4];
 #pragma unroll
   for (int t = 0; t < 8; ++t)
@@ -455,8 +462,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         }
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          mma16816(s[kt][n], h[0][0], h[1][0], h[0][1], h[1][1], q[n][4 * j], q[n][4 * j + 1]);
-          mma16816(s[kt][n], h[0][2], h[1][2], h[0][3], h[1][3], q[n][4 * j + 2], q[n][4 * j + 3]);
+          const uint4 qf = kN > 1 ? sq[(4 * n + j) * 32 + lane] : make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+          mma16816(s[kt][n], h[0][0], h[1][0], h[0][1], h[1][1], qf.x, qf.y);
+          mma16816(s[kt][n], h[0][2], h[1][2], h[0][3], h[1][3], qf.z, qf.w);
         }
       }
     }
