@@ -90,10 +90,10 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* pl, int lane, i
   const int runs = static_cast<int>(min(static_cast<long long>(blocks), max(1ll, div_small(total, kMinUnits + kLead))));
   int tau = 0;
   if (per_group >= active && active > 0) {
-    // the least tau at which the groups' parts fit the grid: not under the mean,
-    // and at hi every request has one part
-    int lo = max(kMinUnits, (sum + per_group - 1) / per_group), hi = max(lo, __reduce_max_sync(0xffffffffu, units));
-    int mid = lo;
+    // the least tau at which the groups' parts fit the grid, if that is no more
+    // than a run of the list: not under the mean, and of use up to `limit` only
+    const int limit = static_cast<int>(min(div_small(total, runs), 1ll << 30));
+    int lo = max(kMinUnits, (sum + per_group - 1) / per_group), hi = limit + 1, mid = lo;
     while (lo < hi) {
       if (static_cast<int>(__reduce_add_sync(0xffffffffu, (units + mid - 1) / mid)) <= per_group)
         hi = mid;
@@ -101,7 +101,7 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* pl, int lane, i
         lo = mid + 1;
       mid = (lo + hi) >> 1;
     }
-    if (lo <= div_small(total, runs)) tau = lo;
+    if (lo <= limit) tau = lo;
   }
   const int n = tau ? (units + tau - 1) / tau * gpr : 0;
   int before = length, nb = n;  // inclusive scans over the requests
@@ -233,7 +233,10 @@ constexpr uint32_t kWarpO = kFewRows * kD * 4;  // a finished warp's O, then its
 static_assert(kWarpO + 2 * kFewRows * 4 <= kWarpRing, "a warp's result fits its ring");
 static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two blocks per SM");
 
-constexpr int kFewMin = kFewWarps, kFewLead = 12;  // a part has a piece for every warp
+// A part has a piece for every warp or more. (One part of 32 pieces instead of
+// four of 8 takes 11.5 instead of 8.7 us for one row on 1000 slots: a piece takes
+// a warp 1.3 us, the merge of the parts 2.)
+constexpr int kFewMin = kFewWarps, kFewLead = 12;
 
 struct FewMisc {
   uint64_t full[kFewWarps][kFewStages];
@@ -359,11 +362,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   const int u0 = sg.a, u1 = sg.a + sg.n;
   const bool whole = sg.n == pl.units[sg.r];
   const long long head0 = static_cast<long long>(head) * rq.head_stride;
-  if (lane == 0)
-    for (int s = 0; s < kFewStages; ++s)
-      if (u0 + warp + s * kFewWarps < u1)
-        few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + (stage + s) % kFewStages * kUnitBytes,
-                 &ms->full[warp][(stage + s) % kFewStages]);
   const int R = p.G * p.rows;
   const size_t q_base = static_cast<size_t>(sg.r) * p.rows * p.Hq + head * p.G;
   // Fragments: lane = 4 r + c. K: slots r (and r + 8) of sixteen, in the order
@@ -373,18 +371,32 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   uint32_t q[16];  // of eight rows; of sixteen in shared memory, for want of registers
   float sc[kN][2];
   uint32_t seen[kN][2];  // visible tree rows (at most 16)
+  uint4 v[kN][4];
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     const int row = 8 * n + r;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + 32 * c);
-    uint4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[n][e] = row < R ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int qr = 8 * n + 2 * c + h, i = qr % p.rows;
+      seen[n][h] = qr >= R ? 0u : rq.anc ? static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned long long*>(rq.anc) + i * p.W)) : 1u << i;
+    }
+  }
+  // the first copies go out behind these loads and before their use
+  if (lane == 0)
+    for (int s = 0; s < kFewStages; ++s)
+      if (u0 + warp + s * kFewWarps < u1)
+        few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + (stage + s) % kFewStages * kUnitBytes,
+                 &ms->full[warp][(stage + s) % kFewStages]);
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
     uint32_t top = 0;  // the largest magnitude's bits: in the order of the absolute values
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = row < R ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
-#pragma unroll
     for (int e = 0; e < 4; ++e) {
-      top = max(top, max(max(v[e].x & 0x7FFFu, v[e].y & 0x7FFFu), max(v[e].z & 0x7FFFu, v[e].w & 0x7FFFu)));
-      top = max(top, max(max(v[e].x & 0x7FFF0000u, v[e].y & 0x7FFF0000u), max(v[e].z & 0x7FFF0000u, v[e].w & 0x7FFF0000u)) >> 16);
+      top = max(top, max(max(v[n][e].x & 0x7FFFu, v[n][e].y & 0x7FFFu), max(v[n][e].z & 0x7FFFu, v[n][e].w & 0x7FFFu)));
+      top = max(top, max(max(v[n][e].x & 0x7FFF0000u, v[n][e].y & 0x7FFF0000u), max(v[n][e].z & 0x7FFF0000u, v[n][e].w & 0x7FFF0000u)) >> 16);
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
     const float factor = score_factor(amax, qf, p.scale_log2, rq.k_global);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+      const uint32_t w[4] = {v[n][e].x, v[n][e].y, v[n][e].z, v[n][e].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         q[4 * e + i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
@@ -405,8 +417,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       sc[n][h] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + h));
-      const int qr = 8 * n + 2 * c + h, i = qr % p.rows;
-      seen[n][h] = qr >= R ? 0u : rq.anc ? static_cast<uint32_t>(rq.anc[i * p.W]) : 1u << i;
       seen[n][h] &= (1u << p.rows) - 1u;  // rows <= 16
     }
   }
@@ -437,36 +447,39 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
     }
     const int key0 = u * kUnit;
     float s[2][kN][4];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) s[kt][n][0] = s[kt][n][1] = s[kt][n][2] = s[kt][n][3] = 0.f;
-      uint4 kw[2];
+    {
+      uint4 kw[2][2];
       uint32_t ks[2][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int slot = 16 * kt + 8 * b + k_slot;
-        kw[b] = *reinterpret_cast<const uint4*>(st + slot * 64 + c * 16);
-        const uint32_t x = scales2_to_f16(*reinterpret_cast<const uint16_t*>(st + 2 * kUnitCodes + slot * 8 + 2 * c));
-        ks[b][0] = prmt(x, x, 0x1010);
-        ks[b][1] = prmt(x, x, 0x3232);
-      }
+      for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t h[2][4];
+        for (int n = 0; n < kN; ++n) s[kt][n][0] = s[kt][n][1] = s[kt][n][2] = s[kt][n][3] = 0.f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          codes8_to_f16(j == 0 ? kw[b].x : j == 1 ? kw[b].y : j == 2 ? kw[b].z : kw[b].w, h[b]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[b][i] = mul_f16x2(h[b][i], ks[b][j >> 1]);
-        }
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          const uint4 qf = kN > 1 ? sq[(4 * n + j) * 32 + lane] : make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
-          mma16816(s[kt][n], h[0][0], h[1][0], h[0][1], h[1][1], qf.x, qf.y);
-          mma16816(s[kt][n], h[0][2], h[1][2], h[0][3], h[1][3], qf.z, qf.w);
+          const int slot = 16 * kt + 8 * b + k_slot;
+          kw[kt][b] = *reinterpret_cast<const uint4*>(st + slot * 64 + c * 16);
+          ks[kt][b] = scales2_to_f16(*reinterpret_cast<const uint16_t*>(st + 2 * kUnitCodes + slot * 8 + 2 * c));
         }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {  // two chains of products side by side
+          uint32_t h[2][4];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            codes8_to_f16(j == 0 ? kw[kt][b].x : j == 1 ? kw[kt][b].y : j == 2 ? kw[kt][b].z : kw[kt][b].w, h[b]);
+            const uint32_t f = prmt(ks[kt][b], ks[kt][b], j < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[b][i] = mul_f16x2(h[b][i], f);
+          }
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            const uint4 qf = kN > 1 ? sq[(4 * n + j) * 32 + lane] : make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+            mma16816(s[kt][n], h[0][0], h[1][0], h[0][1], h[1][1], qf.x, qf.y);
+            mma16816(s[kt][n], h[0][2], h[1][2], h[0][3], h[1][3], qf.z, qf.w);
+          }
+        }
     }
     // s[kt][n][e]: slot 16 kt + 8 (e >> 1) + k_slot, query row 8n + 2c + (e & 1)
     uint32_t zero_v = 0u;  // slots whose V must not be multiplied
