@@ -314,7 +314,13 @@ class Views(list):
 
 
 def _views(x, kind):
-    """The C array of a Views, a list of views, or one view; its items checked."""
+    """x (a Views, a list of views, or one view) as a Views; its items checked.
+    The array of one view alone is kept with it."""
+    if isinstance(x, kind):
+        alone = x.__dict__.get("_alone")
+        if alone is None:
+            alone = x._alone = Views([x])
+        return alone
     if not isinstance(x, Views):
         x = Views(x if isinstance(x, (list, tuple)) else [x])
     if not isinstance(x[0], kind):
@@ -599,7 +605,7 @@ def _on(stream, *tensors):
     for t in tensors:
         if t.get_device() != dev or dev < 0:
             raise ValueError("glance: every array argument must be a CUDA tensor of one device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("glance: the tensors are not on the current device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -705,17 +711,20 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
     t = trees[0]
     if len(layers) % B:
         raise ValueError("glance: layers must hold the same number of views for every request")
-    ints = ((argmax, B * t.rows), (n_accepted, B), (accepted_tok, B * t.L), (new_root, B)) + (
-        ((gated, B),) if gated is not None else ())
-    for x, n in ints:
-        if x.dtype != torch.int32 or x.numel() < n or not x.is_contiguous():
-            raise ValueError("glance: argmax, n_accepted, accepted_tok, new_root and gated must be contiguous int32 "
-                             "[B, N + 1], [B], [B, L], [B], [B]")
-    tensors = [x for x, _ in ints] + [ws, layers[0].k]
+    i32 = torch.int32
+    for x, n in ((argmax, B * t.rows), (n_accepted, B), (accepted_tok, B * t.L), (new_root, B)):
+        if x.dtype != i32 or x.numel() < n or not x.is_contiguous():
+            raise ValueError("glance: argmax, n_accepted, accepted_tok and new_root must be contiguous int32 "
+                             "[B, N + 1], [B], [B, L], [B]")
+    tensors = [argmax, n_accepted, accepted_tok, new_root, ws, layers[0].k]
     if gap is not None:
         if gap.dtype != torch.float32 or gap.numel() < B * t.rows or not gap.is_contiguous():
             raise ValueError("glance: gap must be contiguous float32 [B, N + 1]")
         tensors.append(gap)
+    if gated is not None:
+        if gated.dtype != i32 or gated.numel() < B or not gated.is_contiguous():
+            raise ValueError("glance: gated must be contiguous int32 [B]")
+        tensors.append(gated)
     s = _on(stream, *tensors)
     _check(lib().glance_kv4_accept_commit(ctypes.addressof(trees.c), B, argmax.data_ptr(),
                                           None if gap is None else gap.data_ptr(), gate_threshold,
