@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kMaxB = 16;
 constexpr int kThreads = 128;
-constexpr int kMaxRows = 4;  // rows of one block
+constexpr int kMaxRows = 2;  // rows of one block
 
 struct Cache {
   char* k;
@@ -84,19 +84,40 @@ struct Vec<__nv_bfloat16> {
 // A head is held by kLanes threads, thread i with dims kV i .. kV i + kV - 1
 // and the same dims of the other half, so a rotation pair is in one thread.
 // Block: up to kMaxRows rows of one request; their cosines and sines go to
-// shared memory first (each is used by every q and k head of the row).
+// shared memory first (each is used by every q and k head of the row). Bound by
+// memory: each element is read and written once, so a thread has the loads of
+// kAhead heads (96 bytes) in flight, the first ones before the cosines.
+constexpr int kAhead = 3;
+
 template <typename T, int kHeadDim>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kV = Vec<T>::n;
   constexpr int kHalf = kHeadDim / 2;
   constexpr int kLanes = kHalf / kV;
   constexpr int kSlots = kThreads / kLanes;  // heads at a time
+  constexpr int kHeadBytes = kHeadDim * sizeof(T), kHalfBytes = kHeadBytes / 2;
   __shared__ float2 s_cs[kMaxRows][kHalf];
   pdl_wait_prior();
   pdl_launch_dependents();
   const int req = blockIdx.x / p.blocks_per_req;
   const int row0 = (blockIdx.x - req * p.blocks_per_req) * p.block_rows;
   const int n_rows = min(p.block_rows, p.M - row0);
+  const int i = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  const int n_heads = p.Hq + 2 * p.Hkv;
+  const char* src = p.qkv + (static_cast<long long>(req) * p.M + row0) * p.row_stride + i * 16;
+  uint4 lo[kAhead], hi[kAhead];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + u * kSlots + slot;
+      lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+      if (h < n_heads) {
+        lo[u] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * kHeadBytes));
+        hi[u] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * kHeadBytes + kHalfBytes));
+      }
+    }
+  };
+  load(0);
   const Cache& kv = p.kv[req];
   const int T0 = *kv.t_len;
   const bool room = T0 >= 0 && T0 <= kv.t_cap - p.M;
@@ -109,65 +130,61 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     const float x = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;
     float s, c;
     sincospif(x, &s, &c);
-    s_cs[r][j] = make_float2(c, s);
+    s_cs[r][j % kV * kLanes + j / kV] = make_float2(c, s);  // a head's threads read next to each other
   }
   __syncthreads();
-  const int i = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int n_heads = p.Hq + 2 * p.Hkv;
-  constexpr int kHeadBytes = kHeadDim * sizeof(T), kHalfBytes = kHeadBytes / 2;
   for (int r = 0; r < n_rows; ++r) {
     const long long row = static_cast<long long>(req) * p.M + row0 + r;
-    const char* src = p.qkv + row * p.row_stride + i * 16;
     const int at = T0 + row0 + r;  // cache slot
-    for (int h0 = 0; h0 < n_heads; h0 += kSlots) {  // all threads of a warp take part in the sum's shuffles
-      const int h = h0 + slot;
-      const bool live = h < n_heads;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (live) {
-        lo = __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * kHeadBytes));
-        hi = __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * kHeadBytes + kHalfBytes));
-      }
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-      float a[kV], b[kV];
-      Vec<T>::unpack(lo, a);
-      Vec<T>::unpack(hi, b);
-      const float* w = is_q ? p.q_norm : p.k_norm;
-      float ss = 0.f;
+    for (int h0 = 0; h0 < n_heads; h0 += kAhead * kSlots) {
+      if (h0) load(h0);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+      for (int u = 0; u < kAhead; ++u) {  // all threads of a warp take part in the sum's shuffles
+        const int h = h0 + u * kSlots + slot;
+        const bool live = h < n_heads, is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+        float a[kV], b[kV];
+        Vec<T>::unpack(lo[u], a);
+        Vec<T>::unpack(hi[u], b);
+        const float* w = is_q ? p.q_norm : p.k_norm;
+        float ss = 0.f;
 #pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (live && !is_v) {
-        if (w) {
-          const float inv = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
+        for (int e = 0; e < kV; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!live) continue;
+        if (!is_v) {
+          if (w) {
+            const float inv = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+              a[e] *= inv * __ldg(w + i * kV + e);
+              b[e] *= inv * __ldg(w + i * kV + kHalf + e);
+            }
+          }
 #pragma unroll
           for (int e = 0; e < kV; ++e) {
-            a[e] *= inv * __ldg(w + i * kV + e);
-            b[e] *= inv * __ldg(w + i * kV + kHalf + e);
+            const float2 cs = s_cs[r][e * kLanes + i];
+            const float x = a[e], y = b[e];
+            a[e] = x * cs.x - y * cs.y;
+            b[e] = y * cs.x + x * cs.y;
           }
+          lo[u] = Vec<T>::pack(a);
+          hi[u] = Vec<T>::pack(b);
         }
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-          const float2 cs = s_cs[r][i * kV + e];
-          const float x = a[e], y = b[e];
-          a[e] = x * cs.x - y * cs.y;
-          b[e] = y * cs.x + x * cs.y;
+        char* dst;
+        if (is_q) {
+          dst = p.q_out + (row * p.Hq + h) * kHeadBytes;
+        } else {
+          if (!room || !GLANCE_IN_BOUNDS(at, kv.t_cap)) continue;
+          const int g = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
+          dst = (is_v ? kv.v : kv.k) + g * kv.head_stride + at * kv.row_stride;
         }
-        lo = Vec<T>::pack(a);
-        hi = Vec<T>::pack(b);
+        *reinterpret_cast<uint4*>(dst + i * 16) = lo[u];
+        *reinterpret_cast<uint4*>(dst + i * 16 + kHalfBytes) = hi[u];
       }
-      if (!live) continue;
-      char* dst;
-      if (is_q) {
-        dst = p.q_out + (row * p.Hq + h) * kHeadBytes;
-      } else {
-        if (!room || !GLANCE_IN_BOUNDS(at, kv.t_cap)) continue;
-        const int g = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        dst = (is_v ? kv.v : kv.k) + g * kv.head_stride + at * kv.row_stride;
-      }
-      *reinterpret_cast<uint4*>(dst + i * 16) = lo;
-      *reinterpret_cast<uint4*>(dst + i * 16 + kHalfBytes) = hi;
     }
+    src += p.row_stride;
+    if (r + 1 < n_rows) load(0);
   }
 }
 
