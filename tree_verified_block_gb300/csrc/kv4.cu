@@ -62,20 +62,14 @@ __device__ __forceinline__ float quotient(float x, float d, float inv) {
 // One group of 16 bf16 values (8 words) to 16 codes (2 words) and a scale.
 __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float inv_g, uint32_t (&codes)[2],
                                            uint32_t& scale) {
-  float t[16];
-  float amax = 0.f;
-  bool finite = true;
+  // the largest magnitude from the bit patterns, two at a time: their order is
+  // that of the absolute values, infinities and NaN on top; rounding keeps the
+  // order, so its product is the largest product
+  uint32_t top = x[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t[2 * i] = __uint_as_float(x[i] << 16);
-    t[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    t[i] *= inv_g;
-    amax = fmaxf(amax, fabsf(t[i]));  // drops NaN
-    finite = finite && fabsf(t[i]) < INFINITY;
-  }
+  for (int i = 1; i < 8; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
+  const float amax = __uint_as_float(max(top & 0xFFFF0000u, top << 16)) * inv_g;
+  const bool finite = amax < INFINITY;
   scale = finite ? scale1(__fdiv_rn(amax, 6.f)) & 0xFFu : 0x7Fu;
   const float s = f16x2_to_f32(scales2_to_f16(scale)).x;
   const bool any = finite && s > 0.f;
@@ -83,7 +77,8 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float inv_g, 
   codes[0] = codes[1] = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t c = code2(quotient(t[2 * i], s, inv_s), quotient(t[2 * i + 1], s, inv_s));
+    const float lo = __uint_as_float(x[i] << 16) * inv_g, hi = __uint_as_float(x[i] & 0xFFFF0000u) * inv_g;
+    const uint32_t c = code2(quotient(lo, s, inv_s), quotient(hi, s, inv_s));
     codes[i >> 2] |= c << (8 * (i & 3));
   }
   if (!any) codes[0] = codes[1] = 0u;
@@ -107,17 +102,23 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_rows_kernel(const __gri
   const long long slot0 = head * p.head_stride + T;
   uint32_t x[kPasses][8];
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u)
-    if (row0 + u * kRowsPerPass < p.rows) ld32(src + static_cast<size_t>(row0 + u * kRowsPerPass) * 256, x[u]);
+  for (int u = 0; u < kPasses; ++u)  // behind the last row: that row again, not stored
+    ld32(src + static_cast<size_t>(min(row0 + u * kRowsPerPass, p.rows - 1)) * 256, x[u]);
 #pragma unroll
   for (int u = 0; u < kPasses; ++u) {
     const int row = row0 + u * kRowsPerPass;
-    if (row >= p.rows || !GLANCE_IN_BOUNDS(T + row, p.t_cap)) continue;
+    if (__all_sync(0xffffffffu, row >= p.rows)) break;
     uint32_t codes[2], scale;
     quantise16(x[u], p.inv_global[is_v], codes, scale);
+    // the row's eight scales to its first thread: one store
+    scale <<= 8 * (grp & 3);
+    scale |= __shfl_xor_sync(0xffffffffu, scale, 1);
+    scale |= __shfl_xor_sync(0xffffffffu, scale, 2);
+    const uint32_t upper = __shfl_xor_sync(0xffffffffu, scale, 4);
+    if (row >= p.rows || !GLANCE_IN_BOUNDS(T + row, p.t_cap)) continue;
     const long long slot = slot0 + row;
     *reinterpret_cast<uint2*>(p.cache[lkv].codes + slot * glance::kKv4CodeBytes + grp * 8) = make_uint2(codes[0], codes[1]);
-    p.cache[lkv].scales[slot * glance::kKv4ScaleBytes + grp] = static_cast<unsigned char>(scale);
+    if (grp == 0) *reinterpret_cast<uint2*>(p.cache[lkv].scales + slot * glance::kKv4ScaleBytes) = make_uint2(scale, upper);
   }
 }
 
