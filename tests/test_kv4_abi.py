@@ -183,6 +183,44 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes(glib):
         g._binding._views(g.Views([type("X", (), {"c": t_c()})()]), g.KV4Layer)
 
 
+def test_a_theta_without_finite_frequencies_is_refused(glib):
+    import tree_verified_block_gb300 as g
+    for theta in (5e-324, 1e-320):
+        with pytest.raises(g.GlanceError):
+            g.Rope(128, theta)
+    assert g.Rope(128, 1e-300).c.turn[0] == g.Rope(128, 1e4).c.turn[0]  # frequency 0 is 1 for every theta
+
+
+def test_views_are_of_one_kind_and_one_device(glib):
+    import tree_verified_block_gb300._binding as b
+
+    class Where:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
+
+    def layer(*devs):
+        x = object.__new__(b.KV4Layer)
+        x.k, x.v, x.t_len = map(Where, devs)
+        x.c = view()
+        return x
+    tree = object.__new__(b.Tree)
+    tree.anc, tree.c = Where(0), b.TreeC()
+    assert b.Views([layer(0, 0, 0), layer(0, 0, 0)]).dev == 0
+    for bad in ([layer(0, 0, 1)], [layer(0, 0, 0), layer(1, 1, 1)]):
+        with pytest.raises(ValueError):
+            b.Views(bad)
+    with pytest.raises(TypeError):
+        b.Views([layer(0, 0, 0), tree])
+
+
+def test_attention_workspace_refuses_more_heads_than_the_call(glib):
+    x = view(n_kv_heads=1025)
+    assert glib.glance_kv4_tree_attention_workspace_bytes(1, 1, 1025, ctypes.byref(x)) == 0
+
+
 def t_c():
     import tree_verified_block_gb300._binding as b
     return b.TreeC()

@@ -279,8 +279,8 @@ class KV4Layer:
                     Hkv > 1 and t.stride(0) % w):
                 raise ValueError("glance: a 4-bit cache has one-byte codes [n_kv_heads, t_cap, 64] and scales "
                                  "[n_kv_heads, t_cap, 8] with whole rows next to each other")
-            if t.device != k.device:
-                raise ValueError("glance: codes and scales must be on one device")
+            if t.device != k.device or t_len.device != k.device:
+                raise ValueError("glance: codes, scales and t_len must be on one device")
         if len(heads) != 1:
             raise ValueError("glance: codes and scales need the same number of slots between heads")
         if Hkv == 1 and t_cap % 2:
@@ -302,14 +302,20 @@ class KV4Layer:
 
 
 class Views(list):
-    """A list of Tree, KVLayer or KV4Layer objects with their C array laid out
-    once: calls that take a list of them accept it without building the array
-    again. The list must not be changed afterwards."""
+    """A list of Tree, KVLayer or KV4Layer objects of one device with their C
+    array laid out once: calls that take a list of them accept it without
+    building the array again. The list must not be changed afterwards."""
 
     def __init__(self, items):
         super().__init__(items)
         if not self:
             raise ValueError("glance: an empty list of views")
+        if not all(isinstance(x, type(self[0])) and isinstance(x, (Tree, KVLayer, KV4Layer)) for x in self):
+            raise TypeError("glance: views are Tree, KVLayer or KV4Layer objects, of one kind")
+        on = {t.get_device() for x in self for t in ((x.anc,) if isinstance(x, Tree) else (x.k, x.v, x.t_len))}
+        if len(on) != 1:
+            raise ValueError("glance: every view of a list must be on one device")
+        self.dev = on.pop()
         self.c = (type(self[0].c) * len(self))(*[x.c for x in self])
 
 
@@ -598,10 +604,10 @@ def dense_swiglu(h, W_gate, W_up, in_sumsq, eps, act, stream=None):
 
 # ------------------------------------------- norm + rotary, 4-bit caches
 
-def _on(stream, *tensors):
+def _on(stream, views, *tensors):
     """The stream to launch on: the given one, else the tensors' device's
-    current one. All tensors must be on the current device."""
-    dev = tensors[0].get_device()
+    current one. All tensors and views must be on the current device."""
+    dev = views.dev
     for t in tensors:
         if t.get_device() != dev or dev < 0:
             raise ValueError("glance: every array argument must be a CUDA tensor of one device")
@@ -625,13 +631,13 @@ def qk_norm_rope(qkv, n_q_heads, q_norm, k_norm, eps, pos, rope, q_out, kv, stre
         raise ValueError("glance: pos must be contiguous int32 [n_axes, B * M]")
     if q_out.dtype != qkv.dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
         raise ValueError("glance: q_out must be contiguous [B * M, n_q_heads, head_dim] of qkv's dtype")
-    tensors = [qkv, pos, q_out, kv[0].k]
+    tensors = [qkv, pos, q_out]
     for w in (q_norm, k_norm):
         if w is not None:
             if w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous():
                 raise ValueError("glance: norm weights must be contiguous float32 [head_dim]")
             tensors.append(w)
-    s = _on(stream, *tensors)
+    s = _on(stream, kv, *tensors)
     stride = qkv.stride(0) if rows > 1 else qkv.shape[1]
     _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _dtype_code(qkv), B, rows // B, stride, n_q_heads,
                                      None if q_norm is None else q_norm.data_ptr(),
@@ -650,7 +656,7 @@ def kv4_write_rows(src, layers, rows, stream=None):
     every layer's 4-bit cache at slots T..T+rows-1 (T read on the device)."""
     layers = _views(layers, KV4Layer)
     _rows16(src, len(layers), layers, rows)
-    s = _on(stream, src, layers[0].k)
+    s = _on(stream, layers, src)
     _check(lib().glance_kv4_write_rows(src.data_ptr(), ctypes.addressof(layers.c), len(layers), rows, s))
 
 
@@ -659,7 +665,7 @@ def kv4_read_rows(layers, first, rows, dst, stream=None):
     first .. first + rows - 1 of every layer's 4-bit cache."""
     layers = _views(layers, KV4Layer)
     _rows16(dst, len(layers), layers, rows)
-    s = _on(stream, dst, layers[0].k)
+    s = _on(stream, layers, dst)
     _check(lib().glance_kv4_read_rows(ctypes.addressof(layers.c), len(layers), first, rows, dst.data_ptr(), s))
 
 
@@ -691,8 +697,10 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
         trees = _views(trees, Tree)
         if len(trees) != B or trees[0].rows != rows:
             raise ValueError("glance: need one tree of q's N + 1 rows per request")
+        if trees.dev != kvs.dev:
+            raise ValueError("glance: the trees must be on the caches' device")
         c = trees.c
-    s = _on(stream, q, out, ws, kvs[0].k)
+    s = _on(stream, kvs, q, out, ws)
     _check(lib().glance_kv4_tree_attention(q.data_ptr(), q.shape[-2], ctypes.addressof(kvs.c), ctypes.addressof(c), B,
                                            scale, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s))
 
@@ -716,7 +724,9 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
         if x.dtype != i32 or x.numel() < n or not x.is_contiguous():
             raise ValueError("glance: argmax, n_accepted, accepted_tok and new_root must be contiguous int32 "
                              "[B, N + 1], [B], [B, L], [B]")
-    tensors = [argmax, n_accepted, accepted_tok, new_root, ws, layers[0].k]
+    if trees.dev != layers.dev:
+        raise ValueError("glance: the trees must be on the caches' device")
+    tensors = [argmax, n_accepted, accepted_tok, new_root, ws]
     if gap is not None:
         if gap.dtype != torch.float32 or gap.numel() < B * t.rows or not gap.is_contiguous():
             raise ValueError("glance: gap must be contiguous float32 [B, N + 1]")
@@ -725,7 +735,7 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
         if gated.dtype != i32 or gated.numel() < B or not gated.is_contiguous():
             raise ValueError("glance: gated must be contiguous int32 [B]")
         tensors.append(gated)
-    s = _on(stream, *tensors)
+    s = _on(stream, layers, *tensors)
     _check(lib().glance_kv4_accept_commit(ctypes.addressof(trees.c), B, argmax.data_ptr(),
                                           None if gap is None else gap.data_ptr(), gate_threshold,
                                           ctypes.addressof(layers.c), len(layers) // B, n_accepted.data_ptr(),

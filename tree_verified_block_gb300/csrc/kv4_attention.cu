@@ -32,7 +32,7 @@ struct Params {
   __nv_bfloat16* out;
   float4* part_o;   // unnormalised partial O of a block (few rows)
   float2* part_ml;  // a part's rows' (maximum in log2, sum of weights)
-  uint32_t* count;  // [B][Hkv] blocks of a head that are done
+  uint32_t* count;  // [B][Hkv] blocks of a head that are done; zero between calls
   int B, rows, Hq, Hkv, G, W;
   int n_qt, n_qp;   // query tiles of 128 rows per kv head, and pairs of them
   uint4* part;      // parts of 128 rows: O / l as f16, [16 octets][128 rows]
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   unsigned char* my_ring = ring + warp * kWarpRing;
   int stage = 0;
   uint32_t parity = 0;
+  bool dead = false;  // a wait of this warp ran out: its barriers' phases are unknown, and it copies no more
   do {
   const Request& rq = p.req[sg.r];
   const int head = sg.g, T = pl.T[sg.r], n_keys = T + p.rows;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
     }
   }
   // the first copies go out behind these loads and before their use
-  if (lane == 0)
+  if (lane == 0 && !dead)
     for (int s = 0; s < kFewStages; ++s)
       if (u0 + warp + s * kFewWarps < u1)
         few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + (stage + s) % kFewStages * kUnitBytes,
@@ -436,13 +437,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   // four slots of a lane's V fragment are then 4 apart and the four lanes' next
   // to each other, which loads without bank conflicts
   const int k_slot = 4 * (r & 1) + (r >> 1);
-  for (int u = u0 + warp; u < u1; u += kFewWarps) {
+  for (int u = u0 + warp; u < u1 && !dead; u += kFewWarps) {
     unsigned char* st = my_ring + stage * kUnitBytes;
     if (!__all_sync(0xffffffffu, mbar_wait(&ms->full[warp][stage], parity))) {
       if (lane == 0) report(GLANCE_DEV_PIPELINE_TIMEOUT);
       for (int s = 1; s < kFewStages; ++s)  // the copies in flight land before the block leaves
         if (u + s * kFewWarps < u1)
           (void)mbar_wait(&ms->full[warp][(stage + s) % kFewStages], parity ^ (stage + s >= kFewStages), 50000000ull);
+      dead = true;
       break;
     }
     const int key0 = u * kUnit;
@@ -738,7 +740,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
 }
 
 int few_grid() { return 2 * glance::num_sms(); }  // as many blocks as fit
-size_t few_counter_bytes(int B, int Hkv) { return (static_cast<size_t>(B) * Hkv * 4 + 255) / 256 * 256; }
+// The counters come first in a workspace of any call, those of the largest one,
+// so that calls of different shapes may take turns on one workspace.
+constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHeads * sizeof(uint32_t);
 
 // ------------------------------------------------ many query rows per kv head
 //
@@ -1360,7 +1364,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms->p_ready[x]);
         }
-        if (!ok && pair) break;  // slots that share a query tile leave together, at the barrier below
+        if (!ok && pair) break;
+        // a row that sees a prefix slot has a weight of about 1 unless all its
+        // scores are -infinity: then it is no number
+        if (l == 0.f && j0 < run.tiles && run.key0(j0) < T) l = __uint_as_float(0x7FC00000u);
         // ------------------------------------------------ the segment's output
         const bool whole = s.n == pl.units[s.r];
         bool valid;
@@ -1396,8 +1403,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           float2(*ml)[kBM] = ms->ml[s.index & 1];
           ml[x][lrow] = make_float2(m, l);
           ok = ok && wide_wait(&ms->o_done[0], n_o[0]++ & 1, ms) && (run.tiles < 2 || wide_wait(&ms->o_done[1], n_o[1]++ & 1, ms));
-          ok = !named_bar_or(1, 256, !ok);
-          if (!ok) break;
+          ok = !named_bar_or(1, 256, !ok);  // both go on, or both leave
+          if (!ok) {
+            s.left = 0;
+            break;
+          }
           tc_fence_after();
           const float2 a = ml[0][lrow], b = ml[1][lrow];
           const float M = fmaxf(a.x, b.x);
@@ -1431,7 +1441,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         }
         tc_fence_before();
       } while (next_segment<kWideLead>(p, pl, s));
-      if (!ok) wide_fail(ms);
+      if (!ok) {
+        // after a failed wait the other slot gives up as well, but may first come
+        // to the barrier of a query tile that both slots have
+        wide_fail(ms);
+        while (next_segment<kWideLead>(p, pl, s))
+          if (2 * (s.g % p.n_qp) + 1 >= p.n_qt) {
+            (void)named_bar_or(1, 256, true);
+            break;
+          }
+      }
     }
   }
   tc_fence_before();
@@ -1549,9 +1568,9 @@ bool few_rows(int rows, int G) { return rows * G <= kFewRows; }
 size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
   const int Hkv = kv[0].n_kv_heads;
   if (few_rows(rows, Hq / Hkv))
-    return few_counter_bytes(B, Hkv) + 2 * static_cast<size_t>(few_grid()) * kFewRows * (kD * 4 + sizeof(float2));
+    return kCounterBytes + 2 * static_cast<size_t>(few_grid()) * kFewRows * (kD * 4 + sizeof(float2));
   const int n_qp = (rows * (Hq / Hkv) + 2 * kBM - 1) / (2 * kBM);
-  return wide_group_bytes(B, Hkv, n_qp) + wide_parts() * kBM * (kD * 2 + sizeof(float2));
+  return kCounterBytes + wide_group_bytes(B, Hkv, n_qp) + wide_parts() * kBM * (kD * 2 + sizeof(float2));
 }
 
 }  // namespace
@@ -1559,7 +1578,8 @@ size_t workspace_bytes_of(int B, int rows, int Hq, const glance_kv4* kv) {
 extern "C" size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_heads, const glance_kv4* kv) {
   if (!kv || B < 1 || B > kMaxB || n_rows < 1 || n_rows > 256 || n_q_heads < 1) return 0;
   for (int r = 0; r < B; ++r)
-    if (kv[r].n_kv_heads != kv[0].n_kv_heads || kv[r].n_kv_heads < 1 || n_q_heads % kv[r].n_kv_heads ||
+    if (kv[r].n_kv_heads != kv[0].n_kv_heads || kv[r].n_kv_heads < 1 || kv[r].n_kv_heads > glance::kKv4MaxHeads ||
+        n_q_heads % kv[r].n_kv_heads ||
         kv[r].t_cap < n_rows || kv[r].t_cap > glance::kKv4MaxCap)
       return 0;
   return workspace_bytes_of(B, n_rows, n_q_heads, kv);
@@ -1634,7 +1654,7 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     const auto kernel = rows * G <= 8 ? kv4_attention_few_kernel<1> : kv4_attention_few_kernel<2>;
     char* ws = static_cast<char*>(workspace);
     p.count = reinterpret_cast<uint32_t*>(ws);
-    p.part_o = reinterpret_cast<float4*>(ws + few_counter_bytes(B, Hkv));
+    p.part_o = reinterpret_cast<float4*>(ws + kCounterBytes);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(grid) * kFewRows * 32);
     e = glance::ensure_smem(reinterpret_cast<const void*>(kernel), kFewSmem);
     if (e != cudaSuccess) return glance::cuda_fail(e, who);
@@ -1644,7 +1664,7 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
     e = cudaLaunchKernelEx(&cfg, kernel, p);
   } else {
     const int grid = glance::num_sms();
-    char* ws = static_cast<char*>(workspace);
+    char* ws = static_cast<char*>(workspace) + kCounterBytes;
     p.group = reinterpret_cast<int2*>(ws);
     p.part = reinterpret_cast<uint4*>(ws + wide_group_bytes(B, Hkv, p.n_qp));
     p.part_ml = reinterpret_cast<float2*>(p.part + wide_parts() * kBM * 16);

@@ -24,6 +24,7 @@ constexpr int kKv4D = 128;           // head_dim
 constexpr int kKv4CodeBytes = 64;    // codes of one row
 constexpr int kKv4ScaleBytes = 8;    // scales of one row
 constexpr int kKv4MaxCap = 1 << 30;  // slots per head
+constexpr int kKv4MaxHeads = 1024;   // kv heads
 
 // Checks of one view, shared by the 4-bit calls.
 inline glance_status check_kv4(const char* who, const glance_kv4& x, int rows, int index) {
@@ -31,9 +32,10 @@ inline glance_status check_kv4(const char* who, const glance_kv4& x, int rows, i
     return fail(GLANCE_ERR_INVALID_ARG, "%s: null array in view %d", who, index);
   if (x.head_dim != kKv4D)
     return fail(GLANCE_ERR_UNSUPPORTED, "%s: 4-bit caches need head_dim 128 (view %d)", who, index);
-  if (x.n_kv_heads < 1 || x.n_kv_heads > 1024 || x.t_cap < rows || x.head_stride < x.t_cap || (x.head_stride & 1))
+  if (x.n_kv_heads < 1 || x.n_kv_heads > kKv4MaxHeads || x.t_cap < rows || x.head_stride < x.t_cap || (x.head_stride & 1))
     return fail(GLANCE_ERR_INVALID_ARG,
-                "%s: need 1 <= n_kv_heads <= 1024, t_cap >= rows and an even head_stride >= t_cap (view %d)", who, index);
+                "%s: need 1 <= n_kv_heads <= %d, t_cap >= rows and an even head_stride >= t_cap (view %d)", who, kKv4MaxHeads,
+                index);
   if (x.t_cap > kKv4MaxCap) return fail(GLANCE_ERR_UNSUPPORTED, "%s: t_cap too large (view %d)", who, index);
   if (!aligned16(x.k) || !aligned16(x.k_scale) || !aligned16(x.v) || !aligned16(x.v_scale))
     return fail(GLANCE_ERR_INVALID_ARG, "%s: codes and scales must be 16-byte aligned (view %d)", who, index);

@@ -97,8 +97,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   constexpr int kSlots = kThreads / kLanes;  // heads at a time
   constexpr int kHeadBytes = kHeadDim * sizeof(T), kHalfBytes = kHeadBytes / 2;
   __shared__ float2 s_cs[kMaxRows][kHalf];
-  pdl_wait_prior();
-  pdl_launch_dependents();
+  pdl_wait_prior();  // and no early start for the kernel behind: rows of a prompt may be its prefix
   const int req = blockIdx.x / p.blocks_per_req;
   const int row0 = (blockIdx.x - req * p.blocks_per_req) * p.block_rows;
   const int n_rows = min(p.block_rows, p.M - row0);
@@ -231,6 +230,7 @@ extern "C" glance_status glance_rope_init(glance_rope* rope, int head_dim, doubl
   int run = 0, left = sec[0];  // runs: the current axis and what it has left
   for (int j = 0; j < half; ++j) {
     const double turns = pow(theta, -2.0 * j / head_dim) / 6.283185307179586476925;
+    if (!isfinite(turns)) return fail(GLANCE_ERR_INVALID_ARG, "%s: theta is too small", who);
     const double frac = turns - floor(turns);
     const double scaled = frac * 18446744073709551616.0;
     r.turn[j] = scaled >= 18446744073709549568.0 ? 0ull : static_cast<uint64_t>(scaled + 0.5);
