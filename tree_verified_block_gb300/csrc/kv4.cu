@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_write_rows_kernel(const __gri
 
 template <int kLayers>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_rows_kernel(const __grid_constant__ RowsParams<kLayers> p) {
-  pdl_wait_prior();
-  pdl_launch_dependents();
+  pdl_wait_prior();  // and no early start for the kernel behind: the rows may be the prefix of its 16-bit cache
   const int lkv = blockIdx.y / p.n_kv_heads, head = blockIdx.y - lkv * p.n_kv_heads;
   const float g = p.global[lkv & 1];
   const int grp = threadIdx.x & 7;
