@@ -316,7 +316,10 @@ class Views(list):
         if len(on) != 1:
             raise ValueError("glance: every view of a list must be on one device")
         self.dev = on.pop()
-        self.c = (type(self[0].c) * len(self))(*[x.c for x in self])
+        first = self[0].c
+        self.c = (type(first) * len(self))(*[x.c for x in self])
+        self.at = ctypes.addressof(self.c)
+        self.heads = (self[0].rows, self[0].L) if isinstance(first, TreeC) else (first.n_kv_heads, first.head_dim)
 
 
 def _views(x, kind):
@@ -343,7 +346,7 @@ class Rope:
         sec = list(sections) if sections is not None else [head_dim // 2]
         _check(lib().glance_rope_init(ctypes.byref(self.c), head_dim, float(theta), len(sec),
                                       (ctypes.c_int32 * len(sec))(*sec), int(bool(interleaved))))
-        self.head_dim, self.n_axes = head_dim, len(sec)
+        self.head_dim, self.n_axes, self.at = head_dim, len(sec), ctypes.addressof(self.c)
 
 
 # ------------------------------------------------------------------- calls
@@ -604,6 +607,9 @@ def dense_swiglu(h, W_gate, W_up, in_sumsq, eps, act, stream=None):
 
 # ------------------------------------------- norm + rotary, 4-bit caches
 
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 def _on(stream, views, *tensors):
     """The stream to launch on: the given one, else the tensors' device's
     current one. All tensors and views must be on the current device."""
@@ -623,31 +629,31 @@ def qk_norm_rope(qkv, n_q_heads, q_norm, k_norm, eps, pos, rope, q_out, kv, stre
     of q and k, rotary position, q to q_out [B * M][Hq][D], k and v to slots
     T.. of kv (one KVLayer, or B of them). pos int32 [n_axes][B * M]."""
     kv = _views(kv, KVLayer)
-    B, rows = len(kv), qkv.shape[0]
-    D, Hkv = kv[0].c.head_dim, kv[0].c.n_kv_heads
-    if (qkv.dim() != 2 or qkv.stride(1) != 1 or rows % B or qkv.shape[1] != (n_q_heads + 2 * Hkv) * D or rope.head_dim != D):
+    B, (Hkv, D) = len(kv), kv.heads
+    shape, strides, dtype = qkv.shape, qkv.stride(), qkv.dtype
+    rows = shape[0]
+    if (len(shape) != 2 or strides[1] != 1 or rows % B or shape[1] != (n_q_heads + 2 * Hkv) * D or rope.head_dim != D):
         raise ValueError("glance: qkv must be [B * M, (n_q_heads + 2 * n_kv_heads) * head_dim], rope and kv of its head_dim")
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
     if pos.dtype != torch.int32 or pos.shape[-1] != rows or pos.numel() != rope.n_axes * rows or not pos.is_contiguous():
         raise ValueError("glance: pos must be contiguous int32 [n_axes, B * M]")
-    if q_out.dtype != qkv.dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
+    if q_out.dtype != dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
         raise ValueError("glance: q_out must be contiguous [B * M, n_q_heads, head_dim] of qkv's dtype")
-    tensors = [qkv, pos, q_out]
-    for w in (q_norm, k_norm):
+    tensors, norms = [qkv, pos, q_out], [None, None]
+    for i, w in enumerate((q_norm, k_norm)):
         if w is not None:
             if w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous():
                 raise ValueError("glance: norm weights must be contiguous float32 [head_dim]")
             tensors.append(w)
+            norms[i] = w.data_ptr()
     s = _on(stream, kv, *tensors)
-    stride = qkv.stride(0) if rows > 1 else qkv.shape[1]
-    _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _dtype_code(qkv), B, rows // B, stride, n_q_heads,
-                                     None if q_norm is None else q_norm.data_ptr(),
-                                     None if k_norm is None else k_norm.data_ptr(), eps, pos.data_ptr(),
-                                     ctypes.addressof(rope.c), q_out.data_ptr(), ctypes.addressof(kv.c), s))
+    _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _DTYPES[dtype], B, rows // B, strides[0] if rows > 1 else shape[1],
+                                     n_q_heads, norms[0], norms[1], eps, pos.data_ptr(), rope.at, q_out.data_ptr(), kv.at, s))
 
 
 def _rows16(x, n_layers, kv, rows):
-    if (x.dtype != torch.bfloat16 or not x.is_contiguous() or
-            tuple(x.shape) != (n_layers, 2, kv[0].c.n_kv_heads, rows, 128)):
+    if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.shape != (n_layers, 2, kv.heads[0], rows, 128):
         raise ValueError("glance: rows must be contiguous bfloat16 [n_layers, 2, n_kv_heads, rows, 128]")
 
 
@@ -657,7 +663,7 @@ def kv4_write_rows(src, layers, rows, stream=None):
     layers = _views(layers, KV4Layer)
     _rows16(src, len(layers), layers, rows)
     s = _on(stream, layers, src)
-    _check(lib().glance_kv4_write_rows(src.data_ptr(), ctypes.addressof(layers.c), len(layers), rows, s))
+    _check(lib().glance_kv4_write_rows(src.data_ptr(), layers.at, len(layers), rows, s))
 
 
 def kv4_read_rows(layers, first, rows, dst, stream=None):
@@ -666,12 +672,12 @@ def kv4_read_rows(layers, first, rows, dst, stream=None):
     layers = _views(layers, KV4Layer)
     _rows16(dst, len(layers), layers, rows)
     s = _on(stream, layers, dst)
-    _check(lib().glance_kv4_read_rows(ctypes.addressof(layers.c), len(layers), first, rows, dst.data_ptr(), s))
+    _check(lib().glance_kv4_read_rows(layers.at, len(layers), first, rows, dst.data_ptr(), s))
 
 
 def kv4_tree_attention_workspace_bytes(rows, n_q_heads, kvs):
     kvs = _views(kvs, KV4Layer)
-    return lib().glance_kv4_tree_attention_workspace_bytes(len(kvs), rows, n_q_heads, ctypes.addressof(kvs.c))
+    return lib().glance_kv4_tree_attention_workspace_bytes(len(kvs), rows, n_q_heads, kvs.at)
 
 
 _DECODE = {}
@@ -682,27 +688,28 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
     [N+1][Hq][128] too), kvs B KV4Layer views, trees B Tree objects. trees
     None: plain decoding, one row per request that sees the prefix and itself."""
     kvs = _views(kvs, KV4Layer)
-    B = len(kvs)
-    rows = q.shape[-3]
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or not q.is_contiguous() or not out.is_contiguous() \
-            or q.shape != out.shape or q.shape[-1] != 128 or q.numel() != B * rows * q.shape[-2] * 128:
+    B, shape, bf16 = len(kvs), q.shape, torch.bfloat16
+    rows, heads = shape[-3], shape[-2]
+    if q.dtype != bf16 or out.dtype != bf16 or not q.is_contiguous() or not out.is_contiguous() or shape != out.shape \
+            or shape[-1] != 128 or q.numel() != B * rows * heads * 128:
         raise ValueError("glance: q and out must be contiguous bfloat16 [B, N + 1, n_q_heads, 128]")
     if trees is None:
         c = _DECODE.get(B)
         if c is None:
             c = _DECODE[B] = (TreeC * B)(*[TreeC(0, 1, 1) for _ in range(B)])
+        c = ctypes.addressof(c)
         if rows != 1:
             raise ValueError("glance: without trees q has one row per request")
     else:
         trees = _views(trees, Tree)
-        if len(trees) != B or trees[0].rows != rows:
+        if len(trees) != B or trees.heads[0] != rows:
             raise ValueError("glance: need one tree of q's N + 1 rows per request")
         if trees.dev != kvs.dev:
             raise ValueError("glance: the trees must be on the caches' device")
-        c = trees.c
+        c = trees.at
     s = _on(stream, kvs, q, out, ws)
-    _check(lib().glance_kv4_tree_attention(q.data_ptr(), q.shape[-2], ctypes.addressof(kvs.c), ctypes.addressof(c), B,
-                                           scale, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    _check(lib().glance_kv4_tree_attention(q.data_ptr(), heads, kvs.at, c, B, scale, out.data_ptr(),
+                                           ws.data_ptr(), ws.numel() * ws.element_size(), s))
 
 
 def kv4_accept_commit_workspace_bytes(B, n_layers):
@@ -715,20 +722,19 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
     B * n_layers KV4Layer views (request-major), argmax [B][N+1], outputs [B],
     [B][L], [B]. With gap [B][N+1] and gated [B]: the tie-aware gate."""
     trees, layers = _views(trees, Tree), _views(layers, KV4Layer)
-    B = len(trees)
-    t = trees[0]
-    if len(layers) % B:
+    B, n_layers, (rows, L) = len(trees), len(layers), trees.heads
+    if n_layers % B:
         raise ValueError("glance: layers must hold the same number of views for every request")
+    if trees.dev != layers.dev:
+        raise ValueError("glance: the trees must be on the caches' device")
     i32 = torch.int32
-    for x, n in ((argmax, B * t.rows), (n_accepted, B), (accepted_tok, B * t.L), (new_root, B)):
+    for x, n in ((argmax, B * rows), (n_accepted, B), (accepted_tok, B * L), (new_root, B)):
         if x.dtype != i32 or x.numel() < n or not x.is_contiguous():
             raise ValueError("glance: argmax, n_accepted, accepted_tok and new_root must be contiguous int32 "
                              "[B, N + 1], [B], [B, L], [B]")
-    if trees.dev != layers.dev:
-        raise ValueError("glance: the trees must be on the caches' device")
     tensors = [argmax, n_accepted, accepted_tok, new_root, ws]
     if gap is not None:
-        if gap.dtype != torch.float32 or gap.numel() < B * t.rows or not gap.is_contiguous():
+        if gap.dtype != torch.float32 or gap.numel() < B * rows or not gap.is_contiguous():
             raise ValueError("glance: gap must be contiguous float32 [B, N + 1]")
         tensors.append(gap)
     if gated is not None:
@@ -736,9 +742,8 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
             raise ValueError("glance: gated must be contiguous int32 [B]")
         tensors.append(gated)
     s = _on(stream, layers, *tensors)
-    _check(lib().glance_kv4_accept_commit(ctypes.addressof(trees.c), B, argmax.data_ptr(),
-                                          None if gap is None else gap.data_ptr(), gate_threshold,
-                                          ctypes.addressof(layers.c), len(layers) // B, n_accepted.data_ptr(),
+    _check(lib().glance_kv4_accept_commit(trees.at, B, argmax.data_ptr(), None if gap is None else gap.data_ptr(),
+                                          gate_threshold, layers.at, n_layers // B, n_accepted.data_ptr(),
                                           accepted_tok.data_ptr(), new_root.data_ptr(),
                                           None if gated is None else gated.data_ptr(), ws.data_ptr(),
                                           ws.numel() * ws.element_size(), s))
