@@ -784,7 +784,10 @@ constexpr uint32_t kOffMisc = kOffRaw + kRawStages * kRawBytes;
 constexpr uint32_t kWideMisc = 6144;
 constexpr uint32_t kWideSmem = 1024 + kOffMisc + kWideMisc;
 static_assert(kWideSmem <= 227 * 1024, "shared memory");
-constexpr int kWideMin = 4, kWideLead = 8;  // a part has a tile or more
+// A part has a tile or more. Starting and ending a group costs about 2.5 tiles
+// (8, 10, 12 units measured: 44.6, 42.7, 44.8 us for 64 rows x 8 requests of 512
+// to 8192 slots; 74.2, 70.5, 67.8 us for 256 rows x 5 of 100 to 5000).
+constexpr int kWideMin = 4, kWideLead = 10;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 struct WideMisc {
@@ -880,21 +883,14 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
     if (kk < steps) mma_bf16_ts(d, p + kk * 8, v + ((kk * 2048) >> 4), idesc, kk > 0 || !fresh);
 }
 
-// Slots kb .. kb + 31 (tree index = slot - T) that row `prow` sees.
-__device__ __forceinline__ uint32_t visible32(const Request& rq, int prow, int W, int rows, int kb) {
-  if (kb <= -32) return 0xFFFFFFFFu;
-  const uint32_t prefix = kb < 0 ? (1u << -kb) - 1u : 0u;
-  uint32_t tree;
-  if (kb < 0) {
-    tree = static_cast<uint32_t>(rq.anc[static_cast<size_t>(prow) * W] << -kb);
-  } else {
-    const int w = kb >> 6, o = kb & 63;
-    const uint64_t lo = w < W ? rq.anc[static_cast<size_t>(prow) * W + w] : 0ull;
-    const uint64_t hi = o && w + 1 < W ? rq.anc[static_cast<size_t>(prow) * W + w + 1] : 0ull;
-    tree = static_cast<uint32_t>(o ? (lo >> o) | (hi << (64 - o)) : lo);
-  }
-  const int lim = rows - kb;  // bits from lim on are past the last row
-  return prefix | (tree & (lim >= 32 ? 0xFFFFFFFFu : lim <= 0 ? 0u : (1u << lim) - 1u));
+// The 32 slots from tree index (slot - T) 32 i on that a row sees: slots of the
+// prefix, then the row's mask up to the last packed row.
+__device__ __forceinline__ uint32_t visible32(const uint64_t* anc, int rows, int i) {
+  if (i < 0) return 0xFFFFFFFFu;
+  const int left = rows - 32 * i;
+  if (left <= 0) return 0u;
+  const uint32_t seen = __ldg(reinterpret_cast<const uint32_t*>(anc) + i);
+  return left < 32 ? seen & ((1u << left) - 1u) : seen;
 }
 
 // A thread's share of a tile: rows row + 8i (i = 0..3) of the 128, dims 32q ..
@@ -1189,6 +1185,41 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       const int R = p.G * p.rows;
       uint32_t n_s = 0, n_o[2] = {0, 0};  // phases of s_full (this slot) and o_done so far
       bool ok = true;
+      bool ahead = false;  // the segment's Q is in its tile already
+      // A segment's Q into the slot's tile, 16 bytes at a time (thread = chunk, 16
+      // to a row); rows behind the last are zero. The products that read the tile
+      // before are done.
+      const auto copy_q = [&](const Segment& s) {
+        const int R = p.G * p.rows, head = s.g / p.n_qp, qt0 = 2 * (s.g % p.n_qp), xq = qt0 + 1 < p.n_qt ? x : 0;
+        const int th = (warp & 3) * 32 + lane, c = th & 15;
+        unsigned char* dst = smem + xq * kTileBytes + (c >> 3) * kHalfBytes;
+        int i = th >> 4, qr = (qt0 + xq) * kBM + i;
+        int h = qr / p.rows, pr = qr - h * p.rows;  // query head of the group, packed row
+        const __nv_bfloat16* src = p.q + (static_cast<size_t>(s.r) * p.rows * p.Hq + head * p.G) * kD + c * 8;
+        int at = (pr * p.Hq + h) * kD;  // of the row's head in q
+        const int step = 8 * p.Hq * kD, wrap = kD - p.rows * p.Hq * kD;  // 8 packed rows on; the next head's first
+        dst += i * 128 + (((c & 7) ^ (i & 7)) << 4);  // i steps by 8: the swizzle stays
+#pragma unroll 4
+        for (; i < kBM; i += 8) {
+          if (qr < R)
+            copy16_async(dst, src + at);
+          else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+          dst += 8 * 128;
+          qr += 8;
+          pr += 8;
+          at += step;
+          while (pr >= p.rows) {
+            pr -= p.rows;
+            at += wrap;
+          }
+        }
+      };
+      const auto q_copied = [&] {
+        copy_async_wait();
+        fence_proxy_async_smem();
+        mbar_arrive(&ms->q_ready[x]);
+      };
       Segment s = ms->seg;
       do {
         const Request& rq = p.req[s.r];
@@ -1207,36 +1238,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         };
         // score factor, in log2; at least the least normal number: a score of -infinity stays one
         const float sc = fmaxf(p.scale_log2 * rq.k_global, 1.17549435e-38f);
-        if (pair || !x) {
-          // Q into its tile, 16 bytes at a time (thread = chunk, 16 to a row; the
-          // products that read the previous segment's are done); rows behind the last are zero
-          const int th = (warp & 3) * 32 + lane, c = th & 15;
-          unsigned char* dst = smem + (pair ? x * kTileBytes : 0) + (c >> 3) * kHalfBytes;
-          int i = th >> 4, qr = (pair ? qt0 + x : qt0) * kBM + i;
-          int h = qr / p.rows, pr = qr - h * p.rows;  // query head of the group, packed row
-          const __nv_bfloat16* src = p.q + (static_cast<size_t>(s.r) * p.rows * p.Hq + head * p.G) * kD + c * 8;
-          int at = (pr * p.Hq + h) * kD;  // of the row's head in q
-          const int step = 8 * p.Hq * kD, wrap = kD - p.rows * p.Hq * kD;  // 8 packed rows on; the next head's first
-          dst += i * 128 + (((c & 7) ^ (i & 7)) << 4);  // i steps by 8: the swizzle stays
-#pragma unroll 4
-          for (; i < kBM; i += 8) {
-            if (qr < R)
-              copy16_async(dst, src + at);
-            else
-              *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-            dst += 8 * 128;
-            qr += 8;
-            pr += 8;
-            at += step;
-            while (pr >= p.rows) {
-              pr -= p.rows;
-              at += wrap;
-            }
-          }
-          copy_async_wait();
-          fence_proxy_async_smem();
-          mbar_arrive(&ms->q_ready[x]);
+        if (!ahead && (pair || !x)) {
+          copy_q(s);
+          q_copied();
         }
+        ahead = false;
         float m = -INFINITY, l = 0.f;
         const int step = pair ? 1 : 2, j0 = pair ? 0 : x;
         for (int j = j0; j < run.tiles; j += step) {
@@ -1244,7 +1250,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           const int nc = run.cols(j) / 32;
           const bool tree = key0 + 32 * nc > T;
           uint32_t bad[4] = {0u, 0u, 0u, 0u};  // slots with a V scale that is not a number
+          uint32_t vis[4];                     // slots that the row sees
           if (tree) {
+            bool valid;
+            int prow;
+            (void)query(valid, prow);
+            const uint64_t* anc = rq.anc + static_cast<size_t>(prow) * p.W;
+            const int kb = key0 - T;
+            uint32_t w[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = valid ? visible32(anc, p.rows, (kb >> 5) + i) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vis[i] = __funnelshift_r(w[i], w[i + 1], kb & 31);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int slot = key0 + 32 * i + lane;
@@ -1260,22 +1277,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           tc_fence_after();
           if (tree) {
             // masked in place, so that the rest is the same for every tile
-            bool valid;
-            int prow;
-            (void)query(valid, prow);
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
-              const int s0 = key0 + 32 * c, lim = run.k1 - s0;
-              uint32_t vis = valid ? visible32(rq, prow, p.W, p.rows, s0 - T) : 0u;
-              if (lim < 32) vis &= (1u << lim) - 1u;
+              const uint32_t seen = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
               uint32_t r[32], y[16], z[16];
               tmem_ld32(tS + 32 * c, r);
               tmem_wait32(r);
               const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                y[e] = !(vis >> e & 1u) ? 0xFF800000u : (b >> e & 1u) ? 0x7FC00000u : r[e];
-                z[e] = !(vis >> (16 + e) & 1u) ? 0xFF800000u : (b >> (16 + e) & 1u) ? 0x7FC00000u : r[16 + e];
+                y[e] = !(seen >> e & 1u) ? 0xFF800000u : (b >> e & 1u) ? 0x7FC00000u : r[e];
+                z[e] = !(seen >> (16 + e) & 1u) ? 0xFF800000u : (b >> (16 + e) & 1u) ? 0x7FC00000u : r[16 + e];
               }
               tmem_st16(tS + 32 * c, y);
               tmem_st16(tS + 32 * c + 16, z);
@@ -1380,9 +1392,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         uint4* po = p.part + part * 16 * kBM + lrow;
         if (l != l) m = 0.f;  // a NaN row stays one in every merge
         if (pair) {
+          // the slot's last S is done with the Q tile: the next segment's Q comes
+          // during its last product, and the next S during the output
+          Segment next = s;
+          ahead = next_segment<kWideLead>(p, pl, next) && (!x || 2 * (next.g % p.n_qp) + 1 < p.n_qt);
+          if (ahead) copy_q(next);
           ok = wide_wait(&ms->o_done[x], n_o[x]++ & 1, ms);
           if (!ok) break;
           tc_fence_after();
+          if (ahead) q_copied();
           const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -1445,6 +1463,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         // after a failed wait the other slot gives up as well, but may first come
         // to the barrier of a query tile that both slots have
         wide_fail(ms);
+        copy_async_wait();
         while (next_segment<kWideLead>(p, pl, s))
           if (2 * (s.g % p.n_qp) + 1 >= p.n_qt) {
             (void)named_bar_or(1, 256, true);
