@@ -157,36 +157,33 @@ __device__ __forceinline__ bool take_segment(const Params& p, const Plan& pl, Se
     at = 0;
   }
 }
+// Block b's first segment, by one warp (lane = request, or end of the run).
 template <int kLead>
-__device__ __forceinline__ bool first_segment(const Params& p, const Plan& pl, int b, Segment& s) {
-  const int gpr = p.Hkv * p.n_qp;
+__device__ __forceinline__ bool first_segment(const Params& p, const Plan& pl, int b, int lane, Segment& s) {
+  const int gpr = p.Hkv * p.n_qp, r = min(lane, kMaxB - 1);
   s.index = 0;
-  int r = 0;
   if (pl.tau) {
-    int n = 0, at = 0;
-    for (; r < p.B; ++r) {
-      n = (pl.units[r] + pl.tau - 1) / pl.tau;
-      at = b - pl.blocks0[r];
-      if (at < n * gpr) break;
-    }
-    if (r == p.B) return false;
-    s.r = r;
+    int n = (pl.units[r] + pl.tau - 1) / pl.tau, at = b - pl.blocks0[r];
+    const unsigned mine = __ballot_sync(0xffffffffu, lane < p.B && at >= 0 && at < n * gpr);
+    if (!mine) return false;
+    s.r = __ffs(mine) - 1;
+    n = __shfl_sync(0xffffffffu, n, s.r);
+    at = __shfl_sync(0xffffffffu, at, s.r);
     s.g = at / n;
     s.a = at % n * pl.tau;
-    s.n = min(pl.tau, pl.units[r] - s.a);
+    s.n = min(pl.tau, pl.units[s.r] - s.a);
     s.left = 0;
     return true;
   }
   if (b >= pl.runs || pl.total == 0) return false;
-  const long long x = run_start(pl.total, b, pl.runs);
-  const int len = static_cast<int>(run_start(pl.total, b + 1, pl.runs) - x);
-  while (r + 1 < p.B && x >= pl.base[r + 1]) ++r;  // requests without units share their base with the next
-  const long long in = x - pl.base[r];
-  const int length = pl.units[r] + kLead;
-  s.r = r;
+  const long long end = run_start(pl.total, b + (lane & 1), pl.runs), x = __shfl_sync(0xffffffffu, end, 0);
+  // requests without units share their base with the next
+  s.r = 31 - __clz(__ballot_sync(0xffffffffu, lane < p.B && x >= pl.base[r]));
+  const long long in = x - pl.base[s.r];
+  const int length = pl.units[s.r] + kLead;
   s.g = static_cast<int>(div_small(in, length));
   s.index = -1;
-  s.left = len;
+  s.left = static_cast<int>(__shfl_sync(0xffffffffu, end, 1) - x);
   return take_segment<kLead>(p, pl, s, static_cast<int>(in - static_cast<long long>(s.g) * length));
 }
 template <int kLead>
@@ -346,7 +343,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   if (warp == 0) {
     make_plan<kFewMin, kFewLead>(p, &ms->plan, lane, gridDim.x);
     __syncwarp();
-    if (lane == 0) ms->any = first_segment<kFewLead>(p, ms->plan, blockIdx.x, ms->seg);
+    Segment s;
+    const bool any = first_segment<kFewLead>(p, ms->plan, blockIdx.x, lane, s);
+    if (lane == 0) {
+      ms->any = any;
+      ms->seg = s;
+    }
   }
   __syncthreads();
   const Plan& pl = ms->plan;
@@ -998,7 +1000,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
   if (warp == 3) {
     make_plan<kWideMin, kWideLead>(p, &ms->plan, lane, blocks);
     __syncwarp();
-    if (lane == 0) ms->any = first_segment<kWideLead>(p, ms->plan, blockIdx.x, ms->seg);
+    Segment s;
+    const bool any = first_segment<kWideLead>(p, ms->plan, blockIdx.x, lane, s);
+    if (lane == 0) {
+      ms->any = any;
+      ms->seg = s;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1502,6 +1509,9 @@ __global__ void __launch_bounds__(128 * kSlices) kv4_attention_merge_kernel(cons
   const int qt = tile % p.n_qt, rh = tile / p.n_qt;  // request * Hkv + head
   const int t = threadIdx.x & 127, row = t & 7, octet = t >> 3, slice = threadIdx.x >> 7;
   const int lrow = rows0 + row, qrow = qt * kBM + lrow;
+  const int r = rh / p.Hkv, head = rh % p.Hkv;
+  size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + head * p.G + qrow / p.rows) * kD + octet * 8;
+  asm volatile("" : "+l"(at));  // worked out here, while the kernel before this one ends
   pdl_wait_prior();  // in every block: this kernel ends after the one before it
   pdl_launch_dependents();
   if (qt * kBM + rows0 >= p.G * p.rows) return;
@@ -1570,12 +1580,10 @@ __global__ void __launch_bounds__(128 * kSlices) kv4_attention_merge_kernel(cons
     }
   }
   if (qrow >= p.G * p.rows) return;
-  const int r = rh / p.Hkv, head = rh % p.Hkv;
   const float inv = L == 0.f ? 0.f : p.req[r].v_global / L;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(a[2 * i] * inv, a[2 * i + 1] * inv);
-  const size_t at = ((static_cast<size_t>(r) * p.rows + qrow % p.rows) * p.Hq + head * p.G + qrow / p.rows) * kD + octet * 8;
   *reinterpret_cast<uint4*>(p.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
