@@ -232,8 +232,11 @@ static_assert(2 * (kFewSmem + 1024) <= 228 * 1024, "two blocks per SM");
 
 // A part has a piece for every warp or more. (One part of 32 pieces instead of
 // four of 8 takes 11.5 instead of 8.7 us for one row on 1000 slots: a piece takes
-// a warp 1.3 us, the merge of the parts 2.)
-constexpr int kFewMin = kFewWarps, kFewLead = 12;
+// a warp 1.3 us, the merge of the parts 2.) Starting and ending a group costs the
+// block about two pieces per warp (8, 12, 16, 20 units measured: 34.3, 30.0, 29.2,
+// 28.9 us for 4 rows x 16 requests of 100 to 10000 slots, 41.4, 40.8, 40.5, 40.5
+// us for one row x 16 of 512 to 32768).
+constexpr int kFewMin = kFewWarps, kFewLead = 16;
 
 struct FewMisc {
   uint64_t full[kFewWarps][kFewStages];
