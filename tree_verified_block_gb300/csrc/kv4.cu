@@ -53,10 +53,11 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
 // 2^-46 of the quotient before the final rounding. That rounding is the
 // quotient's: with s = m 2^e, m <= 15, the quotient is a multiple of 1 / m of a
 // unit, so no midpoint of two fp32 numbers is nearer than 1 / 30 of one. A tie
-// between two codes is exact this way and goes to the even one.
-__device__ __forceinline__ float quotient(float x, float d, float inv) {
-  const float q = x * inv;
-  return fmaf(fmaf(-q, d, x), inv, q);
+// between two codes is exact this way and goes to the even one. Two at a time,
+// with -s: the call is bound by instruction issue as much as by memory.
+__device__ __forceinline__ unsigned long long quotient2(unsigned long long x, unsigned long long neg_s, unsigned long long inv) {
+  const unsigned long long q = mul_f2(x, inv);
+  return fma_f2(fma_f2(q, neg_s, x), inv, q);
 }
 
 // One group of 16 bf16 values (8 words) to 16 codes (2 words) and a scale.
@@ -74,11 +75,14 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float inv_g, 
   const float s = f16x2_to_f32(scales2_to_f16(scale)).x;
   const bool any = finite && s > 0.f;
   const float inv_s = any ? __frcp_rn(s) : 0.f;
+  const unsigned long long inv_g2 = pair_f2(inv_g, inv_g), inv_s2 = pair_f2(inv_s, inv_s), neg_s2 = pair_f2(-s, -s);
   codes[0] = codes[1] = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float lo = __uint_as_float(x[i] << 16) * inv_g, hi = __uint_as_float(x[i] & 0xFFFF0000u) * inv_g;
-    const uint32_t c = code2(quotient(lo, s, inv_s), quotient(hi, s, inv_s));
+    float lo, hi;
+    split_f2(quotient2(mul_f2(pair_f2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u)), inv_g2), neg_s2, inv_s2),
+             lo, hi);
+    const uint32_t c = code2(lo, hi);
     codes[i >> 2] |= c << (8 * (i & 3));
   }
   if (!any) codes[0] = codes[1] = 0u;
