@@ -76,14 +76,16 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float inv_g, 
   const bool any = finite && s > 0.f;
   const float inv_s = any ? __frcp_rn(s) : 0.f;
   const unsigned long long inv_g2 = pair_f2(inv_g, inv_g), inv_s2 = pair_f2(inv_s, inv_s), neg_s2 = pair_f2(-s, -s);
-  codes[0] = codes[1] = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float lo, hi;
-    split_f2(quotient2(mul_f2(pair_f2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u)), inv_g2), neg_s2, inv_s2),
-             lo, hi);
-    const uint32_t c = code2(lo, hi);
-    codes[i >> 2] |= c << (8 * (i & 3));
+  for (int w = 0; w < 2; ++w) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = x[4 * w + i];
+      split_f2(quotient2(mul_f2(pair_f2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)), inv_g2), neg_s2, inv_s2),
+               v[2 * i], v[2 * i + 1]);
+    }
+    codes[w] = codes8(v);
   }
   if (!any) codes[0] = codes[1] = 0u;
 }

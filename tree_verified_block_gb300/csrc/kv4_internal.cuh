@@ -72,12 +72,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Two fp32 values as codes (nearest even, at most 6 in magnitude), `lo` in the low half of the byte.
-__device__ __forceinline__ uint32_t code2(float lo, float hi) {
+// Eight fp32 values as codes (nearest even, at most 6 in magnitude), the first in the lowest bits.
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n .reg .b8 t, z;\n mov.b16 {z, t}, 0;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n mov.b32 %0, {t, z, z, z};\n}\n"
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 // An fp32 value >= 0 as an e4m3 scale (nearest even, at most 448).
