@@ -558,7 +558,8 @@ typedef struct {
  * interleaved 0: axis 0 has the first sections[0] frequencies, axis 1 the next
  * and so on. interleaved 1: frequency j goes to axis j mod n_axes while that
  * axis has had fewer than its section, else to axis 0 (every axis but 0 needs
- * sections[a] <= (head_dim / 2 - a + n_axes - 1) / n_axes). theta: finite, > 0.
+ * sections[a] <= (head_dim / 2 - a + n_axes - 1) / n_axes). theta: finite, > 0,
+ * with finite frequencies.
  */
 glance_status glance_rope_init(glance_rope* rope, int head_dim, double theta, int n_axes,
                                const int32_t* sections, int interleaved);
@@ -578,8 +579,9 @@ glance_status glance_rope_init(glance_rope* rope, int head_dim, double theta, in
  *   k, v   to slots T + i of kv[r] (host array of B views, one geometry but
  *          for t_cap and strides, T = *kv[r].t_len; T is not changed).
  * pos: device int32 [n_axes][B M]. q_norm, k_norm: device float [head_dim].
- * All arithmetic is fp32; angles are exact to 2^-32 of a turn at any int32
- * position. dtype BF16 or F32 (that of kv); head_dim 32, 64 or 128. Arrays
+ * All arithmetic is fp32; the angle, position times the frequency in double
+ * precision, is reduced to one turn exactly and rounded to 2^-32 of a turn.
+ * dtype BF16 or F32 (that of kv); head_dim 32, 64 or 128. Arrays
  * 16-byte aligned, strides multiples of 16 bytes; q_out must not overlap qkv.
  * A request with T + M > t_cap sets device status 2 and none of its cache rows
  * are written.
@@ -625,11 +627,12 @@ typedef struct {
  * src: device BF16 [n_layers][2][n_kv_heads][rows][128] (K before V),
  * contiguous, 32-byte aligned. Per group of 16 elements x, in fp32:
  * t = x * (1 / global), the reciprocal rounded first; scale = max|t| / 6
- * rounded to e4m3 (nearest even, at most 448); code = t / scale rounded to nearest even, at most 6 (0 where the scale
- * is 0). A group with a t that is not finite gets the scale 0x7F and codes 0.
+ * rounded to e4m3 (nearest even, at most 448); code = t / scale rounded to
+ * nearest even, at most 6 (0 where the scale is 0). A group with a t that is not finite gets the scale 0x7F and codes 0.
  * Each row is quantised by itself, so a row reads the same whether it was
  * written alone, in a prompt or as a tree row.
- * layers: host array with one t_len, geometry and pair of globals. If
+ * layers: host array of distinct caches with one t_len, geometry and pair of
+ * globals. If
  * T + rows > t_cap the call sets device status 2 and writes nothing.
  * Limits: 1 <= n_layers <= 128, rows >= 1.
  */
@@ -638,16 +641,17 @@ glance_status glance_kv4_write_rows(const void* src, const glance_kv4* layers, i
 
 /*
  * The values that slots first .. first + rows - 1 of every layer stand for, as
- * BF16 [n_layers][2][n_kv_heads][rows][128] (dst, contiguous, 32-byte aligned;
- * rounded once, nearest even): back to a 16-bit cache or to the host.
+ * BF16 [n_layers][2][n_kv_heads][rows][128] (dst, contiguous, 32-byte aligned):
+ * scale * global and that times the code in fp32, then rounded to nearest even;
+ * back to a 16-bit cache or to the host.
  * 0 <= first, first + rows <= t_cap; T is not looked at. Otherwise as
  * glance_kv4_write_rows.
  */
 glance_status glance_kv4_read_rows(const glance_kv4* layers, int n_layers, int first, int rows,
                                    void* dst, void* stream);
 
-/* Workspace bytes for glance_kv4_tree_attention (0 on bad sizes); depends on
- * every request's t_cap, so pass the same kv array as to the call. */
+/* Workspace bytes for glance_kv4_tree_attention (0 on bad sizes); kv: as for
+ * the call. */
 size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_heads,
                                                  const glance_kv4* kv);
 
@@ -666,9 +670,15 @@ size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_head
  * n_q_heads / n_kv_heads in {1, 2, 4, 8}; scale finite and > 0; q, out 16-byte
  * aligned and not overlapping, workspace 256-byte aligned. A request with
  * T + N + 1 > t_cap sets device status 2 and its out is left as it was.
- * The codes are widened to f16, which holds code * scale exactly; q is rounded
- * to f16 after each row is scaled by a power of two; the softmax weights are
- * rounded to f16; all sums are fp32.
+ * Arithmetic: code * scale is exact; the softmax weights are rounded to f16
+ * (2^-11 of each), sums and maxima are fp32, out is rounded to bf16 once. With
+ * n_q_heads / n_kv_heads * (N + 1) <= 16 q is used to 2^-31 of its row's largest
+ * element (smaller ones lose bits), beyond that as it is, and partial results
+ * of a row that several blocks share are rounded to f16 between them (2^-11 of
+ * an element, at least 2^-25 in units of code * scale). The results do not
+ * change from call to call. A q row with an infinity or NaN that sees a slot of
+ * the prefix gives NaN. One workspace, of the largest size among them, serves calls of
+ * any shape in turn.
  */
 glance_status glance_kv4_tree_attention(const void* q, int n_q_heads, const glance_kv4* kv,
                                         const glance_tree* trees, int B, float scale, void* out,
@@ -682,8 +692,8 @@ size_t glance_kv4_accept_commit_workspace_bytes(int B, int n_layers);
  * null) glance_accept_commit_gated_batched, on 4-bit caches; B = 1 for one
  * request. The path rows' codes and scales move from slots T + path_i to slots
  * T + i as they are (no requantisation), then T += a + 1. layers: host array
- * [B][n_layers]; the layers of a request share t_len and geometry, no two
- * requests share a t_len. Limits: 1 <= N <= 255, 1 <= n_layers <= 128,
+ * [B][n_layers], distinct caches; the layers of a request share t_len and
+ * geometry, no two requests share a t_len. Limits: 1 <= N <= 255, 1 <= n_layers <= 128,
  * B * n_layers <= 960.
  */
 glance_status glance_kv4_accept_commit(const glance_tree* trees, int B, const int32_t* argmax,

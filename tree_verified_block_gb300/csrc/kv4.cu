@@ -5,6 +5,14 @@
 // 1), and a prompt's rows go in the same way. Each row is quantised by itself,
 // so the cache after a commit is the cache that one-by-one decoding would have
 // written: the path's rows move as they are.
+//
+// The row kernels read or write 256 bytes of bf16 and 72 of the cache per row
+// and are bound by that: 12 layers x 2 x 8 heads x 8191 rows (516 MB) take 78.6
+// us to write (97 % of the measured copy rate) and 76.9 to read (99 %). A
+// thread has a group of 16 elements of four rows in flight; writing, the
+// arithmetic would bind first (87.8 us with one element per operation) and is
+// done two elements at a time. 64 rows of 36 layers take 3.9 and 2.9 us, a
+// launch and one trip to memory.
 #include "kv4_internal.cuh"
 
 GLANCE_DEFINE_STATUS_WORD(status_kv4)

@@ -2,6 +2,23 @@
 //
 // arXiv 2609.00355, Definition 1: packed row i sees the prefix slots 0..T-1
 // and the tree slots of its own ancestors; N = 0 is one row, plain decoding.
+//
+//   o = sum_s w_s v_s / sum_s w_s,  w_s = 2^(q . k_s * scale * log2 e - m),
+// over the visible slots s in one pass: m is a running maximum that may lag the
+// true one by 8 (the weights then stay below 2^8), and what was summed before
+// is rescaled when it moves. k_s and v_s are code * scale; the globals go into
+// the score factor and the output. Sums, maxima and O are fp32; the weights
+// enter the second product as f16 (half a step 2^-11 of each, at most an
+// eighth of the output's own rounding to bf16), because V's 6 significant bits
+// are exact in f16 and a product takes one 16-bit type.
+//
+// Two kernels, by the query rows that share a kv head (G heads x N + 1 rows):
+// up to 16, the call is bound by the cache's bytes (kv4_attention_few_kernel);
+// beyond, by the products (kv4_attention_wide_kernel, with the tensor core's
+// 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 58.3
+// and 111 us on 131072 slots, 27.8 and 35.9 on 32768, 22.0 and 31.4 for 8
+// requests of 512 to 8192, but 15.7 and 13.0 on 4096; the host that picks the
+// kernel does not know T.
 #include "kv4_internal.cuh"
 
 GLANCE_DEFINE_STATUS_WORD(status_kv4_attention)
@@ -213,6 +230,16 @@ __device__ __forceinline__ bool next_segment(const Params& p, const Plan& pl, Se
 //   accumulator layout into P^T's operand layout.
 // The warps of a block are merged through shared memory, the blocks of a head
 // through the workspace by the block that finishes last.
+//
+// Measured (32 / 8 heads): one row on 131072 slots 37.1 us (60 % of the copy
+// rate), one row x 16 requests of 512 to 32768 slots 40.5 us (56 %). There it is
+// the warps' issue that bounds it (53 % of the issue slots at 16 warps per SM: a
+// piece is 660 instructions, most of them the codes' conversion), not the memory
+// (46 %); three blocks per SM (85 registers a thread) spill and are slower. One
+// row on 1000 slots takes 8.5 us: 1.2 until the block knows its work, 1.3 until
+// q and the first piece are there, 1.2 for that piece, 0.9 to join the block's
+// warps, 1.1 for the ticket and 1.5 to join the parts; much of each step is its
+// instructions' first way to the SM.
 
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
@@ -757,8 +784,9 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // warps turn S into weights, the other slot's products run.
 //
 //   warp 2        bulk copies of codes and scales (half tiles, three in flight)
-//   warps 12..15  codes -> f16 K and V tiles in shared memory, in the
-//                 128-byte-swizzled layout of the tensor core, two stages
+//   warps 12..15  codes -> K (bf16, q's type) and V (f16) tiles in shared
+//                 memory, in the 128-byte-swizzled layout of the tensor core, two
+//                 stages
 //   warp 0        S = Q K^T (both from shared memory) and O += P V (P from
 //                 tensor memory, over the columns of its S)
 //   warps 4..7, 8..11  softmax of slot 0 and 1, one thread per query row: mask,
@@ -772,6 +800,18 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 //
 // A group that one block has whole is written out there; the others' parts are
 // merged by a second kernel.
+//
+// Measured (32 / 8 heads, 64 rows): 131072 slots 117.5 us, 61 % of the tensor
+// rate on the products' operations; 4096 slots 15.4 us; 8 requests of 512 to
+// 8192 slots 39.5 us. A pair of tiles takes 3550 clocks, of which the tensor
+// core works 2048: a slot's chain is S and O's products (1380 with the other
+// slot's in between) and the softmax (2080), and tensor memory (two S, two O of
+// 128 columns) has no room for a second S per slot that would let them overlap.
+// S of 64 slots, which has, reads Q from shared memory twice as often and takes
+// 170 us. Short calls are start-up: 1.4 us until the block knows its work, 3
+// until the first S, 3.1 for two tiles, 0.85 for the output, 1 between the
+// kernels, 3 for the merge (joining inside this kernel takes 17.9 us instead of
+// 16.0 at 4096, blocks that wait for one another).
 
 constexpr int kWideThreads = 512;
 // Registers per thread: 128 at launch (65,536 for the block), then shared out
@@ -819,7 +859,6 @@ struct Run {
   // columns of tile j that its products compute, a multiple of 32
   __device__ __forceinline__ int cols(int j) const { return min(kBN, (k1 - key0(j) + 31) & ~31); }
 };
-
 
 __device__ __forceinline__ void wide_fail(WideMisc* ms) {
   report(GLANCE_DEV_PIPELINE_TIMEOUT);
@@ -900,7 +939,8 @@ __device__ __forceinline__ void load_raw(Raw& x, const unsigned char* codes, con
 }
 
 // ... as 16-bit values into the tile (K as bf16, the type of q; V as f16, the
-// type of the weights: a product has one type, and code * scale is exact in both): row r's 16-byte chunk c of a half (64 dims) is at
+// type of the weights: a product has one type, and code * scale is exact in
+// both): row r's 16-byte chunk c of a half (64 dims) is at
 // r * 128 + 16 (c ^ (r & 7)). Lanes of the upper half take their four chunks
 // in the order 2, 3, 0, 1: eight lanes (two rows, four q) then write eight
 // different 16-byte columns of the 128-byte rows, and no bank twice.
@@ -1377,8 +1417,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         int prow;
         const size_t q_at = query(valid, prow);
         // two parts per block: its first segment's and its last one's, each of
-        // two query tiles, O / l rounded to f16: half a step is 2^-12 of an
-        // element, a sixteenth of the output's, and halves the merge's bytes
+        // two query tiles, O / l rounded to f16: off by at most 2^-11 of an
+        // element, an eighth of the output's own rounding, and half the bytes
         const size_t part = 2 * (2 * static_cast<size_t>(blockIdx.x) + (s.index ? 1 : 0)) + (pair ? x : 0);
         uint4* po = p.part + part * 16 * kBM + lrow;
         if (l != l) m = 0.f;  // a NaN row stays one in every merge
