@@ -318,13 +318,15 @@ class Views(list):
         self.dev = on.pop()
         first = self[0].c
         self.c = (type(first) * len(self))(*[x.c for x in self])
-        self.at = ctypes.addressof(self.c)
+        self.n, self.kind, self.at = len(self), type(self[0]), ctypes.addressof(self.c)
         self.heads = (self[0].rows, self[0].L) if isinstance(first, TreeC) else (first.n_kv_heads, first.head_dim)
 
 
 def _views(x, kind):
     """x (a Views, a list of views, or one view) as a Views; its items checked.
     The array of one view alone is kept with it."""
+    if type(x) is Views and x.kind is kind:
+        return x
     if isinstance(x, kind):
         alone = x.__dict__.get("_alone")
         if alone is None:
@@ -332,8 +334,8 @@ def _views(x, kind):
         return alone
     if not isinstance(x, Views):
         x = Views(x if isinstance(x, (list, tuple)) else [x])
-    if not isinstance(x[0], kind):
-        raise TypeError(f"glance: expected {kind.__name__} views, got {type(x[0]).__name__}")
+    if not issubclass(x.kind, kind):
+        raise TypeError(f"glance: expected {kind.__name__} views, got {x.kind.__name__}")
     return x
 
 
@@ -608,20 +610,19 @@ def dense_swiglu(h, W_gate, W_up, in_sumsq, eps, act, stream=None):
 # ------------------------------------------- norm + rotary, 4-bit caches
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_I32, _F32T, _BF16T = torch.int32, torch.float32, torch.bfloat16
 
 
-def _on(stream, views, *tensors):
-    """The stream to launch on: the given one, else the tensors' device's
-    current one. All tensors and views must be on the current device."""
-    dev = views.dev
-    for t in tensors:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError("glance: every array argument must be a CUDA tensor of one device")
+def _on(stream, dev):
+    """The stream to launch on: the given one, else the device's current one.
+    The device must be the current one."""
     if dev != torch._C._cuda_getDevice():
         raise ValueError("glance: the tensors are not on the current device")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _elsewhere():
+    return ValueError("glance: every array argument must be a CUDA tensor of one device")
 
 
 def qk_norm_rope(qkv, n_q_heads, q_norm, k_norm, eps, pos, rope, q_out, kv, stream=None):
@@ -629,55 +630,57 @@ def qk_norm_rope(qkv, n_q_heads, q_norm, k_norm, eps, pos, rope, q_out, kv, stre
     of q and k, rotary position, q to q_out [B * M][Hq][D], k and v to slots
     T.. of kv (one KVLayer, or B of them). pos int32 [n_axes][B * M]."""
     kv = _views(kv, KVLayer)
-    B, (Hkv, D) = len(kv), kv.heads
-    shape, strides, dtype = qkv.shape, qkv.stride(), qkv.dtype
-    rows = shape[0]
-    if (len(shape) != 2 or strides[1] != 1 or rows % B or shape[1] != (n_q_heads + 2 * Hkv) * D or rope.head_dim != D):
+    B, dev, (Hkv, D), shape, dtype = kv.n, kv.dev, kv.heads, qkv.shape, qkv.dtype
+    rows, (step, unit) = shape[0], qkv.stride() if len(shape) == 2 else (0, 0)
+    if unit != 1 or rows % B or shape[1] != (n_q_heads + 2 * Hkv) * D or rope.head_dim != D:
         raise ValueError("glance: qkv must be [B * M, (n_q_heads + 2 * n_kv_heads) * head_dim], rope and kv of its head_dim")
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
-    if pos.dtype != torch.int32 or pos.shape[-1] != rows or pos.numel() != rope.n_axes * rows or not pos.is_contiguous():
+    if pos.dtype is not _I32 or pos.shape[-1] != rows or pos.numel() != rope.n_axes * rows or not pos.is_contiguous():
         raise ValueError("glance: pos must be contiguous int32 [n_axes, B * M]")
-    if q_out.dtype != dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
+    if q_out.dtype is not dtype or q_out.numel() != rows * n_q_heads * D or not q_out.is_contiguous():
         raise ValueError("glance: q_out must be contiguous [B * M, n_q_heads, head_dim] of qkv's dtype")
-    tensors, norms = [qkv, pos, q_out], [None, None]
-    for i, w in enumerate((q_norm, k_norm)):
-        if w is not None:
-            if w.dtype != torch.float32 or w.numel() != D or not w.is_contiguous():
-                raise ValueError("glance: norm weights must be contiguous float32 [head_dim]")
-            tensors.append(w)
-            norms[i] = w.data_ptr()
-    s = _on(stream, kv, *tensors)
-    _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _DTYPES[dtype], B, rows // B, strides[0] if rows > 1 else shape[1],
-                                     n_q_heads, norms[0], norms[1], eps, pos.data_ptr(), rope.at, q_out.data_ptr(), kv.at, s))
+    if qkv.get_device() != dev or pos.get_device() != dev or q_out.get_device() != dev:
+        raise _elsewhere()
+    _check(lib().glance_qk_norm_rope(qkv.data_ptr(), _DTYPES[dtype], B, rows // B, step if rows > 1 else shape[1], n_q_heads,
+                                     None if q_norm is None else _norm(q_norm, D, dev),
+                                     None if k_norm is None else _norm(k_norm, D, dev), eps, pos.data_ptr(), rope.at,
+                                     q_out.data_ptr(), kv.at, _on(stream, dev)))
 
 
-def _rows16(x, n_layers, kv, rows):
-    if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.shape != (n_layers, 2, kv.heads[0], rows, 128):
+def _norm(w, D, dev):
+    if w.dtype is not _F32T or w.numel() != D or not w.is_contiguous():
+        raise ValueError("glance: norm weights must be contiguous float32 [head_dim]")
+    if w.get_device() != dev:
+        raise _elsewhere()
+    return w.data_ptr()
+
+
+def _rows16(x, layers, rows):
+    if x.dtype is not _BF16T or not x.is_contiguous() or x.shape != (layers.n, 2, layers.heads[0], rows, 128):
         raise ValueError("glance: rows must be contiguous bfloat16 [n_layers, 2, n_kv_heads, rows, 128]")
+    if x.get_device() != layers.dev:
+        raise _elsewhere()
+    return x.data_ptr()
 
 
 def kv4_write_rows(src, layers, rows, stream=None):
     """Quantise src [n_layers, 2, n_kv_heads, rows, 128] (bf16, K before V) into
     every layer's 4-bit cache at slots T..T+rows-1 (T read on the device)."""
     layers = _views(layers, KV4Layer)
-    _rows16(src, len(layers), layers, rows)
-    s = _on(stream, layers, src)
-    _check(lib().glance_kv4_write_rows(src.data_ptr(), layers.at, len(layers), rows, s))
+    _check(lib().glance_kv4_write_rows(_rows16(src, layers, rows), layers.at, layers.n, rows, _on(stream, layers.dev)))
 
 
 def kv4_read_rows(layers, first, rows, dst, stream=None):
     """dst [n_layers, 2, n_kv_heads, rows, 128] (bf16) = the values of slots
     first .. first + rows - 1 of every layer's 4-bit cache."""
     layers = _views(layers, KV4Layer)
-    _rows16(dst, len(layers), layers, rows)
-    s = _on(stream, layers, dst)
-    _check(lib().glance_kv4_read_rows(layers.at, len(layers), first, rows, dst.data_ptr(), s))
+    _check(lib().glance_kv4_read_rows(layers.at, layers.n, first, rows, _rows16(dst, layers, rows), _on(stream, layers.dev)))
 
 
 def kv4_tree_attention_workspace_bytes(rows, n_q_heads, kvs):
     kvs = _views(kvs, KV4Layer)
-    return lib().glance_kv4_tree_attention_workspace_bytes(len(kvs), rows, n_q_heads, kvs.at)
+    return lib().glance_kv4_tree_attention_workspace_bytes(kvs.n, rows, n_q_heads, kvs.at)
 
 
 _DECODE = {}
@@ -688,10 +691,10 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
     [N+1][Hq][128] too), kvs B KV4Layer views, trees B Tree objects. trees
     None: plain decoding, one row per request that sees the prefix and itself."""
     kvs = _views(kvs, KV4Layer)
-    B, shape, bf16 = len(kvs), q.shape, torch.bfloat16
+    B, dev, shape = kvs.n, kvs.dev, q.shape
     rows, heads = shape[-3], shape[-2]
-    if q.dtype != bf16 or out.dtype != bf16 or not q.is_contiguous() or not out.is_contiguous() or shape != out.shape \
-            or shape[-1] != 128 or q.numel() != B * rows * heads * 128:
+    if q.dtype is not _BF16T or out.dtype is not _BF16T or not q.is_contiguous() or not out.is_contiguous() \
+            or shape != out.shape or shape[-1] != 128 or q.numel() != B * rows * heads * 128:
         raise ValueError("glance: q and out must be contiguous bfloat16 [B, N + 1, n_q_heads, 128]")
     if trees is None:
         c = _DECODE.get(B)
@@ -702,18 +705,28 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
             raise ValueError("glance: without trees q has one row per request")
     else:
         trees = _views(trees, Tree)
-        if len(trees) != B or trees.heads[0] != rows:
+        if trees.n != B or trees.heads[0] != rows:
             raise ValueError("glance: need one tree of q's N + 1 rows per request")
-        if trees.dev != kvs.dev:
-            raise ValueError("glance: the trees must be on the caches' device")
+        if trees.dev != dev:
+            raise _elsewhere()
         c = trees.at
-    s = _on(stream, kvs, q, out, ws)
-    _check(lib().glance_kv4_tree_attention(q.data_ptr(), heads, kvs.at, c, B, scale, out.data_ptr(),
-                                           ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    if q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev:
+        raise _elsewhere()
+    _check(lib().glance_kv4_tree_attention(q.data_ptr(), heads, kvs.at, c, B, scale, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                           _on(stream, dev)))
 
 
 def kv4_accept_commit_workspace_bytes(B, n_layers):
     return lib().glance_kv4_accept_commit_workspace_bytes(B, n_layers)
+
+
+def _array(x, dtype, n, dev):
+    if x.dtype is not dtype or x.numel() < n or not x.is_contiguous():
+        raise ValueError("glance: argmax, n_accepted, accepted_tok, new_root and gated must be contiguous int32 [B, N + 1], [B], "
+                         "[B, L], [B], [B], gap contiguous float32 [B, N + 1]")
+    if x.get_device() != dev:
+        raise _elsewhere()
+    return x.data_ptr()
 
 
 def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root, ws, gap=None, gate_threshold=0.0,
@@ -722,31 +735,17 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
     B * n_layers KV4Layer views (request-major), argmax [B][N+1], outputs [B],
     [B][L], [B]. With gap [B][N+1] and gated [B]: the tie-aware gate."""
     trees, layers = _views(trees, Tree), _views(layers, KV4Layer)
-    B, n_layers, (rows, L) = len(trees), len(layers), trees.heads
-    if n_layers % B:
+    B, dev, (rows, L) = trees.n, layers.dev, trees.heads
+    if layers.n % B:
         raise ValueError("glance: layers must hold the same number of views for every request")
-    if trees.dev != layers.dev:
-        raise ValueError("glance: the trees must be on the caches' device")
-    i32 = torch.int32
-    for x, n in ((argmax, B * rows), (n_accepted, B), (accepted_tok, B * L), (new_root, B)):
-        if x.dtype != i32 or x.numel() < n or not x.is_contiguous():
-            raise ValueError("glance: argmax, n_accepted, accepted_tok and new_root must be contiguous int32 "
-                             "[B, N + 1], [B], [B, L], [B]")
-    tensors = [argmax, n_accepted, accepted_tok, new_root, ws]
-    if gap is not None:
-        if gap.dtype != torch.float32 or gap.numel() < B * rows or not gap.is_contiguous():
-            raise ValueError("glance: gap must be contiguous float32 [B, N + 1]")
-        tensors.append(gap)
-    if gated is not None:
-        if gated.dtype != i32 or gated.numel() < B or not gated.is_contiguous():
-            raise ValueError("glance: gated must be contiguous int32 [B]")
-        tensors.append(gated)
-    s = _on(stream, layers, *tensors)
-    _check(lib().glance_kv4_accept_commit(trees.at, B, argmax.data_ptr(), None if gap is None else gap.data_ptr(),
-                                          gate_threshold, layers.at, n_layers // B, n_accepted.data_ptr(),
-                                          accepted_tok.data_ptr(), new_root.data_ptr(),
-                                          None if gated is None else gated.data_ptr(), ws.data_ptr(),
-                                          ws.numel() * ws.element_size(), s))
+    if trees.dev != dev or ws.get_device() != dev:
+        raise _elsewhere()
+    _check(lib().glance_kv4_accept_commit(trees.at, B, _array(argmax, _I32, B * rows, dev),
+                                          None if gap is None else _array(gap, _F32T, B * rows, dev), gate_threshold, layers.at,
+                                          layers.n // B, _array(n_accepted, _I32, B, dev), _array(accepted_tok, _I32, B * L, dev),
+                                          _array(new_root, _I32, B, dev),
+                                          None if gated is None else _array(gated, _I32, B, dev), ws.data_ptr(), ws.nbytes,
+                                          _on(stream, dev)))
 
 
 def device_status():
