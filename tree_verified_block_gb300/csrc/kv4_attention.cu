@@ -16,8 +16,8 @@
 // up to 16, the call is bound by the cache's bytes (kv4_attention_few_kernel);
 // beyond, by the products (kv4_attention_wide_kernel, with the tensor core's
 // 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 58.3
-// and 111 us on 131072 slots, 27.8 and 35.9 on 32768, 22.0 and 31.4 for 8
-// requests of 512 to 8192, but 15.7 and 13.0 on 4096; the host that picks the
+// and 111 us on 131072 slots, 28.0 and 35.9 on 32768, 21.7 and 31.4 for 8
+// requests of 512 to 8192, but 15.2 and 13.0 on 4096; the host that picks the
 // kernel does not know T.
 #include "kv4_internal.cuh"
 
@@ -269,6 +269,7 @@ struct FewMisc {
   uint64_t full[kFewWarps][kFewStages];
   Segment seg;
   Plan plan;
+  float factor[kFewRows];  // of the query rows' scores
   int any;
   int first_part, n_parts;  // of the segment's group: 2 * block + (the block's first or last segment)
   int last;
@@ -401,59 +402,63 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   // below, dims 32c ..; Q: row r, dims 32c ..; a lane's scores and O are of
   // query rows 2c and 2c + 1 (of each eight).
   const int r = lane >> 2, c = lane & 3;
-  uint32_t q[16];  // of eight rows; of sixteen in shared memory, for want of registers
-  float sc[kN][2];
   uint32_t seen[kN][2];  // visible tree rows (at most 16)
-  uint4 v[kN][4];
 #pragma unroll
-  for (int n = 0; n < kN; ++n) {
-    const int row = 8 * n + r;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (q_base + static_cast<size_t>(row % p.rows) * p.Hq + row / p.rows) * kD + 32 * c);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[n][e] = row < R ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int qr = 8 * n + 2 * c + h, i = qr % p.rows;
       seen[n][h] = qr >= R ? 0u : rq.anc ? static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned long long*>(rq.anc) + i * p.W)) : 1u << i;
     }
-  }
+  // a warp has kN of the query rows, a lane 8 dims of one of them
+  const int q_row = kN * warp + (lane >> 4), piece = lane & 15;
+  const bool has_q = kN == 2 || lane < 16;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (has_q && q_row < R)
+    v = __ldg(reinterpret_cast<const uint4*>(p.q + (q_base + static_cast<size_t>(q_row % p.rows) * p.Hq + q_row / p.rows) * kD) + piece);
   // the first copies go out behind these loads and before their use
   if (lane == 0 && !dead)
     for (int s = 0; s < kFewStages; ++s)
       if (u0 + warp + s * kFewWarps < u1)
         few_copy(rq, head0, u0 + warp + s * kFewWarps, n_keys, my_ring + (stage + s) % kFewStages * kUnitBytes,
                  &ms->full[warp][(stage + s) % kFewStages]);
+  {
+    // the largest magnitude's bits: in the order of the absolute values
+    uint32_t top = max(max(v.x & 0x7FFFu, v.y & 0x7FFFu), max(v.z & 0x7FFFu, v.w & 0x7FFFu));
+    top = max(top, max(max(v.x & 0x7FFF0000u, v.y & 0x7FFF0000u), max(v.z & 0x7FFF0000u, v.w & 0x7FFF0000u)) >> 16);
 #pragma unroll
-  for (int n = 0; n < kN; ++n) {
-    uint32_t top = 0;  // the largest magnitude's bits: in the order of the absolute values
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      top = max(top, max(max(v[n][e].x & 0x7FFFu, v[n][e].y & 0x7FFFu), max(v[n][e].z & 0x7FFFu, v[n][e].w & 0x7FFFu)));
-      top = max(top, max(max(v[n][e].x & 0x7FFF0000u, v[n][e].y & 0x7FFF0000u), max(v[n][e].z & 0x7FFF0000u, v[n][e].w & 0x7FFF0000u)) >> 16);
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float amax = top >= 0x7F80u ? INFINITY : __uint_as_float(top << 16);
     const float qf = query_factor(amax);
-    const float factor = score_factor(amax, qf, p.scale_log2, rq.k_global);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t w[4] = {v[n][e].x, v[n][e].y, v[n][e].z, v[n][e].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[4 * e + i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
-    }
-    if (kN > 1 && warp == 0) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sq[(4 * n + e) * 32 + lane] = make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sc[n][h] = __shfl_sync(0xffffffffu, factor, 4 * (2 * c + h));
-      seen[n][h] &= (1u << p.rows) - 1u;  // rows <= 16
+    for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
+    if (has_q) {
+      sq[(4 * (q_row >> 3) + (piece & 3)) * 32 + 4 * (q_row & 7) + (piece >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
+      if (piece == 0) ms->factor[q_row] = score_factor(amax, qf, p.scale_log2, rq.k_global);
     }
   }
-  if (kN > 1) __syncthreads();
+  __syncthreads();
+  uint32_t q[16];  // of eight rows; of sixteen in shared memory, for want of registers
+  float sc[kN][2];
+#pragma unroll
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[n][h] = ms->factor[8 * n + 2 * c + h];
+      seen[n][h] &= (1u << p.rows) - 1u;  // rows <= 16
+    }
+  if (kN == 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint4 f = sq[e * 32 + lane];
+      q[4 * e] = f.x;
+      q[4 * e + 1] = f.y;
+      q[4 * e + 2] = f.z;
+      q[4 * e + 3] = f.w;
+    }
+  }
   float o[8][kN][4];
 #pragma unroll
   for (int t = 0; t < 8; ++t)
@@ -807,8 +812,9 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // core works 2048: a slot's chain is S and O's products (1380 with the other
 // slot's in between) and the softmax (2080), and tensor memory (two S, two O of
 // 128 columns) has no room for a second S per slot that would let them overlap.
-// S of 64 slots, which has, reads Q from shared memory twice as often and takes
-// 170 us. Short calls are start-up: 1.4 us until the block knows its work, 3
+// S in two halves of 64 slots, which has, takes 170 us (twice the products, Q
+// read from shared memory twice as often), weights handed over by halves 136: a
+// hand-over costs more than what it lets overlap. Short calls are start-up: 1.4 us until the block knows its work, 3
 // until the first S, 3.1 for two tiles, 0.85 for the output, 1 between the
 // kernels, 3 for the merge (joining inside this kernel takes 17.9 us instead of
 // 16.0 at 4096, blocks that wait for one another).
