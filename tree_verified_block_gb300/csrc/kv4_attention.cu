@@ -806,11 +806,12 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // A group that one block has whole is written out there; the others' parts are
 // merged by a second kernel.
 //
-// Measured (32 / 8 heads, 64 rows): 131072 slots 117.5 us, 61 % of the tensor
-// rate on the products' operations; 4096 slots 15.4 us; 8 requests of 512 to
-// 8192 slots 39.5 us. A pair of tiles takes 3550 clocks, of which the tensor
+// Measured (32 / 8 heads, 64 rows): 131072 slots 115.3 us, 62 % of the tensor
+// rate on the products' operations; 4096 slots 15.1 us; 8 requests of 512 to
+// 8192 slots 38.9 us. A pair of tiles takes 3500 clocks, of which the tensor
 // core works 2048: a slot's chain is S and O's products (1380 with the other
-// slot's in between) and the softmax (2080), and tensor memory (two S, two O of
+// slot's in between) and the softmax (2080), the conversion warps need about as
+// long for the pair's K and V, and tensor memory (two S, two O of
 // 128 columns) has no room for a second S per slot that would let them overlap.
 // S in two halves of 64 slots, which has, takes 170 us (twice the products, Q
 // read from shared memory twice as often), weights handed over by halves 136: a
