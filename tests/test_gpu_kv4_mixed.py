@@ -55,11 +55,13 @@ def test_one_workspace_serves_calls_of_every_shape(dev, clean_status):
                     l.t_len -= 1
 
 
-# more groups (request, kv head, pair of query tiles) than blocks, and an odd
-# number of query tiles per kv head
+# more groups (request, kv head, pair of query tiles) than blocks, an odd number
+# of query tiles per kv head, and blocks with pairs of query tiles and single ones
+# in every order
 @pytest.mark.parametrize("N,Hq,Hkv,Ts", [
     (0, 32, 32, [300 + 37 * r for r in range(16)]), (0, 320, 320, [40, 90]), (3, 64, 32, [5, 0, 77, 1000] * 4),
-    (20, 16, 16, [64, 200, 30, 7] * 4), (130, 16, 8, [300, 20, 700]), (100, 200, 200, [150]), (255, 32, 8, [90, 1000])])
+    (20, 16, 16, [64, 200, 30, 7] * 4), (130, 16, 8, [300, 20, 700]), (100, 200, 200, [150]), (255, 32, 8, [90, 1000]),
+    (128, 192, 24, [265, 21, 198]), (130, 80, 40, [265, 21, 198]), (128, 24, 24, [1, 2, 700, 31] * 4), (200, 64, 16, [40] * 16)])
 def test_many_heads(dev, clean_status, N, Hq, Hkv, Ts):
     check(dev, Ts, N, Hq, Hkv, seed=43)
 

@@ -1222,7 +1222,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
       const int R = p.G * p.rows;
-      uint32_t n_s = 0, n_o[2] = {0, 0};  // phases of s_full (this slot) and o_done so far
+      uint32_t n_s = 0, n_o = 0;  // phases of this slot's s_full and o_done so far
       bool ok = true;
       bool ahead = false;  // the segment's Q is in its tile already
       // A segment's Q into the slot's tile, 16 bytes at a time (thread = chunk, 16
@@ -1436,7 +1436,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           Segment next = s;
           ahead = next_segment<kWideLead>(p, pl, next) && (!x || 2 * (next.g % p.n_qp) + 1 < p.n_qt);
           if (ahead) copy_q(next);
-          ok = wide_wait(&ms->o_done[x], n_o[x]++ & 1, ms);
+          ok = wide_wait(&ms->o_done[x], n_o++ & 1, ms);
           if (!ok) break;
           tc_fence_after();
           if (ahead) q_copied();
@@ -1459,7 +1459,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           // both slots have this query tile: slot x writes dims 64x .. 64x + 63
           float2(*ml)[kBM] = ms->ml[s.index & 1];
           ml[x][lrow] = make_float2(m, l);
-          ok = ok && wide_wait(&ms->o_done[0], n_o[0]++ & 1, ms) && (run.tiles < 2 || wide_wait(&ms->o_done[1], n_o[1]++ & 1, ms));
+          // each waits for its own products (one tile: slot 1 has none), the barrier for the other's
+          if (ok && x < run.tiles) ok = wide_wait(&ms->o_done[x], n_o++ & 1, ms);
+          tc_fence_before();
           ok = !named_bar_or(1, 256, !ok);  // both go on, or both leave
           if (!ok) {
             s.left = 0;
