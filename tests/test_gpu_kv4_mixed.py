@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import workloads as W
-from _kv4_util import layer_of, random_cache, random_tree, up, upload_tree
+from _kv4_util import anc_words, attention64, layer_of, random_cache, random_tree, up, upload_tree
 from _util import bf16_tensor
 from test_gpu_kv4_attention import check
 
@@ -64,6 +64,54 @@ def test_one_workspace_serves_calls_of_every_shape(dev, clean_status):
     (128, 192, 24, [265, 21, 198]), (130, 80, 40, [265, 21, 198]), (128, 24, 24, [1, 2, 700, 31] * 4), (200, 64, 16, [40] * 16)])
 def test_many_heads(dev, clean_status, N, Hq, Hkv, Ts):
     check(dev, Ts, N, Hq, Hkv, seed=43)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_batches_on_one_workspace(dev, seed):
+    """Any geometry, lengths, masks (also ones that leave rows empty) and requests
+    without room in between, on one workspace: the formula's output, the same bits
+    twice, and nothing written for a request without room."""
+    import tree_verified_block_gb300 as g
+    g.reset_device_status()
+    gen = W.rng(71, seed)
+    kg, vg, scale = 0.75, 5.5 / 2688, 128 ** -0.5
+    ws = None
+    for _ in range(8):
+        B, Hkv, G = (int(gen.choice(c)) for c in ([1, 2, 3, 5, 16], [1, 2, 3, 8, 24], [1, 2, 4, 8]))
+        N, hi = int(gen.choice([0, 1, 3, 7, 15, 16, 31, 63, 64, 100, 128, 200, 255])), int(gen.choice([2, 40, 300, 2000]))
+        rows, Hq, hi = N + 1, G * Hkv, max(2, min(hi, 100000 // (B * Hkv)))
+        caches, layers, trees, seens, Ts, room = [], [], [], [], [], []
+        for _ in range(B):
+            T = int(gen.integers(0, hi))
+            cap = T + rows + (T + rows) % 2
+            room.append(bool(gen.random() > 0.2))
+            t_len = T if room[-1] else int(gen.choice([-1, cap - rows + 1, 2 ** 31 - 1]))
+            t = random_tree(gen, N, 16, T)
+            if N and gen.random() < 0.5:
+                t["seen"] = np.tril(gen.random((rows, rows)) < gen.choice([0.02, 0.5, 0.98]))
+                t["anc"] = anc_words(t["seen"])
+            caches.append(random_cache(gen, Hkv, cap, kg, vg))
+            layers.append(layer_of(g, caches[-1], torch.tensor([t_len], dtype=torch.int32, device=dev), dev, kg, vg))
+            trees.append(upload_tree(g, t, 16, dev))
+            seens.append(t["seen"])
+            Ts.append(T)
+        q = bf16_tensor(W.normal_bf16(gen, (B, rows, Hq, 128)), dev)
+        need = g.kv4_tree_attention_workspace_bytes(rows, Hq, layers)
+        if ws is None or ws.numel() < need:
+            ws = g.workspace(need, dev)
+        outs = [torch.full_like(q, 3.0) for _ in range(2)]
+        for out in outs:
+            g.kv4_tree_attention(q, layers, trees, scale, out, ws)
+        what = (B, Hkv, G, N, Ts, room)
+        assert g.device_status()[0] == (0 if all(room) else 2), what
+        g.reset_device_status()
+        assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16)), what
+        for r in range(B):
+            if room[r]:
+                o, tol = attention64(q[r], caches[r], Ts[r], seens[r], scale, kg, vg, dev)
+                assert torch.all((outs[0][r].double() - o).abs() <= tol), what
+            else:
+                assert torch.all(outs[0][r] == 3), what
 
 
 @pytest.mark.parametrize("N", [2, 50])
