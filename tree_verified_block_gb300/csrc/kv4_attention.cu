@@ -807,7 +807,7 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // merged by a second kernel.
 //
 // Measured (32 / 8 heads, 64 rows): 131072 slots 115.3 us, 62 % of the tensor
-// rate on the products' operations; 4096 slots 15.1 us; 8 requests of 512 to
+// rate on the products' operations; 4096 slots 14.9 us; 8 requests of 512 to
 // 8192 slots 38.9 us. A pair of tiles takes 3500 clocks, of which the tensor
 // core works 2048: a slot's chain is S and O's products (1380 with the other
 // slot's in between) and the softmax (2080), the conversion warps need about as
