@@ -866,6 +866,9 @@ struct Run {
   __device__ __forceinline__ int key0(int j) const { return k0 + j * kBN; }
   // columns of tile j that its products compute, a multiple of 32
   __device__ __forceinline__ int cols(int j) const { return min(kBN, (k1 - key0(j) + 31) & ~31); }
+  // whether tile j's products reach behind the prefix: the one rule by which V
+  // rows without a number are left out of them and the softmax looks at the masks
+  __device__ __forceinline__ bool tree(int j, int T) const { return key0(j) + cols(j) > T; }
 };
 
 __device__ __forceinline__ void wide_fail(WideMisc* ms) {
@@ -1188,10 +1191,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           load_raw(x, src, src + kRawCodes, row, q, run.k1 - key0);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms->raw_empty[rs]);
-          if (is_v && key0 + kBN > T) {
+          if (is_v && run.tree(e >> 1, T)) {
             // a V row with a scale that is not a number is left out: 0 * NaN
             // would reach the rows that do not see it (the softmax marks the
-            // scores of those that do)
+            // scores of those that do). In a tile of prefix slots alone it stays:
+            // every row sees it
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const bool nan = (x.scales[i] & 0x7Fu) == 0x7Fu || (x.scales[i] & 0x7F00u) == 0x7F00u;
@@ -1287,7 +1291,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         for (int j = j0; j < run.tiles; j += step) {
           const int key0 = run.key0(j);
           const int nc = run.cols(j) / 32;
-          const bool tree = key0 + 32 * nc > T;
+          const bool tree = run.tree(j, T);
           uint32_t bad[4] = {0u, 0u, 0u, 0u};  // slots with a V scale that is not a number
           uint32_t vis[4];                     // slots that the row sees
           if (tree) {
