@@ -671,7 +671,8 @@ size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_head
  * aligned and not overlapping, workspace 256-byte aligned. A request with
  * T + N + 1 > t_cap sets device status 2 and its out is left as it was.
  * Arithmetic: code * scale is exact; the softmax weights are rounded to f16
- * (2^-11 of each), sums and maxima are fp32, out is rounded to bf16 once. With
+ * (2^-11 of each, or 2^-32 of the row's largest weight for those below 2^-21 of
+ * it), sums and maxima are fp32, out is rounded to bf16 once. With
  * n_q_heads / n_kv_heads * (N + 1) <= 16 q is used to 2^-31 of its row's largest
  * element (smaller ones lose bits), beyond that as it is, and partial results
  * of a row that several blocks share are rounded to f16 between them (2^-11 of

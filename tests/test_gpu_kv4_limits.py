@@ -1,13 +1,17 @@
 """Attention over 4-bit caches at the limits of its formats: scales that are not
 numbers next to the end of the prefix, weights far below the largest, query rows
 that are not finite."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import workloads as W
+from _kv4_tight import tight64
 from _kv4_util import layer_of, random_cache, random_tree, upload_tree
 from _util import bf16_tensor
+from oracle import kv4 as okv4
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +50,42 @@ def test_a_scale_that_is_no_number_at_the_end_of_the_prefix_reaches_every_row(de
                 scales[head, slot, 3] = old
         g.kv4_tree_attention(q, views, c_trees, 0.09, out, ws)
         assert not out.isnan().any()
+
+
+def sinks(Hkv, n, T):
+    """Bytes of a cache of n slots: every 96th prefix slot has a large K in its
+    first dim and V = 0, the others K = 0 and V that differs by dim only, at the
+    largest scale."""
+    code = np.zeros((Hkv, n, 128), np.uint8)
+    at = np.arange(5, T, 96)
+    k = code.copy()
+    k[:, at, 0] = 7  # magnitude 6
+    v = code.copy()
+    v[:] = np.resize(np.array([1, 7, 10, 15, 4, 13], np.uint8), 128)
+    v[:, at] = 0
+    one = np.full((Hkv, n, 8), 0x38, np.uint8)
+    return [okv4.pack(k), one, okv4.pack(v), np.full_like(one, 0x7E)]
+
+
+@pytest.mark.parametrize("below", [20.7, 25.5])
+@pytest.mark.parametrize("N,Hq,Hkv,T", [(0, 1, 1, 20000), (0, 32, 8, 5000), (9, 1, 1, 20000), (3, 8, 2, 3001), (40, 1, 1, 20000),
+                                        (63, 8, 1, 20000), (63, 32, 8, 4096), (255, 2, 1, 9001)])
+def test_many_small_weights_beside_large_ones_are_kept(dev, clean_status, N, Hq, Hkv, T, below):
+    """Attention sinks: slots of a large weight and V = 0 beside many of 2^-below
+    of it, which make up the whole output."""
+    import tree_verified_block_gb300 as g
+    gen = W.rng(89, N)
+    rows = N + 1
+    cache = sinks(Hkv, T + rows + (T + rows) % 2, T)
+    t = random_tree(gen, N, 16, T)
+    layer = layer_of(g, cache, torch.tensor([T], dtype=torch.int32, device=dev), dev)
+    q = torch.zeros(1, rows, Hq, 128, dtype=torch.bfloat16, device=dev)
+    q[..., 0] = 1
+    scale = below * math.log(2) / 6
+    out = torch.zeros_like(q)
+    g.kv4_tree_attention(q, [layer], [upload_tree(g, t, 16, dev)], scale, out,
+                         g.workspace(g.kv4_tree_attention_workspace_bytes(rows, Hq, [layer]), dev))
+    o, tol = tight64(q[0], cache, T, t["seen"], scale, 1.0, 1.0, dev)
+    assert torch.all(tol < 0.04 * o.abs())  # of use: the tolerance is far below the output
+    err = (out[0].double() - o).abs()
+    assert torch.all(err <= tol), float((err / tol).max())

@@ -4,13 +4,17 @@
 // and the tree slots of its own ancestors; N = 0 is one row, plain decoding.
 //
 //   o = sum_s w_s v_s / sum_s w_s,  w_s = 2^(q . k_s * scale * log2 e - m),
-// over the visible slots s in one pass: m is a running maximum that may lag the
-// true one by 8 (the weights then stay below 2^8), and what was summed before
-// is rescaled when it moves. k_s and v_s are code * scale; the globals go into
-// the score factor and the output. Sums, maxima and O are fp32; the weights
-// enter the second product as f16 (half a step 2^-11 of each, at most an
-// eighth of the output's own rounding to bf16), because V's 6 significant bits
-// are exact in f16 and a product takes one 16-bit type.
+// over the visible slots s in one pass: m + 7 is a running maximum that may lag
+// the true one by 8, and what was summed before is rescaled when it moves. k_s
+// and v_s are code * scale; the globals go into the score factor and the output.
+// Sums, maxima and O are fp32; the weights enter the second product as f16,
+// because V's 6 significant bits are exact in f16 and a product takes one 16-bit
+// type. Half a step is 2^-11 of a weight, an eighth of the output's own rounding
+// to bf16, down to 2^-21 of the largest weight, and 2^-32 of the largest weight
+// below: the 7 puts the largest at 2^7 to 2^15, the top of f16's range, so that
+// the small ones of a long prefix beside a few large ones are not lost (with the
+// largest at 1 to 2^8, 20000 weights of 2^-25.5 came out as nothing). It cancels
+// between O and the sum and costs no instruction.
 //
 // Two kernels, by the query rows that share a kv head (G heads x N + 1 rows):
 // up to 16, the call is bound by the cache's bytes (kv4_attention_few_kernel);
@@ -30,6 +34,9 @@ namespace {
 constexpr int kD = glance::kKv4D;
 constexpr int kMaxB = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+// The m of a row is kept this much (log2) under its running maximum, and moves
+// when the maximum has grown by 8: weights are at most 2^15.
+constexpr float kUnder = 7.f, kGrow = kUnder + 8.f;
 
 struct Request {
   const unsigned char* k;
@@ -560,11 +567,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sc[n][h];  // sc > 0, or NaN (then mx is of no account)
-        // the running maximum moves only when it has grown by 8 (in log2): until
-        // then the weights stay below 2^8 and nothing is rescaled
-        const bool grow = mx > m[n][h] + 8.f;
+        // m moves only when the maximum has grown by 8 (in log2): until then the
+        // weights stay below 2^15 and nothing is rescaled
+        const bool grow = mx > m[n][h] + kGrow;
         if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? mx : m[n][h];
+          const float mn = grow ? mx - kUnder : m[n][h];
           const float alpha = m[n][h] == -INFINITY ? 0.f : ex2_approx(m[n][h] - mn);
           m[n][h] = mn;
           l[n][h] *= alpha;
@@ -1356,10 +1363,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
               }
             }
             const float mt = fmaxf(max3f(mx[0], mx[1], mx[2]), max3f(max3f(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sc;
-            // the running maximum moves when some row of the warp grew by 8 (log2):
-            // a stale one keeps the weights below 2^8 and cancels between O and l
-            if (__any_sync(0xffffffffu, mt > m + 8.f)) {
-              const float mn = fmaxf(m, mt);
+            // m moves when some row of the warp grew by 8 (log2): a stale one keeps
+            // the weights below 2^15 and cancels between O and l
+            if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+              const float mn = fmaxf(m, mt - kUnder);
               const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - mn);
               m = mn;
               l *= alpha;
@@ -1420,7 +1427,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           if (lane == 0) mbar_arrive(&ms->p_ready[x]);
         }
         if (!ok && pair) break;
-        // a row that sees a prefix slot has a weight of about 1 unless all its
+        // a row that sees a prefix slot has a weight of 2^7 or more unless all its
         // scores are -infinity: then it is no number
         if (l == 0.f && j0 < run.tiles && run.key0(j0) < T) l = __uint_as_float(0x7FC00000u);
         // ------------------------------------------------ the segment's output
