@@ -322,15 +322,27 @@ class Views(list):
         self.heads = (self[0].rows, self[0].L) if isinstance(first, TreeC) else (first.n_kv_heads, first.head_dim)
 
 
+class _Alone:
+    """What a call needs to know of one view by itself: its C struct is an array
+    of one. Kept with the view, so it must not refer to it: the caches of a view
+    that is dropped are freed at once."""
+    __slots__ = ("c", "at", "n", "kind", "dev", "heads")
+
+    def __init__(self, view):
+        checked = Views([view])
+        self.c, self.at, self.n = view.c, ctypes.addressof(view.c), 1
+        self.kind, self.dev, self.heads = checked.kind, checked.dev, checked.heads
+
+
 def _views(x, kind):
-    """x (a Views, a list of views, or one view) as a Views; its items checked.
-    The array of one view alone is kept with it."""
+    """x (a Views, a list of views, or one view) with its items checked, as a
+    Views or, one view by itself, an _Alone."""
     if type(x) is Views and x.kind is kind:
         return x
     if isinstance(x, kind):
         alone = x.__dict__.get("_alone")
-        if alone is None:
-            alone = x._alone = Views([x])
+        if alone is None or alone.c is not x.c:
+            alone = x._alone = _Alone(x)
         return alone
     if not isinstance(x, Views):
         x = Views(x if isinstance(x, (list, tuple)) else [x])
