@@ -61,3 +61,19 @@ def test_a_view_alone_is_passed_as_it_is_at_the_call(b, kind):
     x.c = c(n_kv_heads=2, head_dim=128, t_cap=16)
     assert c.from_address(b._views(x, kind).at).t_cap == 16
     assert ctypes.addressof(x.c) == b._views(x, kind).at
+
+
+def test_views_do_not_change(b):
+    """The C array is laid out once and holds addresses of the views' tensors."""
+    layers = [view_of(b, b.KV4Layer) for _ in range(3)]
+    v = b.Views(x for x in layers)
+    assert list(v) == layers and v.n == len(v) == 3
+    for change in (lambda: v.append(layers[0]), lambda: v.clear(), lambda: v.pop(), lambda: v.extend(layers), lambda: v.insert(0, 1),
+                   lambda: v.__setitem__(0, layers[1]), lambda: v.__delitem__(0)):
+        with pytest.raises(AttributeError):
+            change()
+    assert b._views(v, b.KV4Layer) is v
+    twice = v
+    twice += (layers[0],)  # a new tuple, which a call lays out anew
+    assert v.n == len(v) == 3 and b._views(twice, b.KV4Layer).n == 4
+    assert b._views(v[:2], b.KV4Layer).n == 2

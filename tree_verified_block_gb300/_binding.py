@@ -301,13 +301,13 @@ class KV4Layer:
                    torch.zeros((n_kv_heads, n, 64), **u8), torch.zeros((n_kv_heads, n, 8), **u8), t_len, k_global, v_global)
 
 
-class Views(list):
-    """A list of Tree, KVLayer or KV4Layer objects of one device with their C
-    array laid out once: calls that take a list of them accept it without
-    building the array again. The list must not be changed afterwards."""
+class Views(tuple):
+    """Tree, KVLayer or KV4Layer objects of one device with their C array laid
+    out once: calls that take a list of them accept it without building the
+    array again. A tuple: the array points into the objects' tensors, so none
+    may be added, exchanged or dropped."""
 
     def __init__(self, items):
-        super().__init__(items)
         if not self:
             raise ValueError("glance: an empty list of views")
         if not all(isinstance(x, type(self[0])) and isinstance(x, (Tree, KVLayer, KV4Layer)) for x in self):
