@@ -5,6 +5,7 @@ import gc
 import weakref
 
 import pytest
+import torch
 
 from _util import ensure_built
 
@@ -17,10 +18,22 @@ def b():
 
 
 class Array:
-    """Stands for a device tensor."""
+    """Stands for a tensor on device 0."""
+
+    def __init__(self, shape=(1,), dtype=torch.uint8, contiguous=True):
+        self.shape, self.dtype, self.contiguous, self.nbytes = torch.Size(shape), dtype, contiguous, 1 << 30
 
     def get_device(self):
         return 0
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return 1 << 20
 
 
 def view_of(b, kind):
@@ -77,3 +90,15 @@ def test_views_do_not_change(b):
     twice += (layers[0],)  # a new tuple, which a call lays out anew
     assert v.n == len(v) == 3 and b._views(twice, b.KV4Layer).n == 4
     assert b._views(v[:2], b.KV4Layer).n == 2
+
+
+def test_a_workspace_that_does_not_lie_in_one_piece_is_refused(b):
+    """An expanded tensor of one byte says that it has any number of them."""
+    layer, tree = view_of(b, b.KV4Layer), view_of(b, b.Tree)
+    ws = Array(contiguous=False)
+    q = Array((4, 4, 128), torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace"):
+        b.kv4_tree_attention(q, layer, tree, 0.1, Array((4, 4, 128), torch.bfloat16), ws)
+    i32 = [Array((4,), torch.int32) for _ in range(4)]
+    with pytest.raises(ValueError, match="workspace"):
+        b.kv4_accept_commit(tree, i32[0], layer, i32[1], i32[2], i32[3], ws)

@@ -633,6 +633,16 @@ def _on(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _workspace(ws, dev):
+    """Address of a call's workspace: bytes that lie next to each other (an
+    expanded tensor counts bytes that it does not have)."""
+    if not ws.is_contiguous():
+        raise ValueError("glance: the workspace must be contiguous")
+    if ws.get_device() != dev:
+        raise _elsewhere()
+    return ws.data_ptr()
+
+
 def _elsewhere():
     return ValueError("glance: every array argument must be a CUDA tensor of one device")
 
@@ -722,9 +732,9 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
         if trees.dev != dev:
             raise _elsewhere()
         c = trees.at
-    if q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev:
+    if q.get_device() != dev or out.get_device() != dev:
         raise _elsewhere()
-    _check(lib().glance_kv4_tree_attention(q.data_ptr(), heads, kvs.at, c, B, scale, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+    _check(lib().glance_kv4_tree_attention(q.data_ptr(), heads, kvs.at, c, B, scale, out.data_ptr(), _workspace(ws, dev), ws.nbytes,
                                            _on(stream, dev)))
 
 
@@ -750,13 +760,13 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
     B, dev, (rows, L) = trees.n, layers.dev, trees.heads
     if layers.n % B:
         raise ValueError("glance: layers must hold the same number of views for every request")
-    if trees.dev != dev or ws.get_device() != dev:
+    if trees.dev != dev:
         raise _elsewhere()
     _check(lib().glance_kv4_accept_commit(trees.at, B, _array(argmax, _I32, B * rows, dev),
                                           None if gap is None else _array(gap, _F32T, B * rows, dev), gate_threshold, layers.at,
                                           layers.n // B, _array(n_accepted, _I32, B, dev), _array(accepted_tok, _I32, B * L, dev),
                                           _array(new_root, _I32, B, dev),
-                                          None if gated is None else _array(gated, _I32, B, dev), ws.data_ptr(), ws.nbytes,
+                                          None if gated is None else _array(gated, _I32, B, dev), _workspace(ws, dev), ws.nbytes,
                                           _on(stream, dev)))
 
 
