@@ -102,3 +102,19 @@ def test_a_workspace_that_does_not_lie_in_one_piece_is_refused(b):
     i32 = [Array((4,), torch.int32) for _ in range(4)]
     with pytest.raises(ValueError, match="workspace"):
         b.kv4_accept_commit(tree, i32[0], layer, i32[1], i32[2], i32[3], ws)
+
+
+def test_numbers_beyond_32_bits_are_refused(b):
+    """2^32 + x reached the library as x: other rows, another plan."""
+    layer = view_of(b, b.KV4Layer)
+    for first in (2 ** 32, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="first"):
+            b.kv4_read_rows(layer, first, 16, Array((1, 2, 2, 16, 128), torch.bfloat16))
+    with pytest.raises(ValueError, match="head_dim"):
+        b.Rope(2 ** 32 + 128, 1e4, [64])
+    with pytest.raises(ValueError, match="section"):
+        b.Rope(128, 1e4, [2 ** 32 + 64])
+    with pytest.raises(ValueError, match="rows"):
+        b.kv4_tree_attention_workspace_bytes(2 ** 32 + 1, 4, layer)
+    with pytest.raises(ValueError, match="n_layers"):
+        b.kv4_accept_commit_workspace_bytes(1, 2 ** 32 + 1)

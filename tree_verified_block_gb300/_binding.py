@@ -351,14 +351,21 @@ def _views(x, kind):
     return x
 
 
+def _i32(x, name):
+    """x as an int32: ctypes would drop the bits above."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"glance: {name} does not fit 32 bits")
+    return x
+
+
 class Rope:
     """Rotary positions as a plan (glance_rope_init): sections = how many of the
     head_dim / 2 frequencies each position axis turns (None: one axis)."""
 
     def __init__(self, head_dim, theta, sections=None, interleaved=False):
         self.c = RopeC()
-        sec = list(sections) if sections is not None else [head_dim // 2]
-        _check(lib().glance_rope_init(ctypes.byref(self.c), head_dim, float(theta), len(sec),
+        sec = [_i32(n, "a section") for n in (sections if sections is not None else [head_dim // 2])]
+        _check(lib().glance_rope_init(ctypes.byref(self.c), _i32(head_dim, "head_dim"), float(theta), len(sec),
                                       (ctypes.c_int32 * len(sec))(*sec), int(bool(interleaved))))
         self.head_dim, self.n_axes, self.at = head_dim, len(sec), ctypes.addressof(self.c)
 
@@ -697,12 +704,12 @@ def kv4_read_rows(layers, first, rows, dst, stream=None):
     """dst [n_layers, 2, n_kv_heads, rows, 128] (bf16) = the values of slots
     first .. first + rows - 1 of every layer's 4-bit cache."""
     layers = _views(layers, KV4Layer)
-    _check(lib().glance_kv4_read_rows(layers.at, layers.n, first, rows, _rows16(dst, layers, rows), _on(stream, layers.dev)))
+    _check(lib().glance_kv4_read_rows(layers.at, layers.n, _i32(first, "first"), rows, _rows16(dst, layers, rows), _on(stream, layers.dev)))
 
 
 def kv4_tree_attention_workspace_bytes(rows, n_q_heads, kvs):
     kvs = _views(kvs, KV4Layer)
-    return lib().glance_kv4_tree_attention_workspace_bytes(kvs.n, rows, n_q_heads, kvs.at)
+    return lib().glance_kv4_tree_attention_workspace_bytes(kvs.n, _i32(rows, "rows"), _i32(n_q_heads, "n_q_heads"), kvs.at)
 
 
 _DECODE = {}
@@ -739,7 +746,7 @@ def kv4_tree_attention(q, kvs, trees, scale, out, ws, stream=None):
 
 
 def kv4_accept_commit_workspace_bytes(B, n_layers):
-    return lib().glance_kv4_accept_commit_workspace_bytes(B, n_layers)
+    return lib().glance_kv4_accept_commit_workspace_bytes(_i32(B, "B"), _i32(n_layers, "n_layers"))
 
 
 def _array(x, dtype, n, dev):
