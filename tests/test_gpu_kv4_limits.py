@@ -9,7 +9,7 @@ import torch
 
 import workloads as W
 from _kv4_tight import tight64
-from _kv4_util import layer_of, random_cache, random_tree, upload_tree
+from _kv4_util import anc_words, layer_of, random_cache, random_tree, upload_tree
 from _util import bf16_tensor
 from oracle import kv4 as okv4
 
@@ -89,3 +89,24 @@ def test_many_small_weights_beside_large_ones_are_kept(dev, clean_status, N, Hq,
     assert torch.all(tol < 0.04 * o.abs())  # of use: the tolerance is far below the output
     err = (out[0].double() - o).abs()
     assert torch.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("N,Hq,Hkv", [(1, 4, 2), (3, 8, 2), (9, 2, 2), (40, 8, 2)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_a_query_row_that_sees_nothing_is_zero_whatever_it_holds(dev, clean_status, N, Hq, Hkv, what):
+    import tree_verified_block_gb300 as g
+    gen = W.rng(97, N)
+    rows = N + 1
+    seen = np.eye(rows, dtype=bool)
+    seen[0] = seen[N] = False
+    t = random_tree(gen, N, 16)
+    t["anc"] = anc_words(seen)
+    layer = layer_of(g, random_cache(gen, Hkv, rows + rows % 2, 1.0, 1.0), torch.zeros(1, dtype=torch.int32, device=dev), dev)
+    q = bf16_tensor(W.normal_bf16(gen, (1, rows, Hq, 128)), dev)
+    q[0, 0, :, 7] = what
+    q[0, N, Hq - 1] = what
+    out = torch.full_like(q, 3.0)
+    g.kv4_tree_attention(q, [layer], [upload_tree(g, t, 16, dev)], 0.09, out,
+                         g.workspace(g.kv4_tree_attention_workspace_bytes(rows, Hq, [layer]), dev))
+    assert torch.all(out[0, 0] == 0) and torch.all(out[0, N] == 0)
+    assert not out.isnan().any()

@@ -300,15 +300,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // The factor that brings a query row whose largest magnitude is `amax` to
 // [2^14, 2^15), so that f16 holds every element down to 2^-31 of it exactly
 // (a bf16 has 8 bits): a power of two, at most 2^100. Its inverse goes into
-// the row's score factor; a row that is not finite gets NaN there.
+// the row's score factor. A row that is not finite gets NaN, which makes all of
+// its scores NaN, and with them every output that sees a slot; the scores of
+// slots that it does not see are masked as any row's.
 __device__ __forceinline__ float query_factor(float amax) {
   int e = 141 - static_cast<int>(__float_as_uint(amax) >> 23);
   e = e > 100 ? 100 : e;
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  return amax < INFINITY ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : __uint_as_float(0x7FC00000u);
 }
-__device__ __forceinline__ float score_factor(float amax, float factor, float scale_log2, float k_global) {
-  // at least the least normal number: a score of -infinity stays one
-  return amax < INFINITY ? fmaxf(scale_log2 * k_global * (1.f / factor), 1.17549435e-38f) : __uint_as_float(0x7FC00000u);
+__device__ __forceinline__ float score_factor(float factor, float scale_log2, float k_global) {
+  // at least the least normal number, for a factor of NaN as well: a score of -infinity stays one
+  return fmaxf(scale_log2 * k_global * (1.f / factor), 1.17549435e-38f);
 }
 
 // Which parts the group of a segment (not a whole group) has: their number and
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
     for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(__uint_as_float(w[i] << 16) * qf, __uint_as_float(w[i] & 0xFFFF0000u) * qf);
     if (has_q) {
       sq[(4 * (q_row >> 3) + (piece & 3)) * 32 + 4 * (q_row & 7) + (piece >> 2)] = make_uint4(h[0], h[1], h[2], h[3]);
-      if (piece == 0) ms->factor[q_row] = score_factor(amax, qf, p.scale_log2, rq.k_global);
+      if (piece == 0) ms->factor[q_row] = score_factor(qf, p.scale_log2, rq.k_global);
     }
   }
   __syncthreads();
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         float mx = fmaxf(fmaxf(s[0][n][h], s[0][n][2 + h]), fmaxf(s[1][n][h], s[1][n][2 + h]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sc[n][h];  // sc > 0, or NaN (then mx is of no account)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sc[n][h];  // sc > 0
         // m moves only when the maximum has grown by 8 (in log2): until then the
         // weights stay below 2^15 and nothing is rescaled
         const bool grow = mx > m[n][h] + kGrow;
