@@ -667,8 +667,9 @@ size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_head
  * a row does not see holds never reaches that row; a slot that it does see
  * and that has a scale that is not a number makes the row NaN, all of it or
  * the elements of that scale's group.
- * n_q_heads / n_kv_heads in {1, 2, 4, 8}; scale finite and > 0; q, out 16-byte
- * aligned and not overlapping, workspace 256-byte aligned. A request with
+ * n_q_heads / n_kv_heads in {1, 2, 4, 8}; scale finite and > 0, and finite in
+ * fp32 times log2 e and each k_global; q, out 16-byte aligned and not
+ * overlapping, workspace 256-byte aligned. A request with
  * T + N + 1 > t_cap sets device status 2 and its out is left as it was.
  * Arithmetic: code * scale is exact; the softmax weights are rounded to f16
  * (2^-11 of each, or 2^-32 of the row's largest weight for those below 2^-21 of

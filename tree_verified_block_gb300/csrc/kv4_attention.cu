@@ -1690,6 +1690,9 @@ extern "C" glance_status glance_kv4_tree_attention(const void* q, int n_q_heads,
   if (G != 1 && G != 2 && G != 4 && G != 8)
     return fail(GLANCE_ERR_UNSUPPORTED, "%s: need n_q_heads / n_kv_heads in {1, 2, 4, 8}", who);
   if (!(scale > 0.f) || !isfinite(scale)) return fail(GLANCE_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+  for (int r = 0; r < B; ++r)  // the kernels' score factor: with infinity a score of 0 would be NaN
+    if (!isfinite(scale * kLog2e * kv[r].k_global))
+      return fail(GLANCE_ERR_INVALID_ARG, "%s: scale * k_global * log2 e must be finite (request %d)", who, r);
   if (!glance::aligned16(q) || !glance::aligned16(out))
     return fail(GLANCE_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", who);
   const size_t n_out = static_cast<size_t>(B) * rows * n_q_heads * kD * 2;
