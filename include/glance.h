@@ -580,7 +580,9 @@ glance_status glance_rope_init(glance_rope* rope, int head_dim, double theta, in
  *          for t_cap and strides, T = *kv[r].t_len; T is not changed).
  * pos: device int32 [n_axes][B M]. q_norm, k_norm: device float [head_dim].
  * All arithmetic is fp32; the angle, position times the frequency in double
- * precision, is reduced to one turn exactly and rounded to 2^-32 of a turn.
+ * precision, is reduced to one turn exactly, cut to 2^-32 of a turn and rounded
+ * to fp32: off by 2^-26 + 2^-32 of a turn at most (near half a turn, less for
+ * small angles).
  * dtype BF16 or F32 (that of kv); head_dim 32, 64 or 128. Arrays
  * 16-byte aligned, strides multiples of 16 bytes; q_out must not overlap qkv.
  * A request with T + M > t_cap sets device status 2 and none of its cache rows
