@@ -569,7 +569,8 @@ glance_status glance_rope_init(glance_rope* rope, int head_dim, double theta, in
  * rows (a prompt's text and image tokens before the first round, or a round's
  * tree rows where the projection was made elsewhere): per-head RMS norm of q
  * and k, rotate-half rotary position, q to q_out, k and v into the caches.
- * For request r of B (1 <= B <= 16) and row i of M (M >= 1), with row r M + i:
+ * For request r of B (1 <= B <= 16) and row i of M (M >= 1, B M <= 2^30), with
+ * row r M + i (1 to 4096 query heads and as many key heads at most):
  *   qkv    [B M] rows of (n_q_heads + 2 n_kv_heads) * head_dim elements (q
  *          heads, k heads, v heads), row_stride elements apart;
  *   y      = x / sqrt(mean x^2 + eps) * w for q heads (w = q_norm) and k heads
@@ -615,7 +616,7 @@ typedef struct {
   void* v_scale;
   float k_global;      /* finite, 2^-60 .. 2^60 */
   float v_global;
-  int32_t n_kv_heads;
+  int32_t n_kv_heads;  /* 1 .. 1024 */
   int32_t head_dim;    /* 128 */
   int32_t t_cap;       /* slots per head that may be used (<= 2^30) */
   int64_t head_stride; /* slots between heads: >= t_cap, even */
@@ -630,13 +631,13 @@ typedef struct {
  * contiguous, 32-byte aligned. Per group of 16 elements x, in fp32:
  * t = x * (1 / global), the reciprocal rounded first; scale = max|t| / 6
  * rounded to e4m3 (nearest even, at most 448); code = t / scale rounded to
- * nearest even, at most 6 (0 where the scale is 0). A group with a t that is not finite gets the scale 0x7F and codes 0.
+ * nearest even, at most 6 (0 where the scale is 0). A group with a t that is
+ * not finite gets the scale 0x7F and codes 0.
  * Each row is quantised by itself, so a row reads the same whether it was
  * written alone, in a prompt or as a tree row.
  * layers: host array of distinct caches with one t_len, geometry and pair of
- * globals. If
- * T + rows > t_cap the call sets device status 2 and writes nothing.
- * Limits: 1 <= n_layers <= 128, rows >= 1.
+ * globals. If T + rows > t_cap the call sets device status 2 and writes nothing.
+ * Limits: 1 <= n_layers <= 128, n_layers * n_kv_heads <= 32767, rows >= 1.
  */
 glance_status glance_kv4_write_rows(const void* src, const glance_kv4* layers, int n_layers,
                                     int rows, void* stream);

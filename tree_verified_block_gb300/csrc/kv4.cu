@@ -232,7 +232,7 @@ glance_status rows_call(const char* who, bool write, void* rows16, const glance_
     return fail(GLANCE_ERR_INVALID_ARG, "%s: slots %d .. %lld end behind t_cap = %d", who, first,
                 static_cast<long long>(first) + rows - 1, l0.t_cap);
   if (n_layers * 2ll * l0.n_kv_heads > 65535)
-    return fail(GLANCE_ERR_UNSUPPORTED, "%s: n_layers * n_kv_heads too large", who);
+    return fail(GLANCE_ERR_UNSUPPORTED, "%s: need n_layers * n_kv_heads <= 32767", who);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_layers <= kSmallLayers) return launch_rows<kSmallLayers>(who, write, rows16, layers, n_layers, rows, first, s);
   return launch_rows<kMaxLayers>(who, write, rows16, layers, n_layers, rows, first, s);
