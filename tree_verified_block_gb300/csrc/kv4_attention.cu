@@ -19,7 +19,7 @@
 // Two kernels, by the query rows that share a kv head (G heads x N + 1 rows):
 // up to 16, the call is bound by the cache's bytes (kv4_attention_few_kernel);
 // beyond, by the products (kv4_attention_wide_kernel, with the tensor core's
-// 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 58.3
+// 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 58.9
 // and 111 us on 131072 slots, 28.0 and 35.9 on 32768, 21.7 and 31.4 for 8
 // requests of 512 to 8192, but 15.2 and 13.0 on 4096; the host that picks the
 // kernel does not know T.
@@ -239,11 +239,15 @@ __device__ __forceinline__ bool next_segment(const Params& p, const Plan& pl, Se
 // through the workspace by the block that finishes last.
 //
 // Measured (32 / 8 heads): one row on 131072 slots 37.1 us (60 % of the copy
-// rate), one row x 16 requests of 512 to 32768 slots 40.5 us (56 %). There it is
-// the warps' issue that bounds it (53 % of the issue slots at 16 warps per SM: a
-// piece is 660 instructions, most of them the codes' conversion), not the memory
-// (46 %); three blocks per SM (85 registers a thread) spill and are slower. One
-// row on 1000 slots takes 8.5 us: 1.2 until the block knows its work, 1.3 until
+// rate), one row x 16 requests of 512 to 32768 slots 40.5 us (56 %). There nothing
+// is full (issue slots 52 %, ALU 50 %, memory 46 %): it is latency, a piece being
+// one dependent chain of 660 instructions per warp (conversion, S, softmax,
+// conversion, O) with four warps per scheduler, which wait for one another's
+// blocks at the ends of the runs too. Three blocks per SM (85 registers a thread)
+// spill and are slower. Sixteen rows on 131072 slots take 58.9 us (issue slots
+// 52 %, memory 34 %): their O and weights do not fit 128 registers a thread, which
+// spills 188 bytes of stores and 244 of loads, and every piece reads Q from shared
+// memory. One row on 1000 slots takes 8.4 us: 1.2 until the block knows its work, 1.3 until
 // q and the first piece are there, 1.2 for that piece, 0.9 to join the block's
 // warps, 1.1 for the ticket and 1.5 to join the parts; much of each step is its
 // instructions' first way to the SM.
@@ -815,13 +819,15 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // A group that one block has whole is written out there; the others' parts are
 // merged by a second kernel.
 //
-// Measured (32 / 8 heads, 64 rows): 131072 slots 115.3 us, 62 % of the tensor
-// rate on the products' operations; 4096 slots 14.9 us; 8 requests of 512 to
-// 8192 slots 38.9 us. A pair of tiles takes 3500 clocks, of which the tensor
-// core works 2048: a slot's chain is S and O's products (1380 with the other
-// slot's in between) and the softmax (2080), the conversion warps need about as
-// long for the pair's K and V, and tensor memory (two S, two O of
-// 128 columns) has no room for a second S per slot that would let them overlap.
+// Measured (32 / 8 heads, 64 rows): 131072 slots 115.3 us, whose useful operations
+// are 62 % of the measured rate of a large bf16 product (the tensor core is active
+// in 51 % of the kernel's clocks); 4096 slots 14.9 us; 8 requests of 512 to 8192
+// slots 39.4 us. In the steady loop a pair of tiles takes 3500 clocks, of which
+// the tensor core is active in 2048: a slot's chain is S and O's products (1380
+// with the other slot's in between) and the softmax (2080), together 3460, the
+// conversion warps need about as long for the pair's K and V, and tensor memory
+// (two S, two O of 128 columns) has no room for a second S per slot that would let
+// them overlap.
 // S in two halves of 64 slots, which has, takes 170 us (twice the products, Q
 // read from shared memory twice as often), weights handed over by halves 136: a
 // hand-over costs more than what it lets overlap. Short calls are start-up: 1.4 us until the block knows its work, 3
