@@ -9,7 +9,7 @@ import torch
 
 import workloads as W
 from _kv4_tight import tight64
-from _kv4_util import anc_words, layer_of, random_cache, random_tree, upload_tree
+from _kv4_util import anc_words, layer_of, random_cache, random_tree, up, upload_tree
 from _util import bf16_tensor
 from oracle import kv4 as okv4
 
@@ -110,3 +110,74 @@ def test_a_query_row_that_sees_nothing_is_zero_whatever_it_holds(dev, clean_stat
                          g.workspace(g.kv4_tree_attention_workspace_bytes(rows, Hq, [layer]), dev))
     assert torch.all(out[0, 0] == 0) and torch.all(out[0, N] == 0)
     assert not out.isnan().any()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,T", [(0, 8, 2, 300), (0, 4, 4, 5000), (3, 8, 2, 300), (9, 2, 2, 3000), (40, 8, 2, 300), (63, 32, 8, 4000),
+                                        (100, 8, 1, 2000)])
+@pytest.mark.parametrize("size", range(20, 68, 2))
+def test_scores_of_any_size_leave_the_largest_one_s_value(dev, clean_status, N, Hq, Hkv, T, size):
+    """Scores of about 2^size (log2), far past the fp32 numbers that are whole:
+    the largest one's V row is the output where no other is near it.
+
+    Near: the fp32 scores are off by 132 steps of 2^-23 of sum |q| |k|, as in
+    tight64, each; twice that, and 40 more for the others' weights."""
+    import tree_verified_block_gb300 as g
+    gen = W.rng(109, N, size)
+    rows = N + 1
+    cache = random_cache(gen, Hkv, T + rows + (T + rows) % 2, 1.0, 1.0)
+    t = random_tree(gen, N, 16, T)
+    layer = layer_of(g, cache, torch.tensor([T], dtype=torch.int32, device=dev), dev)
+    q = bf16_tensor(W.normal_bf16(gen, (1, rows, Hq, 128)), dev)
+    scale = 2.0 ** size / 40
+    out = torch.zeros_like(q)
+    g.kv4_tree_attention(q, [layer], [upload_tree(g, t, 16, dev)], scale, out,
+                         g.workspace(g.kv4_tree_attention_workspace_bytes(rows, Hq, [layer]), dev))
+    n, G = T + rows, Hq // Hkv
+    k = up(okv4.values(cache[0][:, :n], cache[1][:, :n], 1.0), dev)
+    v = up(okv4.values(cache[2][:, :n], cache[3][:, :n], 1.0), dev)
+    vis = torch.cat((torch.ones(rows, T, dtype=torch.bool), torch.from_numpy(t["seen"])), 1).to(dev)
+    clear = 0
+    for h in range(Hq):
+        x = q[0, :, h].double()
+        s = (x @ k[h // G].t()).masked_fill(~vis, -torch.inf)
+        top, at = s.topk(2, -1)
+        off = (x.abs() @ k[h // G].abs().t()).amax(-1) * 132 * 2 ** -23
+        one = top[:, 0] - top[:, 1] > 2 * off + 40 / scale
+        o = v[h // G][at[:, 0]]
+        assert not out[0, :, h].isnan().any()
+        assert torch.all(((out[0, :, h].double() - o).abs() <= (2 ** -8 + 2 ** -10) * o.abs() + 2 ** -25)[one])
+        clear += int(one.sum())
+    assert clear >= rows * Hq // 2
+
+
+@pytest.mark.parametrize("N,Hq,Hkv", [(0, 1, 1), (9, 1, 1), (40, 1, 1), (255, 1, 1)])
+@pytest.mark.parametrize("run", [64, 256])
+def test_climbing_scores_of_any_size_give_a_mean_of_the_values(dev, clean_status, N, Hq, Hkv, run):
+    """Scores that climb by up to 8 (log2) every 64 slots or every 256, the most
+    for which sums need not be rescaled, on top of 2^20 to 2^30: whatever fp32
+    makes of them, the output is a mean of V rows, which are 1 to 6 here."""
+    import tree_verified_block_gb300 as g
+    gen = W.rng(113, N)
+    rows, T = N + 1, 64 * run
+    n = T + rows + (T + rows) % 2
+    k = np.zeros((Hkv, n, 128), np.uint8)
+    k[..., 0] = 7
+    step = np.minimum(np.arange(n) // run, 63)
+    for bit in range(6):
+        k[..., 16 + bit] = 2 * (step >> bit & 1)  # 1 or 0
+    ks = np.full((Hkv, n, 8), 0x38, np.uint8)
+    ks[..., 0] = 0x7E  # 6 * 448
+    v = gen.integers(2, 8, (Hkv, n, 128), dtype=np.uint8)
+    cache = [okv4.pack(k), ks, okv4.pack(v), np.full((Hkv, n, 8), 0x38, np.uint8)]
+    t = random_tree(gen, N, 16, T)
+    layer, tree = layer_of(g, cache, torch.tensor([T], dtype=torch.int32, device=dev), dev), upload_tree(g, t, 16, dev)
+    ws = g.workspace(g.kv4_tree_attention_workspace_bytes(rows, Hq, [layer]), dev)
+    out = torch.zeros(1, rows, Hq, 128, dtype=torch.bfloat16, device=dev)
+    for base in np.arange(20, 31, 0.25):
+        for climb in (7.5, 7.875, 7.9375, 8.0):
+            for sign in (1, -1):
+                q = torch.zeros_like(out)
+                q[..., 0] = sign * 2.0 ** base / 2688
+                q[..., 16:22] = torch.tensor([climb * 2.0 ** b for b in range(6)], dtype=torch.bfloat16)
+                g.kv4_tree_attention(q, layer, tree, math.log(2), out, ws)
+                assert torch.all((out >= 1) & (out <= 6)), (base, climb, sign)

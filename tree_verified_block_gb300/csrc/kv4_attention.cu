@@ -23,6 +23,8 @@
 // and 111 us on 131072 slots, 28.0 and 35.9 on 32768, 21.7 and 31.4 for 8
 // requests of 512 to 8192, but 15.2 and 13.0 on 4096; the host that picks the
 // kernel does not know T.
+#include <type_traits>
+
 #include "kv4_internal.cuh"
 
 GLANCE_DEFINE_STATUS_WORD(status_kv4_attention)
@@ -37,6 +39,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The m of a row is kept this much (log2) under its running maximum, and moves
 // when the maximum has grown by 8: weights are at most 2^15.
 constexpr float kUnder = 7.f, kGrow = kUnder + 8.f;
+// A weight's exponent is one fused multiply-add, score * factor - m, and m comes
+// from rounded products: apart by up to half a step of a product, and a weight
+// could be 2^(that) larger. Where m is set below kFused the products that count
+// are below 2^24, the half step is 1/2 at most, and 2^15.5 is still an f16. From
+// kFused on the product is rounded first, in loops of their own (with the choice
+// inside, the usual ones take 2 to 4 % longer).
+constexpr float kFused = 0x1p23f;
 
 struct Request {
   const unsigned char* k;
@@ -487,6 +496,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
   // four slots of a lane's V fragment are then 4 apart and the four lanes' next
   // to each other, which loads without bank conflicts
   const int k_slot = 4 * (r & 1) + (r >> 1);
+  const auto take_pieces = [&](auto rounded) {
+  constexpr bool kRounded = decltype(rounded)::value;
   for (int u = u0 + warp; u < u1 && !dead; u += kFewWarps) {
     unsigned char* st = my_ring + stage * kUnitBytes;
     if (!__all_sync(0xffffffffu, mbar_wait(&ms->full[warp][stage], parity))) {
@@ -572,10 +583,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         float mx = fmaxf(fmaxf(s[0][n][h], s[0][n][2 + h]), fmaxf(s[1][n][h], s[1][n][2 + h]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * sc[n][h];  // sc > 0
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        mx = __fmul_rn(mx, sc[n][h]);  // sc > 0; not fused with what follows: the rounded products' own maximum
         // m moves only when the maximum has grown by 8 (in log2): until then the
         // weights stay below 2^15 and nothing is rescaled
-        const bool grow = mx > m[n][h] + kGrow;
+        const bool grow = mx > __fadd_rd(m[n][h], kGrow);
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = grow ? mx - kUnder : m[n][h];
           const float alpha = m[n][h] == -INFINITY ? 0.f : ex2_approx(m[n][h] - mn);
@@ -592,7 +604,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            w[h][kt][b] = ex2_approx(fmaf(s[kt][n][2 * b + h], sc[n][h], -off));
+            const float x = s[kt][n][2 * b + h];
+            w[h][kt][b] = ex2_approx(kRounded ? __fadd_rn(__fmul_rn(x, sc[n][h]), -off) : fmaf(x, sc[n][h], -off));
             l[n][h] += w[h][kt][b];
           }
       }
@@ -644,6 +657,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv4_attention_few_kernel(const
       parity ^= 1;
     }
   }
+  };
+  // scores are at most 128 * 2^15 * 2688 < 2^33.4 times the row's factor: below 2^24
+  bool below = true;
+#pragma unroll
+  for (int n = 0; n < kN; ++n) below = below && fmaxf(sc[n][0], sc[n][1]) < kFused * 0x1p-33f;
+  if (__all_sync(0xffffffffu, below))
+    take_pieces(std::false_type());
+  else
+    take_pieces(std::true_type());
   const auto warp_o = [&](int w) { return reinterpret_cast<float4*>(ring + w * kWarpRing); };
   const auto warp_m = [&](int w) { return reinterpret_cast<float*>(ring + w * kWarpRing + kWarpO); };
   // the block's rows: maxima first, then every warp's O relative to them
@@ -1303,7 +1325,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
         ahead = false;
         float m = -INFINITY, l = 0.f;
         const int step = pair ? 1 : 2, j0 = pair ? 0 : x;
-        for (int j = j0; j < run.tiles; j += step) {
+        // The segment's tiles from j on, the first one from its half `from` on where
+        // that is not -1. Without rounded products: returns at the half whose maximum
+        // is the first beyond kFused; else -1.
+        const auto softmax_tiles = [&](auto rounded, int& j, int from) -> int {
+        constexpr bool kRounded = decltype(rounded)::value;
+        for (; j < run.tiles; j += step) {
           const int key0 = run.key0(j);
           const int nc = run.cols(j) / 32;
           const bool tree = run.tree(j, T);
@@ -1330,8 +1357,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
               bad[i] = __ballot_sync(0xffffffffu, nan != 0u);
             }
           }
+          if (!kRounded || from < 0) {
           ok = wide_wait(&ms->s_full[x], n_s++ & 1, ms);
-          if (!ok) break;
+          if (!ok) return -1;
           tc_fence_after();
           if (tree) {
             // masked in place, so that the rest is the same for every tile
@@ -1352,9 +1380,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
             }
             tmem_st_wait();
           }
+          }
           // 64 slots at a time: a whole row would not fit the registers
 #pragma unroll 1
-          for (int h = 0; 2 * h < nc; ++h) {
+          for (int h = kRounded ? max(from, 0) : 0; 2 * h < nc; ++h) {
             uint32_t sr[64];
             tmem_row64(tS + 64 * h, sr);
             const bool both = 2 * h + 1 < nc;  // the product has the second 32 slots
@@ -1370,10 +1399,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
                 mx[i] = max3f(mx[i], __uint_as_float(sr[48 + i]), __uint_as_float(sr[56 + i]));
               }
             }
-            const float mt = fmaxf(max3f(mx[0], mx[1], mx[2]), max3f(max3f(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sc;
+            const float top = fmaxf(max3f(mx[0], mx[1], mx[2]), max3f(max3f(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+            const float mt = __fmul_rn(top, sc);  // not fused with what follows: the rounded products' own maximum
             // m moves when some row of the warp grew by 8 (log2): a stale one keeps
             // the weights below 2^15 and cancels between O and l
-            if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+            if (__any_sync(0xffffffffu, mt > __fadd_rd(m, kGrow))) {
+              if (!kRounded && __any_sync(0xffffffffu, fabsf(mt) >= kFused && mt > -INFINITY)) return h;
               const float mn = fmaxf(m, mt - kUnder);
               const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - mn);
               m = mn;
@@ -1414,7 +1445,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   float u0, u1;
-                  split_f2(fma_f2(pair_f2(__uint_as_float(sr[32 * c + 2 * e]), __uint_as_float(sr[32 * c + 2 * e + 1])), sc2, no2),
+                  const float s0 = __uint_as_float(sr[32 * c + 2 * e]), s1 = __uint_as_float(sr[32 * c + 2 * e + 1]);
+                  split_f2(kRounded ? add_f2(pair_f2(__fmul_rn(s0, sc), __fmul_rn(s1, sc)), no2) : fma_f2(pair_f2(s0, s1), sc2, no2),
                            u0, u1);
                   const float p0 = ex2_approx(u0), p1 = ex2_approx(u1);
                   if (e & 1)
@@ -1433,7 +1465,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv4_attention_wide_kernel(con
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms->p_ready[x]);
+          if (kRounded) from = -1;
         }
+        return -1;
+        };
+        int j = j0;
+        const int from = softmax_tiles(std::false_type(), j, -1);
+        if (from >= 0) (void)softmax_tiles(std::true_type(), j, from);
         if (!ok && pair) break;
         // a row that sees a prefix slot has a weight of 2^7 or more unless all its
         // scores are -infinity: then it is no number

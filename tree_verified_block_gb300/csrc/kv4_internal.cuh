@@ -146,7 +146,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Two fp32 values in one register pair, each operation as on one.
+// Two fp32 values in one register pair, each operation as on one; but a mul_f2
+// whose only use is an add_f2 becomes one fused operation (seen with nvcc 13.0):
+// where the product's rounding counts, __fmul_rn on each half.
 __device__ __forceinline__ unsigned long long pair_f2(float lo, float hi) {
   unsigned long long v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
