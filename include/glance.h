@@ -678,12 +678,13 @@ size_t glance_kv4_tree_attention_workspace_bytes(int B, int n_rows, int n_q_head
  * (2^-11 of each, or 2^-32 of the row's largest weight for those below 2^-21 of
  * it), sums and maxima are fp32, out is rounded to bf16 once. With
  * n_q_heads / n_kv_heads * (N + 1) <= 16 q is used to 2^-31 of its row's largest
- * element (smaller ones lose bits), beyond that as it is, and partial results
+ * element or to 2^-117, whichever is more (smaller ones lose bits), beyond that
+ * as it is, and partial results
  * of a row that several blocks share are rounded to f16 between them (2^-11 of
  * an element, at least 2^-25 in units of code * scale). The results do not
  * change from call to call. A q row with an infinity or NaN that sees a slot of
- * the prefix gives NaN. One workspace, of the largest size among them, serves calls of
- * any shape in turn.
+ * the prefix gives NaN. Finite scores of any size give a mean of the V rows. One
+ * workspace, of the largest size among them, serves calls of any shape in turn.
  */
 glance_status glance_kv4_tree_attention(const void* q, int n_q_heads, const glance_kv4* kv,
                                         const glance_tree* trees, int B, float scale, void* out,

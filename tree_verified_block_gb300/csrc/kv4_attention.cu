@@ -19,9 +19,9 @@
 // Two kernels, by the query rows that share a kv head (G heads x N + 1 rows):
 // up to 16, the call is bound by the cache's bytes (kv4_attention_few_kernel);
 // beyond, by the products (kv4_attention_wide_kernel, with the tensor core's
-// 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 58.9
-// and 111 us on 131072 slots, 28.0 and 35.9 on 32768, 21.7 and 31.4 for 8
-// requests of 512 to 8192, but 15.2 and 13.0 on 4096; the host that picks the
+// 128-row tiles). At 16 rows, 32 / 8 heads, the first and the second take 56.7
+// and 111 us on 131072 slots, 27.6 and 35.9 on 32768, 21.5 and 31.4 for 8
+// requests of 512 to 8192, but 14.9 and 13.0 on 4096; the host that picks the
 // kernel does not know T.
 #include <type_traits>
 
@@ -247,15 +247,15 @@ __device__ __forceinline__ bool next_segment(const Params& p, const Plan& pl, Se
 // The warps of a block are merged through shared memory, the blocks of a head
 // through the workspace by the block that finishes last.
 //
-// Measured (32 / 8 heads): one row on 131072 slots 37.1 us (60 % of the copy
-// rate), one row x 16 requests of 512 to 32768 slots 40.5 us (56 %). There nothing
-// is full (issue slots 52 %, ALU 50 %, memory 46 %): it is latency, a piece being
+// Measured (32 / 8 heads): one row on 131072 slots 36.7 us (61 % of the copy
+// rate), one row x 16 requests of 512 to 32768 slots 40.4 us (57 %). There nothing
+// is full (issue slots 52 %, ALU 49 %, memory 45 %): it is latency, a piece being
 // one dependent chain of 660 instructions per warp (conversion, S, softmax,
 // conversion, O) with four warps per scheduler, which wait for one another's
 // blocks at the ends of the runs too. Three blocks per SM (85 registers a thread)
-// spill and are slower. Sixteen rows on 131072 slots take 58.9 us (issue slots
-// 52 %, memory 34 %): their O and weights do not fit 128 registers a thread, which
-// spills 188 bytes of stores and 244 of loads, and every piece reads Q from shared
+// spill and are slower. Sixteen rows on 131072 slots take 56.7 us (issue slots
+// 53 %, memory 34 %): their O and weights do not fit 128 registers a thread, which
+// spills (280 bytes of stores and of loads in the code of both loops), and every piece reads Q from shared
 // memory. One row on 1000 slots takes 8.4 us: 1.2 until the block knows its work, 1.3 until
 // q and the first piece are there, 1.2 for that piece, 0.9 to join the block's
 // warps, 1.1 for the ticket and 1.5 to join the parts; much of each step is its
@@ -841,10 +841,10 @@ constexpr size_t kCounterBytes = static_cast<size_t>(kMaxB) * glance::kKv4MaxHea
 // A group that one block has whole is written out there; the others' parts are
 // merged by a second kernel.
 //
-// Measured (32 / 8 heads, 64 rows): 131072 slots 115.3 us, whose useful operations
+// Measured (32 / 8 heads, 64 rows): 131072 slots 116.3 us, whose useful operations
 // are 62 % of the measured rate of a large bf16 product (the tensor core is active
-// in 51 % of the kernel's clocks); 4096 slots 14.9 us; 8 requests of 512 to 8192
-// slots 39.4 us. In the steady loop a pair of tiles takes 3500 clocks, of which
+// in 51 % of the kernel's clocks); 4096 slots 15.0 us; 8 requests of 512 to 8192
+// slots 39.3 us. In the steady loop a pair of tiles takes 3500 clocks, of which
 // the tensor core is active in 2048: a slot's chain is S and O's products (1380
 // with the other slot's in between) and the softmax (2080), together 3460, the
 // conversion warps need about as long for the pair's K and V, and tensor memory
