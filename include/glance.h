@@ -709,6 +709,88 @@ glance_status glance_kv4_accept_commit(const glance_tree* trees, int B, const in
                                        int32_t* new_root, int32_t* gated, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------------------- 8-bit rows */
+
+/*
+ * The target's dense layers in 8 bits, beside the bf16 ones above: rows of the
+ * residual stream normalised and quantised in one pass, and products of such
+ * rows with 8-bit weights.
+ *
+ * An 8-bit row is d codes of one byte, e4m3 (sign, four exponent bits, three
+ * fraction bits; magnitudes up to 448), and one fp32 scale; an element stands
+ * for code * scale. The calls below write scales that are powers of two, the
+ * least with which no element of the row exceeds 448 (at least 2^-126; 1 for a
+ * row of zeros), so that code * scale is exact in bf16 and fp32. Codes are the
+ * element times 2^-e rounded to nearest even. A row that has an element that
+ * is not finite gets the scale NaN and codes 0.
+ * Limits of the three calls: 1 <= M <= 2^24, d a multiple of 16 up to 32768
+ * (BF16) or 16384 (F32); arrays 16-byte aligned (scales 4-byte), strides (in
+ * elements) multiples of 16 bytes that cover a row.
+ */
+
+/*
+ * codes, scales <- rows of x (an activation before its projection, or weights
+ * once, as [out][in]). dtype: that of x, BF16 or F32.
+ */
+glance_status glance_q8_rows(const void* x, int64_t x_stride, glance_dtype dtype, int M, int d,
+                             void* codes, int64_t code_stride, float* scales, void* stream);
+
+/*
+ * The residual's addition, the RMS norm and the quantisation, in one pass over
+ * the rows: s = x + residual rounded to dtype (nullable residual: s = x),
+ * stored to total (nullable; it may be x or residual itself, with its stride),
+ * and the 8-bit form of s / sqrt(mean s^2 + eps) * weight (device float [d],
+ * 16-byte aligned; null: ones). All arithmetic is fp32; eps finite and >= 0.
+ * No other output may overlap an input.
+ */
+glance_status glance_q8_norm_rows(const void* x, int64_t x_stride, const void* residual,
+                                  int64_t residual_stride, glance_dtype dtype, int M, int d,
+                                  const float* weight, float eps, void* total, int64_t total_stride,
+                                  void* codes, int64_t code_stride, float* scales, void* stream);
+
+/* out [M][d] (dtype BF16 or F32) = code * scale in fp32, rounded once to dtype. */
+glance_status glance_q8_read_rows(const void* codes, int64_t code_stride, const float* scales,
+                                  glance_dtype dtype, int M, int d, void* out, int64_t out_stride,
+                                  void* stream);
+
+typedef enum {
+  GLANCE_ACT_NONE = 0,
+  GLANCE_ACT_SILU = 1,     /* v / (1 + e^-v) */
+  GLANCE_ACT_GELU = 2,     /* v (1 + erf(v / sqrt 2)) / 2 */
+  GLANCE_ACT_GELU_TANH = 3 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+} glance_act;
+
+/*
+ * Product of 8-bit rows with 8-bit weights, with the epilogue of a projection:
+ *   v[m][n]   = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n]
+ *   out[m][n] = act(v[m][n]) + residual[m][n]                    (gated 0)
+ *   out[m][j] = act(v[m][j]) * v[m][N + j] + residual[m][j]      (gated 1)
+ * x: e4m3 [M][K], rows x_stride bytes apart; w: e4m3 [N][K], rows w_stride
+ * bytes apart (gated: [2 N][K], the N gate rows, then the N up rows); x_scale
+ * float [M]; w_scale and bias (nullable) float [N] (gated: [2 N]); any scales,
+ * those of the row calls or a checkpoint's. residual (nullable) and out: [M][N]
+ * of out_dtype, strides in elements; out may be the residual itself (with its
+ * stride) and must overlap no other input.
+ * The products are exact and summed in fp32, the epilogue is fp32, out is
+ * rounded once. The results do not change from call to call, nor with the other
+ * rows of the call for as long as M stays in one of the ranges 1 to 16, 17 to
+ * 32, 33 to 64, 65 to 128 and so on of the kernels (the order of the sums does).
+ * A row of x (a weight row) with a code that is not a number or such a scale
+ * makes NaN of that row (column) of out alone.
+ * Limits: 1 <= M <= 2^24, N a multiple of 8 up to 2^22, K a multiple of 16 up
+ * to 2^20; x, w, residual and out 16-byte aligned with strides that are
+ * multiples of 16 bytes, scales and bias 4-byte aligned.
+ * The call is a programmatic dependent of the previous kernel in the stream: it
+ * may read w (nothing else) before that kernel has finished, when that kernel
+ * lets dependents start early (this library's attention and dense calls do; the
+ * row calls above do not, so they may write w).
+ */
+glance_status glance_q8_linear(const void* x, int64_t x_stride, const float* x_scale, int M,
+                               const void* w, int64_t w_stride, const float* w_scale, int N, int K,
+                               int gated, glance_act act, const float* bias, const void* residual,
+                               int64_t residual_stride, void* out, int64_t out_stride,
+                               glance_dtype out_dtype, void* stream);
+
 /* ------------------------------------------------------------------ status */
 
 /* Text of the last host-side error on this thread ("" if none). */

@@ -38,6 +38,7 @@ EXPORTS = [
     "glance_kv4_write_rows", "glance_kv4_read_rows",
     "glance_kv4_tree_attention_workspace_bytes", "glance_kv4_tree_attention",
     "glance_kv4_accept_commit_workspace_bytes", "glance_kv4_accept_commit",
+    "glance_q8_rows", "glance_q8_norm_rows", "glance_q8_read_rows", "glance_q8_linear",
     "glance_last_error", "glance_status_string", "glance_device_status",
     "glance_reset_device_status", "glance_get_status", "glance_kv_write_rows", "glance_clear_status", "glance_version",
 ]
@@ -176,6 +177,15 @@ def lib():
     L.glance_kv4_accept_commit_workspace_bytes.restype = sz
     L.glance_kv4_accept_commit.argtypes = [vp, i32, vp, vp, ctypes.c_float, vp, i32, vp, vp, vp, vp, vp, sz, vp]
     L.glance_kv4_accept_commit.restype = st
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.glance_q8_rows.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp]
+    L.glance_q8_rows.restype = st
+    L.glance_q8_norm_rows.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, f32, vp, i64, vp, i64, vp, vp]
+    L.glance_q8_norm_rows.restype = st
+    L.glance_q8_read_rows.argtypes = [vp, i64, vp, i32, i32, i32, vp, i64, vp]
+    L.glance_q8_read_rows.restype = st
+    L.glance_q8_linear.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i32, i32, i32, vp, vp, i64, vp, i64, i32, vp]
+    L.glance_q8_linear.restype = st
     L.glance_last_error.argtypes = []
     L.glance_last_error.restype = ctypes.c_char_p
     L.glance_status_string.argtypes = [st]
@@ -775,6 +785,79 @@ def kv4_accept_commit(trees, argmax, layers, n_accepted, accepted_tok, new_root,
                                           _array(new_root, _I32, B, dev),
                                           None if gated is None else _array(gated, _I32, B, dev), _workspace(ws, dev), ws.nbytes,
                                           _on(stream, dev)))
+
+
+# ------------------------------------------------------------- 8-bit rows
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _matrix(x, dtypes, what, dev, shape=None):
+    """(address, elements between rows) of a matrix whose rows lie in one piece each."""
+    if x.dtype not in dtypes or x.dim() != 2 or x.stride(1) != 1 and x.shape[1] > 1 or shape is not None and x.shape != shape:
+        raise ValueError(f"glance: {what}")
+    if x.get_device() != dev:
+        raise _elsewhere()
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _floats(x, n, what, dev):
+    if x.dtype is not _F32T or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"glance: {what}")
+    if x.get_device() != dev:
+        raise _elsewhere()
+    return x.data_ptr()
+
+
+_CODES_TEXT = "codes must be uint8 or float8_e4m3fn of the rows' shape"
+_SCALES_TEXT = "scales must be contiguous float32, one per row"
+_ROWS_TEXT = "x, residual and total must be float32 or bfloat16 [M, d], all of one type"
+
+
+def q8_rows(x, codes, scales, stream=None):
+    """codes (uint8 or float8_e4m3fn [M, d]), scales (float32 [M]) <- rows of x [M, d]: e4m3 with a power-of-two scale per row."""
+    dev, (M, d) = x.get_device(), x.shape
+    (xp, xs), (cp, cs) = _matrix(x, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, x.shape)
+    _check(lib().glance_q8_rows(xp, xs, _DTYPES[x.dtype], M, d, cp, cs, _floats(scales, M, _SCALES_TEXT, dev), _on(stream, dev)))
+
+
+def q8_norm_rows(x, residual, weight, eps, total, codes, scales, stream=None):
+    """total <- x + residual (either None; total may be x or residual), codes and scales <- its RMS-normed rows times weight
+    (float32 [d] or None), in e4m3 with a power-of-two scale per row."""
+    dev, (M, d) = x.get_device(), x.shape
+    one = (x.dtype,)
+    (xp, xs), (cp, cs) = _matrix(x, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, x.shape)
+    rp, rs = (None, 0) if residual is None else _matrix(residual, one, _ROWS_TEXT, dev, x.shape)
+    tp, ts = (None, 0) if total is None else _matrix(total, one, _ROWS_TEXT, dev, x.shape)
+    wp = None if weight is None else _floats(weight, d, "weight must be contiguous float32 [d]", dev)
+    _check(lib().glance_q8_norm_rows(xp, xs, rp, rs, _DTYPES[x.dtype], M, d, wp, eps, tp, ts, cp, cs,
+                                     _floats(scales, M, _SCALES_TEXT, dev), _on(stream, dev)))
+
+
+def q8_read_rows(codes, scales, out, stream=None):
+    """out [M, d] (float32 or bfloat16) = code * scale."""
+    dev, (M, d) = out.get_device(), out.shape
+    (op, os_), (cp, cs) = _matrix(out, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, out.shape)
+    _check(lib().glance_q8_read_rows(cp, cs, _floats(scales, M, _SCALES_TEXT, dev), _DTYPES[out.dtype], M, d, op, os_,
+                                     _on(stream, dev)))
+
+
+def q8_linear(x, x_scale, w, w_scale, out, bias=None, act="none", gated=False, residual=None, stream=None):
+    """out [M, N] (float32 or bfloat16) = act(x_scale x . w w_scale + bias) + residual: x [M, K] and w [N, K] codes of the row
+    calls (or any e4m3), w_scale and bias float32 [N]. gated: w [2 N, K], gate rows then up rows, out = act(gate) * up."""
+    dev, (M, N), K = out.get_device(), out.shape, x.shape[1]
+    rows = 2 * N if gated else N
+    if act not in ACTS:
+        raise ValueError("glance: act must be one of " + ", ".join(ACTS))
+    (op, os_), (xp, xs) = _matrix(out, _DTYPES, "out must be float32 or bfloat16 [M, N]", dev), _matrix(
+        x, _CODES, "x must be uint8 or float8_e4m3fn [M, K]", dev, (M, K))
+    wp, wst = _matrix(w, _CODES, "w must be uint8 or float8_e4m3fn [N, K] (gated: [2 N, K])", dev, (rows, K))
+    rp, rs = (None, 0) if residual is None else _matrix(residual, (out.dtype,), "residual must be of out's shape and type", dev, out.shape)
+    _check(lib().glance_q8_linear(xp, xs, _floats(x_scale, M, "x_scale must be contiguous float32 [M]", dev), M, wp, wst,
+                                  _floats(w_scale, rows, "w_scale must be contiguous float32, one per row of w", dev), N, K, bool(gated),
+                                  ACTS[act], None if bias is None else _floats(bias, rows, "bias must be contiguous float32, one per row of w", dev),
+                                  rp, rs, op, os_, _DTYPES[out.dtype], _on(stream, dev)))
 
 
 def device_status():
