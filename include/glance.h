@@ -91,6 +91,7 @@ typedef enum { GLANCE_F32 = 0, GLANCE_BF16 = 1 } glance_dtype;
 #define GLANCE_DEV_PIPELINE_TIMEOUT 4 /* a pipeline wait ran out of time (2 s) */
 #define GLANCE_DEV_OUT_OF_BOUNDS 5    /* bounds-checked build (GLANCE_CHECK) only: a computed
                                         index fell outside its buffer; the access was skipped */
+#define GLANCE_DEV_BAD_SAMPLING 6     /* a row's sampling parameters are out of range */
 
 /* A packed candidate tree: device arrays with N + 1 rows, caller-allocated. */
 typedef struct {
@@ -790,6 +791,43 @@ glance_status glance_q8_linear(const void* x, int64_t x_stride, const float* x_s
                                int gated, glance_act act, const float* bias, const void* residual,
                                int64_t residual_stride, void* out, int64_t out_stride,
                                glance_dtype out_dtype, void* stream);
+
+/* -------------------------------------------------------- sampled verify */
+
+/*
+ * A token from each row of logits (Section 5.4: under sampling the committed
+ * token is a draw from the target's own verified row, so the walk runs unchanged
+ * on these tokens), with temperature, top-k, min-p and top-p of the row.
+ * logits: [M][V] of dtype, rows row_stride elements apart; -infinity is a token
+ * that is not allowed. For a row with r = 1 / temperature (fp32) and weights
+ * w_v = exp((l_v - max l) r), in the order of logits descending, ids ascending:
+ *   keep the first top_k tokens (top_k <= 0 or >= V: all),
+ *   of these the ones with w_v >= min_p (<= 0: all; the first always stays),
+ *   of these the shortest prefix whose weights reach top_p of their sum (>= 1:
+ *   all; the first always stays);
+ * token = argmax l_v r + g_v over what is kept (lowest id among equals), g_v the
+ * noise of glance_lmhead_sample: keyed by (seed, position[row], seq[row]) and v,
+ * so that the same seed gives a position the same draw in whatever round it is
+ * verified, and with nothing cut off the token is glance_lmhead_sample's.
+ * temperature 0: the row's argmax (lowest id among equals); nothing else applies.
+ * gap (nullable): best minus second best of what was compared (infinity if one
+ * token was left).
+ * temperature, top_k, top_p, min_p: device arrays [M], each nullable (1; off).
+ * position: device int32 [M], required, the absolute position of the token that
+ * the row predicts; seq: device int32 [M], nullable (0).
+ * While a token is cut off by top_k or top_p, tokens of weight below e^-32 do
+ * not count: together they weigh less than 4e-9 of the sum.
+ * A row with a NaN, +infinity or nothing but -infinity sets device status 1; a
+ * row whose temperature is negative, not finite or without a finite reciprocal
+ * > 0, or whose top_p or min_p is NaN, device status 6; such a row gets token -1
+ * and gap NaN, the other rows their results.
+ * F32 or BF16, any alignment of the type; 2 <= V <= 262144, 1 <= M <= 2^20.
+ * One launch without a workspace; the results do not change from call to call.
+ */
+glance_status glance_sample(const void* logits, int64_t row_stride, glance_dtype dtype, int M, int V,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, uint64_t seed, const int32_t* position,
+                            const int32_t* seq, int32_t* tokens, float* gap, void* stream);
 
 /* ------------------------------------------------------------------ status */
 

@@ -32,7 +32,7 @@ from ._binding import (STATUS_WORDS, BF16, EXPORTS, F32, LIB_PATH, GlanceError, 
                        tree_attention_workspace_bytes, version, workspace,
                        KV4Layer, Rope, Views, kv4_accept_commit, kv4_accept_commit_workspace_bytes, kv4_read_rows,
                        kv4_tree_attention, kv4_tree_attention_workspace_bytes, kv4_write_rows, qk_norm_rope,
-                       q8_linear, q8_norm_rows, q8_read_rows, q8_rows)
+                       q8_linear, q8_norm_rows, q8_read_rows, q8_rows, sample)
 
 __all__ = ["STATUS_WORDS", "BF16", "EXPORTS", "F32", "LIB_PATH", "GlanceError", "KVLayer", "Tree",
            "accept_commit", "accept_commit_batched", "accept_commit_batched_workspace_bytes",
@@ -48,4 +48,4 @@ __all__ = ["STATUS_WORDS", "BF16", "EXPORTS", "F32", "LIB_PATH", "GlanceError", 
            "tree_attention_batched_workspace_bytes", "tree_attention_workspace_bytes", "version",
            "workspace", "KV4Layer", "Rope", "Views", "kv4_accept_commit", "kv4_accept_commit_workspace_bytes",
            "kv4_read_rows", "kv4_tree_attention", "kv4_tree_attention_workspace_bytes", "kv4_write_rows", "qk_norm_rope",
-           "q8_linear", "q8_norm_rows", "q8_read_rows", "q8_rows"]
+           "q8_linear", "q8_norm_rows", "q8_read_rows", "q8_rows", "sample"]

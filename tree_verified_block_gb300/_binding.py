@@ -17,7 +17,8 @@ STATUS = {0: "GLANCE_OK", 1: "GLANCE_ERR_INVALID_ARG", 2: "GLANCE_ERR_UNSUPPORTE
           3: "GLANCE_ERR_CAPACITY", 4: "GLANCE_ERR_CUDA", 5: "GLANCE_ERR_DEVICE"}
 DEV_STATUS = {0: "ok", 1: "non-finite draft logits", 2: "tree does not fit the cache",
               3: "inconsistent tree", 4: "pipeline wait timed out",
-              5: "index out of bounds (bounds-checked build)"}
+              5: "index out of bounds (bounds-checked build)",
+              6: "sampling parameters out of range"}
 
 EXPORTS = [
     "glance_build_tree_workspace_bytes", "glance_build_tree",
@@ -38,7 +39,7 @@ EXPORTS = [
     "glance_kv4_write_rows", "glance_kv4_read_rows",
     "glance_kv4_tree_attention_workspace_bytes", "glance_kv4_tree_attention",
     "glance_kv4_accept_commit_workspace_bytes", "glance_kv4_accept_commit",
-    "glance_q8_rows", "glance_q8_norm_rows", "glance_q8_read_rows", "glance_q8_linear",
+    "glance_q8_rows", "glance_q8_norm_rows", "glance_q8_read_rows", "glance_q8_linear", "glance_sample",
     "glance_last_error", "glance_status_string", "glance_device_status",
     "glance_reset_device_status", "glance_get_status", "glance_kv_write_rows", "glance_clear_status", "glance_version",
 ]
@@ -186,6 +187,8 @@ def lib():
     L.glance_q8_read_rows.restype = st
     L.glance_q8_linear.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i32, i32, i32, vp, vp, i64, vp, i64, i32, vp]
     L.glance_q8_linear.restype = st
+    L.glance_sample.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, vp, ctypes.c_uint64, vp, vp, vp, vp, vp]
+    L.glance_sample.restype = st
     L.glance_last_error.argtypes = []
     L.glance_last_error.restype = ctypes.c_char_p
     L.glance_status_string.argtypes = [st]
@@ -858,6 +861,30 @@ def q8_linear(x, x_scale, w, w_scale, out, bias=None, act="none", gated=False, r
                                   _floats(w_scale, rows, "w_scale must be contiguous float32, one per row of w", dev), N, K, bool(gated),
                                   ACTS[act], None if bias is None else _floats(bias, rows, "bias must be contiguous float32, one per row of w", dev),
                                   rp, rs, op, os_, _DTYPES[out.dtype], _on(stream, dev)))
+
+
+def _per_row(x, dtype, M, dev):
+    if x is None:
+        return None
+    if x.dtype is not dtype or x.numel() != M or not x.is_contiguous():
+        raise ValueError("glance: temperature, top_p, min_p and gap must be contiguous float32, top_k, position, seq and tokens "
+                         "contiguous int32, one per row of logits")
+    if x.get_device() != dev:
+        raise _elsewhere()
+    return x.data_ptr()
+
+
+def sample(logits, temperature, top_k, top_p, min_p, seed, position, seq, tokens, gap=None, stream=None):
+    """tokens (int32 [M]) drawn from rows of logits [M, V] (float32 or bfloat16) with each row's temperature (0: argmax), top_k,
+    top_p and min_p (tensors [M] or None), the noise keyed by (seed, position[row], seq[row]) as in lmhead_sample."""
+    dev, (M, V) = logits.get_device(), logits.shape
+    lp, ls = _matrix(logits, _DTYPES, "logits must be float32 or bfloat16 [M, V]", dev)
+    if position is None or tokens is None:
+        raise ValueError("glance: position and tokens are required")
+    _check(lib().glance_sample(lp, ls, _DTYPES[logits.dtype], M, V, _per_row(temperature, _F32T, M, dev), _per_row(top_k, _I32, M, dev),
+                               _per_row(top_p, _F32T, M, dev), _per_row(min_p, _F32T, M, dev), int(seed) & ((1 << 64) - 1),
+                               _per_row(position, _I32, M, dev), _per_row(seq, _I32, M, dev), _per_row(tokens, _I32, M, dev),
+                               _per_row(gap, _F32T, M, dev), _on(stream, dev)))
 
 
 def device_status():

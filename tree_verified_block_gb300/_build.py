@@ -25,8 +25,9 @@ OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libglance.so")
 CHECK_OUT = os.path.join(OUT, "check")
 LIB_CHECK = os.path.join(OUT, "libglance_check.so")
-UNITS = ["api", "build_tree", "tree_attention", "lmhead", "commit", "dense", "kv4", "kv4_attention", "rope", "q8_rows", "q8_linear"]
+UNITS = ["api", "build_tree", "tree_attention", "lmhead", "commit", "dense", "kv4", "kv4_attention", "rope", "q8_rows", "q8_linear", "sample"]
 HEADERS = [os.path.join(CSRC, "glance_internal.cuh"), os.path.join(CSRC, "kv4_internal.cuh"), os.path.join(CSRC, "q8_internal.cuh"),
+           os.path.join(CSRC, "noise.cuh"),
            os.path.join(ROOT, "include", "glance.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

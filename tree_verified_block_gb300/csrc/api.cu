@@ -109,8 +109,8 @@ const char* glance_status_string(glance_status s) {
 // The families of status words, in the order of glance_get_status, and the
 // units that report with one of them (the family's index).
 constexpr int kStatusUnits = 5;
-constexpr int kStatusExtra = 5;
-static const int kExtraFamily[kStatusExtra] = {1, 3, 4, 4, 4};  // attention, walk + commit, dense layers
+constexpr int kStatusExtra = 6;
+static const int kExtraFamily[kStatusExtra] = {1, 3, 4, 4, 4, 2};  // attention, walk + commit, dense layers, LM head
 
 static glance_status read_all_status(int32_t* code_out, bool reset) {
   cudaError_t e = cudaDeviceSynchronize();
@@ -119,7 +119,7 @@ static glance_status read_all_status(int32_t* code_out, bool reset) {
   cudaError_t (*fns[kStatusUnits + kStatusExtra])(int*, bool) = {
       glance::status_build_tree, glance::status_attention, glance::status_lmhead, glance::status_commit,
       glance::status_dense, glance::status_kv4_attention, glance::status_kv4, glance::status_rope,
-      glance::status_q8_rows, glance::status_q8_linear};
+      glance::status_q8_rows, glance::status_q8_linear, glance::status_sample};
   for (auto fn : fns) {
     int v = 0;
     e = fn(&v, reset);
@@ -158,7 +158,7 @@ __global__ void first_status_kernel(int32_t* out, int n, ExtraWords extra) {
 cudaError_t extra_words(void* (&addr)[kStatusExtra]) {
   cudaError_t (*fns[kStatusExtra])(void**) = {glance::status_kv4_attention_addr, glance::status_kv4_addr,
                                               glance::status_rope_addr, glance::status_q8_rows_addr,
-                                              glance::status_q8_linear_addr};
+                                              glance::status_q8_linear_addr, glance::status_sample_addr};
   for (int i = 0; i < kStatusExtra; ++i) {
     const cudaError_t e = fns[i](&addr[i]);
     if (e != cudaSuccess) return e;

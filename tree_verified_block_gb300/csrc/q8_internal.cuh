@@ -14,6 +14,7 @@ namespace glance {
 
 GLANCE_DECLARE_STATUS_WORD(status_q8_rows)
 GLANCE_DECLARE_STATUS_WORD(status_q8_linear)
+GLANCE_DECLARE_STATUS_WORD(status_sample)
 
 constexpr int kQ8MaxRows = 1 << 24;  // rows of a call
 constexpr int64_t kQ8MaxStride = 1ll << 40;
