@@ -725,7 +725,7 @@ glance_status glance_kv4_accept_commit(const glance_tree* trees, int B, const in
  * element times 2^-e rounded to nearest even. A row that has an element that
  * is not finite gets the scale NaN and codes 0.
  * Limits of the three calls: 1 <= M <= 2^24, d a multiple of 16 up to 32768
- * (BF16) or 16384 (F32); arrays 16-byte aligned (scales 4-byte), strides (in
+ * (rows of F32 that are quantised: 16384); arrays 16-byte aligned (scales 4-byte), strides (in
  * elements) multiples of 16 bytes that cover a row.
  */
 

@@ -295,11 +295,10 @@ glance_status launch(const char* who, const void* kernel_args, const void* kerne
 // Bytes from the first to behind the last element of rows.
 int64_t span(int M, int64_t stride_bytes, int64_t row_bytes) { return (M - 1) * stride_bytes + row_bytes; }
 
-glance_status check_shape(const char* who, glance_dtype dtype, int M, int d, int64_t code_stride) {
+glance_status check_shape(const char* who, glance_dtype dtype, int M, int d, int most, int64_t code_stride) {
   using glance::fail;
   if (dtype != GLANCE_BF16 && dtype != GLANCE_F32) return fail(GLANCE_ERR_INVALID_ARG, "%s: dtype must be F32 or BF16", who);
   if (M < 1 || M > glance::kQ8MaxRows) return fail(GLANCE_ERR_INVALID_ARG, "%s: need 1 <= M <= 2^24", who);
-  const int most = kMaxVecs * 16 / (dtype == GLANCE_BF16 ? 2 : 4);
   if (d < 16 || d > most || d % 16) return fail(GLANCE_ERR_UNSUPPORTED, "%s: d must be a multiple of 16, at most %d", who, most);
   if (code_stride < d || code_stride > glance::kQ8MaxStride || code_stride % 16)
     return fail(GLANCE_ERR_INVALID_ARG, "%s: code_stride must cover a row and be a multiple of 16", who);
@@ -316,9 +315,9 @@ glance_status run_rows(const char* who, const void* x, int64_t x_stride, const v
   using glance::fail;
   using glance::overlap;
   if (!x || !codes || !scales) return fail(GLANCE_ERR_INVALID_ARG, "%s: null pointer argument", who);
-  const glance_status st = check_shape(who, dtype, M, d, code_stride);
-  if (st != GLANCE_OK) return st;
   const int esize = dtype == GLANCE_BF16 ? 2 : 4;
+  const glance_status st = check_shape(who, dtype, M, d, kMaxVecs * 16 / esize, code_stride);
+  if (st != GLANCE_OK) return st;
   if (bad_stride(x_stride, d, esize) || (residual && bad_stride(r_stride, d, esize)) || (total && bad_stride(t_stride, d, esize)))
     return fail(GLANCE_ERR_INVALID_ARG, "%s: row strides must cover a row and be multiples of 16 bytes", who);
   if (norm && (!(eps >= 0.f) || !isfinite(eps))) return fail(GLANCE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
@@ -381,7 +380,7 @@ glance_status glance_q8_read_rows(const void* codes, int64_t code_stride, const 
   using glance::fail;
   const char* who = "glance_q8_read_rows";
   if (!codes || !scales || !out) return fail(GLANCE_ERR_INVALID_ARG, "%s: null pointer argument", who);
-  const glance_status st = check_shape(who, dtype, M, d, code_stride);
+  const glance_status st = check_shape(who, dtype, M, d, kMaxVecs * 8, code_stride);
   if (st != GLANCE_OK) return st;
   const int esize = dtype == GLANCE_BF16 ? 2 : 4;
   if (bad_stride(out_stride, d, esize))
