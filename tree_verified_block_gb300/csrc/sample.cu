@@ -10,22 +10,34 @@
 // = earlier. The token is argmax l_v r + g_v over the kept ones, g_v the noise of
 // the LM head's sampling mode: a draw from their renormalised softmax.
 //
-// A row is read once, by a cluster of CTAs that keep it in their shared memory.
-// Its border is found without a sort of the row:
-// * A histogram of (max - l) r in steps of 1/64 holds each bin's count and its
-//   weight. Within a bin weights are W (1 - d), d < 1/64, W a constant of the
-//   bin: the sum of the d is kept as an integer (2^-22 units), so that it does not
-//   depend on the order of the additions and is good to 2^-23 of each weight.
-// * Where at most kList tokens lie in the bins up to the border's, they are
-//   gathered by the cluster's first CTA, sorted, summed and drawn from there.
-// * Else the border's bin is divided by further histograms, over ranges of the
-//   50-bit numbers, until what is left fits the list; then every CTA looks at its
-//   part of the row once more for the draw.
-// Weights below e^-32 of the largest are outside the histogram: 2^18 of them
-// hold 4e-9 of the sum, under what an fp32 top_p can name.
+// A row is never sorted. One pass finds its maximum, and 512 maxima of disjoint
+// parts of it. Then, whichever comes first:
+// * k up to 384: at least k tokens are no smaller than the k-th largest of the
+//   parts' maxima, and seldom many more. They are gathered, sorted, summed and
+//   drawn from by one CTA.
+// * Else a histogram of (max - l) r in steps of 1/64 holds each bin's count, or
+//   its count and weight. Where at most kList tokens lie in the bins up to the
+//   border's, these are gathered as above. Where not, the border's bin is (divided
+//   by further histograms, over ranges of the 50-bit numbers, until it fits the
+//   list, and) sorted, which gives the last token, and every CTA draws from its
+//   part of the row.
+// Within a bin weights are W (1 + y), |y| < 1/127, W a constant of the bin: the
+// sum of the y is kept as an integer in 2^-21 units, so that it does not depend
+// on the order of the additions and is good to 2^-22 of each weight. For top-p
+// alone, tokens whose weights are so small that all of them together could not
+// reach (1 - p) / 2 are summed without a bin. Weights below e^-31.9 of the largest
+// are outside the histogram: 2^18 of them hold 4e-9 of the sum, under what an
+// fp32 top_p can name.
 //
 // The draw's values are fp32 and compared in fp32 except for those that are near
 // the best: these are evaluated again in fp64, so that rounding decides nothing.
+// Most tokens need no logarithm: g >= t only if 1 - u <= e^-t, and once a warp has
+// two values the noise's own bits decide.
+//
+// Forms of the kernel, by how many rows there are to fill the GPU: a CTA per row,
+// which reads the row again from L2 for a second pass, or a cluster that keeps
+// the row in its shared memory. Every decision that a cluster's CTAs take by
+// themselves is taken from values that all of them hold alike.
 #include <cstring>
 #include <mutex>
 
@@ -40,15 +52,19 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
 constexpr int kList = 2048;
-constexpr int kMaxCluster = 16;
+constexpr int kPer = kList / kThreads;
+constexpr int kGroups = kThreads;         // parts of a row whose maxima are known
+constexpr int kGroupK = kGroups * 3 / 4;  // so many of them are below the k-th, and the list will do
 constexpr int kIdBits = 18;
 constexpr int kMaxV = 1 << kIdBits;
-constexpr int kMaxSlice = 32768;  // ids of a CTA: a bin's sum of d (2^16 units each at most) stays within 32 bits
-constexpr int kCand = kThreads;
-constexpr float kBinsPerNat = 64.f, kRange = 32.f;
-constexpr float kUnit = 4194304.f;  // 2^22
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kBinsPerNat = 64.f, kRange = 31.9f;  // of the histogram
+constexpr int kUnitBits = 21;
+// What a token adds to its bin: (1 + y) 2^21 less this, which is e^(-1/128) 2^21
+// and a little less: at most 2^15 + 200 units, which 2^16 tokens leave within 32 bits.
+constexpr uint32_t kUnitOff = 2080639u;
 
 struct Params {
   const char* logits;
@@ -65,9 +81,15 @@ struct Params {
   int M, V, slice;  // slice: ids of a CTA, a multiple of 64
 };
 
-// e^-i/2 and e^-i/64 to double precision: a bin's W is the product of two.
+// Weights are added up as integers in units of 2^-40 (a row's largest weight is
+// 1, its sum at most 2^18): exact, so that the order does not matter, and without
+// the fp64 units, of which an SM has two.
+typedef unsigned long long Mass;
+constexpr int kMassBits = 40;
+
+// e^-i/2 and e^-i/64 in units of 2^-63: a bin's W is the product of two.
 struct Exps {
-  double half[64], part[32];
+  Mass half[64], part[32];
 };
 constexpr double series_exp(double x) {  // |x| <= 1/2
   double term = 1, sum = 1;
@@ -79,60 +101,95 @@ constexpr double series_exp(double x) {  // |x| <= 1/2
 }
 constexpr Exps make_exps() {
   Exps e = {};
-  e.half[0] = 1;
-  for (int i = 1; i < 64; ++i) e.half[i] = e.half[i - 1] * series_exp(-0.5);
-  for (int i = 0; i < 32; ++i) e.part[i] = series_exp(-i / 64.0);
+  double h = 1;
+  for (int i = 0; i < 64; ++i, h *= series_exp(-0.5)) e.half[i] = static_cast<Mass>(h * 9223372036854775808.0);
+  for (int i = 0; i < 32; ++i) e.part[i] = static_cast<Mass>(series_exp(-i / 64.0) * 9223372036854775808.0);
   return e;
 }
 __constant__ Exps c_exps = make_exps();
+// W of a bin in units of 2^-62.
+__device__ __forceinline__ Mass weight_of_bin(int bin) { return __umul64hi(c_exps.half[bin >> 5], c_exps.part[bin & 31]); }
+// W times a sum in units of 2^-21 (at most 2^40).
+__device__ __forceinline__ Mass mass_of(Mass w, Mass sum) { return __umul64hi(w, sum << (64 + kMassBits - 62 - kUnitBits)); }
+static_assert(kUnitBits + kIdBits + (64 + kMassBits - 62 - kUnitBits) < 64, "units");
+// A share (in units of 2^-64) of a weight, at least one unit.
+__device__ __forceinline__ Mass part_of(Mass all, Mass share) {
+  const Mass m = __umul64hi(all, share);
+  return m ? m : 1;
+}
 
 struct Border {  // the bin in which a prefix ends
   int bin;       // -1: the prefix has all
   uint32_t count_before, count_in;
-  double mass_before, mass_all;
+  Mass mass_before, mass_all;
 };
 struct Best {
-  float z1, z2;
-  int id;
+  float z1, z2;  // the two best values, of
+  int id;        // the best one's token
+  float l;       // and its logit
+};
+struct Cut {
+  uint64_t number;  // the last token that is kept
+  Mass mass;        // the weight up to it (of a search by weight)
 };
 
+template <int kCtas>
 struct Shared {
+  // a CTA with a whole row adds its warps' sums to four places: 2^16 tokens each at most
+  static constexpr int kSums = kCtas == 1 ? 4 : 1;
   union {
     struct {
-      uint32_t count[kBins], d[kBins];
-    } hist;
-    uint64_t list[kList];
+      uint32_t count[kBins], sum[kSums][kBins];
+    };
+    struct {
+      uint64_t list[kList];  // the first CTA's: numbers of tokens
+      int part[kThreads];    // one CTA: the threads whose tokens are looked at again
+    };
+    struct {  // of the draw
+      double near_z[kThreads];
+      float near_l[kThreads];
+      int near_id[kThreads];
+    };
   };
   // written by the cluster's other CTAs
-  float peer_max[kMaxCluster];
-  uint64_t peer_lo[kMaxCluster], peer_hi[kMaxCluster];
-  double peer_mass[kMaxCluster];
-  uint32_t peer_count[kMaxCluster];
-  Best peer_best[kMaxCluster];
-  Border border;
-  uint64_t cut;
-  double cut_mass;
-  uint32_t list_n, cand_n;
-  float cand_l[kCand];
-  int cand_id[kCand];
+  float group[kGroups];
+  Mass coarse_mass[kCtas][kCoarse + 1];  // [kCoarse]: of tokens without a bin
+  uint32_t coarse_count[kCtas][kCoarse];
+  Best peer_best[kCtas];
+  uint64_t peer_lo[kCtas], peer_hi[kCtas];
+  Cut cut;
+  uint32_t list_n[3];
   // this CTA's own
-  double warp_mass[kWarps];
+  uint32_t near_n, part_n;
+  Border border;
+  Mass fine_mass[kCtas][kFine];
+  uint32_t fine_count[kCtas][kFine];
+  Mass warp_mass[kWarps];
   uint32_t warp_count[kWarps];
-  float warp_f[kWarps];
+  float warp_f[kWarps], warp_second[kWarps];
   uint64_t warp_lo[kWarps], warp_hi[kWarps];
   Best warp_best[kWarps];
   float min_l;
   double log_min_p;
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// ------------------------------------------------- the cluster, if it is one
+
+template <int kCtas>
+__device__ __forceinline__ void sync_row() {
+  __syncwarp();  // the cluster's barrier wants whole warps
+  if (kCtas > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
 }
-template <typename X>
-__device__ __forceinline__ void to_peer(X* local, int rank, X v) {
-  // plain stores of 4-byte words to the same place in CTA `rank`
+// To the same place in CTA `rank`.
+template <int kCtas, typename X>
+__device__ __forceinline__ void to_peer(X* local, int rank, const X& v) {
+  if (kCtas == 1) {
+    *local = v;
+    return;
+  }
   static_assert(sizeof(X) % 4 == 0, "words");
   const uint32_t at = dsmem_addr(local, rank);
   uint32_t w[sizeof(X) / 4];
@@ -141,541 +198,755 @@ __device__ __forceinline__ void to_peer(X* local, int rank, X v) {
   for (int i = 0; i < static_cast<int>(sizeof(X) / 4); ++i)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(w[i]) : "memory");
 }
-__device__ __forceinline__ uint32_t peer_u32(const void* local, int rank) {
+template <int kCtas>
+__device__ __forceinline__ uint32_t peer_u32(const uint32_t* local, int rank) {
+  if (kCtas == 1) return *reinterpret_cast<const volatile uint32_t*>(local);
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(local, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t peer_add(uint32_t* local, int rank, uint32_t v) {
+template <int kCtas>
+__device__ __forceinline__ uint32_t add_first(uint32_t* local, uint32_t v) {  // to the first CTA's counter
+  if (kCtas == 1) return atomicAdd(local, v);
   uint32_t old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(dsmem_addr(local, rank)), "r"(v) : "memory");
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(dsmem_addr(local, 0)), "r"(v) : "memory");
   return old;
 }
+
+// -------------------------------------------------------------------- the row
 
 __device__ __forceinline__ uint64_t number_of(float l, int id) {
   return static_cast<uint64_t>(ord_key(l)) << kIdBits | static_cast<uint32_t>(kMaxV - 1 - id);
 }
 __device__ __forceinline__ int id_of(uint64_t number) { return kMaxV - 1 - static_cast<int>(number & (kMaxV - 1)); }
-__device__ __forceinline__ float logit_of(uint64_t number) {
-  const uint32_t k = static_cast<uint32_t>(number >> kIdBits);
-  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ float logit_of(uint64_t number) { return of_key(static_cast<uint32_t>(number >> kIdBits)); }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// The row as this thread sees it.
+// The row as this CTA sees it.
 struct Row {
-  float top, r;  // the largest logit; 1 / T
-  float min_l;   // tokens below are not kept
-  int rank, ctas, first, n;  // this CTA's ids: first .. first + n - 1
+  const unsigned char* at;  // its part: in shared memory, padded with -infinity, or global
+  bool vec;                 // global: four logits from a multiple of four on are aligned
+  float own;                // the largest logit of this thread's tokens
+  float top, r;             // the row's largest; 1 / T
+  float min_l;              // tokens below are not kept
+  int rank, first, n;       // ids first .. first + n - 1
 };
-
-// (max - l) r, its rounding error, and from them the bin and d
-__device__ __forceinline__ bool place(const Row& w, float l, int& bin, float& d) {
-  const float x = w.top - l, prod = x * w.r;
-  if (!(prod < kRange) || l < w.min_l) return false;
-  const float err = fmaf(x, w.r, -prod);
-  bin = static_cast<int>(prod * kBinsPerNat);
-  const float y = fmaxf(fmaf(static_cast<float>(bin), -1.f / kBinsPerNat, prod) + err, 0.f);
-  // 1 - e^-y, y < 1/64 (to y^5 / 120 < 1e-11)
-  d = y * fmaf(y, fmaf(y, fmaf(y, -1.f / 24, 1.f / 6), -0.5f), 1.f);
-  return true;
-}
-__device__ __forceinline__ double weight_of_bin(int bin) { return c_exps.half[bin >> 5] * c_exps.part[bin & 31]; }
 
 template <typename T>
-struct Row4;  // four consecutive logits in shared memory
+__device__ __forceinline__ void unpack4(const unsigned char* p, float (&l)[4]);
 template <>
-struct Row4<float> {
-  static __device__ __forceinline__ void load(const unsigned char* s, int i, float (&l)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(s + 4 * i);
-    l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
-  }
-};
+__device__ __forceinline__ void unpack4<float>(const unsigned char* p, float (&l)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+}
 template <>
-struct Row4<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const unsigned char* s, int i, float (&l)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(s + 2 * i);
-    l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xFFFF0000u);
-  }
-};
-
-// Calls f(logit, id) for this CTA's tokens, four consecutive ids a thread at a
-// time (ids behind the row are -infinity).
-template <typename T, typename F>
-__device__ __forceinline__ void each(const unsigned char* s_row, const Row& w, F f) {
-  for (int i = 4 * static_cast<int>(threadIdx.x); i < w.n; i += 4 * kThreads) {
-    float l[4];
-    Row4<T>::load(s_row, i, l);
+__device__ __forceinline__ void unpack4<__nv_bfloat16>(const unsigned char* p, float (&l)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void pack4(float* p, const float (&l)[4]) { *reinterpret_cast<float4*>(p) = make_float4(l[0], l[1], l[2], l[3]); }
+__device__ __forceinline__ void pack4(__nv_bfloat16* p, const float (&l)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3]));
+}
+template <typename T, bool kGlobal>
+__device__ __forceinline__ void load4(const Row& w, int i, float (&l)[4]) {
+  const unsigned char* p = w.at + static_cast<size_t>(i) * sizeof(T);
+  if (!kGlobal || (w.vec && i + 4 <= w.n)) {
+    unpack4<T>(p, l);
+  } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f(l[j], w.first + i + j);
+    for (int j = 0; j < 4; ++j) l[j] = i + j < w.n ? static_cast<float>(reinterpret_cast<const T*>(p)[j]) : -INFINITY;
   }
 }
-
-__device__ __forceinline__ void clear_hist(Shared* s) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s->hist.count[i] = s->hist.d[i] = 0u;
-}
-
-__device__ __forceinline__ uint32_t scan_add(uint32_t v, int lane) {
+// Calls f(four logits, the first one's id) for this CTA's tokens, from a
+// multiple of four on; kBatch loads of a thread are in flight. after() follows
+// each batch, with every warp's lanes together. A thread with its largest logit
+// below `least` is passed over.
+template <typename T, bool kGlobal, int kBatch, typename F, typename G>
+__device__ __forceinline__ void each4(const Row& w, float least, F f, G after) {
+  const bool mine = w.own >= least;
+  if (!__any_sync(0xffffffffu, mine)) return;
+  const int t = threadIdx.x, warp0 = 4 * (t & ~31);
+  for (int base = 0; base + warp0 < w.n; base += 4 * kThreads * kBatch) {
+    float l[kBatch][4];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-__device__ __forceinline__ double scan_add(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
-// The bin of the cluster's histogram in which the prefix of `want` tokens
-// (want > 0) or else of `share` of the weight (of mass_all, if given, else of
-// what the histogram has) ends. fixed_bin >= 0: every bin's W is that bin's.
-// count0, mass0: what lies before the histogram. All threads of the cluster get
-// the same answer.
-__device__ Border find_border(Shared* s, const Row& w, uint32_t want, double share, double mass_all, int fixed_bin, uint32_t count0,
-                              double mass0) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  cluster_sync_all();  // the histograms are complete
-  const int mine = kBins / w.ctas, per = (mine + kThreads - 1) / kThreads;  // bins of this CTA, of a thread: 1, 2 or 4
-  uint32_t c[4];
-  double m[4], mass = 0;
-  uint32_t count = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    c[j] = 0;
-    m[j] = 0;
-    const int in = static_cast<int>(threadIdx.x) * per + j;
-    if (j < per && in < mine) {
-      const int bin = w.rank * mine + in;
-      uint64_t d = 0;
-      for (int q = 0; q < w.ctas; ++q) {
-        c[j] += peer_u32(&s->hist.count[bin], q);
-        d += peer_u32(&s->hist.d[bin], q);
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = base + 4 * t + u * 4 * kThreads;
+      if (mine && i < w.n) {
+        load4<T, kGlobal>(w, i, l[u]);
+      } else {
+        l[u][0] = l[u][1] = l[u][2] = l[u][3] = -INFINITY;
       }
-      if (c[j]) m[j] = weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin) * (c[j] - static_cast<double>(d) * (1.0 / kUnit));
     }
-    count += c[j];
-    mass += m[j];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) f(l[u], w.first + base + 4 * t + u * 4 * kThreads);
+    __syncwarp();
+    after();
   }
-  const uint32_t count_to = scan_add(count, lane);
-  const double mass_to = scan_add(mass, lane);
-  if (lane == 31) {
-    s->warp_count[warp] = count_to;
-    s->warp_mass[warp] = mass_to;
+}
+template <typename T, bool kGlobal, typename F>
+__device__ __forceinline__ void each(const Row& w, float least, F f) {
+  each4<T, kGlobal, 4>(
+      w, least,
+      [&](const float(&l)[4], int id) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f(l[j], id + j);
+      },
+      [] {});
+}
+// The same, for the few threads that have a token with l >= least (others may
+// come too). A CTA that has to fetch their tokens from L2 shares them out to all.
+template <typename T, int kCtas, bool kGlobal, typename F>
+__device__ __forceinline__ void each_of_few(Shared<kCtas>* s, const Row& w, float least, F f) {
+  if constexpr (kGlobal) {
+    if (threadIdx.x == 0) s->part_n = 0;
+    __syncthreads();
+    if (w.own >= least) s->part[atomicAdd(&s->part_n, 1u)] = threadIdx.x;
+    __syncthreads();
+    const int parts = s->part_n, per = (w.n + 4 * kThreads - 1) / (4 * kThreads);  // groups of four of a thread
+    if (parts <= kThreads / 4) {
+      constexpr int kBatch = 4;
+      for (int i0 = threadIdx.x; i0 < parts * per; i0 += kThreads * kBatch) {
+        float l[kBatch][4];
+        int at[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = i0 + u * kThreads;
+          at[u] = i < parts * per ? 4 * (s->part[i / per] + kThreads * (i % per)) : w.n;
+          if (at[u] < w.n) load4<T, true>(w, at[u], l[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (at[u] < w.n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(l[u][j], w.first + at[u] + j);
+          }
+      }
+      return;
+    }
+  }
+  each<T, kGlobal>(w, least, f);
+}
+
+// ------------------------------------------------------------- bins and sums
+
+// A token's bin, the nearest multiple of 1/64 to (max - l) r, and e^(bin / 64 -
+// (max - l) r) - 1. False: not kept, or too small for the histogram. The bin does
+// not decrease as l falls.
+__device__ __forceinline__ bool place(const Row& w, float l, int& bin, float& y) {
+  const float x = __fmul_rn(w.top - l, w.r);
+  if (!(x < kRange) || l < w.min_l) return false;
+  const float n = fmaf(x, kBinsPerNat, 8388608.f);  // 2^23: rounds to a whole number in the low bits
+  bin = static_cast<int>(__float_as_uint(n) & 0x7FFFFFu);
+  const float d = fmaf(n - 8388608.f, 1.f / kBinsPerNat, -x);  // |d| <= 1/128
+  y = d * fmaf(d, fmaf(d, fmaf(d, 1.f / 24, 1.f / 6), 0.5f), 1.f);  // to d^5 / 120 < 3e-13
+  return true;
+}
+// A logit that no token of the bins up to `bin` is below.
+__device__ __forceinline__ float least_of_bin(const Row& w, int bin) {
+  const float x = (static_cast<float>(bin) + 0.51f) / kBinsPerNat / w.r;
+  return w.top - x - 1e-6f * (fabsf(w.top) + x);
+}
+
+template <int kCtas>
+__device__ __forceinline__ void clear_hist(Shared<kCtas>* s) {
+  uint4* h = reinterpret_cast<uint4*>(s->count);
+  for (int i = threadIdx.x; i < kBins * (1 + Shared<kCtas>::kSums) / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+template <int kCtas>
+__device__ __forceinline__ void add_hist(Shared<kCtas>* s, int bin, float y, bool weigh) {
+  atomicAdd(&s->count[bin], 1u);
+  if (!weigh) return;
+  // (1 + y) 2^21 rounded, from the low bits of a float, less the base
+  const uint32_t f = (__float_as_uint(fmaf(y, 2097152.f, 2097152.f + 8388608.f)) & 0x7FFFFFu) - kUnitOff;
+  atomicAdd(&s->sum[(threadIdx.x >> 5) & (Shared<kCtas>::kSums - 1)][bin], f);
+}
+
+template <typename X>
+__device__ __forceinline__ X scan_add(X v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const X u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ Mass sum_of(uint32_t count, uint64_t sum) { return static_cast<Mass>(count) * kUnitOff + sum; }
+
+// The bin of the row's histogram in which the prefix of `want` tokens (want > 0)
+// or else of `share` of the weight (of mass_all if given, else of what there is)
+// ends; loose: the weight of this thread's tokens without a bin. fixed_bin >= 0:
+// every bin's W is that bin's. count0, mass0: what lies before the histogram.
+// Every CTA joins 64 sums of 32 bins of all of them, and looks at one of the 64
+// more closely: the same in all of them.
+template <int kCtas>
+__device__ Border find_border(Shared<kCtas>* s, const Row& w, uint32_t want, Mass share, Mass mass_all, float loose, int fixed_bin,
+                              uint32_t count0, Mass mass0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
+  constexpr int kEach = kBins / kThreads, kJoin = kFine / kEach;  // bins of a thread, threads of a coarse bin
+  __syncthreads();
+  uint32_t count = 0;
+  Mass mass = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int bin = t * kEach + j;
+    const uint32_t c = s->count[bin];
+    if (c) {
+      uint64_t sum = 0;
+#pragma unroll
+      for (int i = 0; i < Shared<kCtas>::kSums; ++i) sum += s->sum[i][bin];
+      count += c;
+      mass += mass_of(weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin), sum_of(c, sum));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < kJoin; o <<= 1) {
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  }
+  Mass extra = __float2ull_rn(loose * 1099511627776.f);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) extra += __shfl_xor_sync(0xffffffffu, extra, o);
+  if (lane == 0) s->warp_mass[warp] = extra;
+  for (int q = t % kJoin; q < kCtas; q += kJoin) {
+    to_peer<kCtas>(&s->coarse_count[w.rank][t / kJoin], q, count);
+    to_peer<kCtas>(&s->coarse_mass[w.rank][t / kJoin], q, mass);
   }
   __syncthreads();
-  uint32_t count_at = 0, count_cta = 0;
-  double mass_at = 0, mass_cta = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    if (i == warp) {
-      count_at = count_cta;
-      mass_at = mass_cta;
-    }
-    count_cta += s->warp_count[i];
-    mass_cta += s->warp_mass[i];
+  if (t < kCtas) {
+    Mass all = 0;
+    for (int i = 0; i < kWarps; ++i) all += s->warp_mass[i];
+    to_peer<kCtas>(&s->coarse_mass[w.rank][kCoarse], t, all);
   }
-  if (threadIdx.x < w.ctas) {
-    to_peer(&s->peer_count[w.rank], threadIdx.x, count_cta);
-    to_peer(&s->peer_mass[w.rank], threadIdx.x, mass_cta);
-  }
-  if (threadIdx.x == 0) s->border.bin = -1;
-  cluster_sync_all();
-  uint32_t base_count = count0, count_all = count0;
-  double base = mass0, all = mass0;
-  for (int q = 0; q < w.ctas; ++q) {
-    if (q == w.rank) {
-      base_count = count_all;
-      base = all;
-    }
-    count_all += s->peer_count[q];
-    all += s->peer_mass[q];
-  }
-  if (mass_all <= 0) mass_all = all;
-  const double target = share * mass_all;
-  count_at += base_count + count_to - count;
-  mass_at += base + mass_to - mass;
+  if (t == 0) s->border.bin = -1;
+  sync_row<kCtas>();
+  uint32_t count_to = 0;
+  Mass mass_to = 0;
+  count = 0;
+  mass = 0;
+  if (t < kCoarse) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // the first token at which the prefix is long or heavy enough is in this bin
-    const bool here = c[j] && (want ? count_at < want && count_at + c[j] >= want
-                                    : mass_at < target && mass_at + m[j] >= target);
-    if (here) {
-      const Border b = {w.rank * mine + static_cast<int>(threadIdx.x) * per + j, count_at, c[j], mass_at, mass_all};
-      for (int q = 0; q < w.ctas; ++q) to_peer(&s->border, q, b);
+    for (int q = 0; q < kCtas; ++q) {
+      count += s->coarse_count[q][t];
+      mass += s->coarse_mass[q][t];
     }
-    count_at += c[j];
-    mass_at += m[j];
+    count_to = scan_add(count, lane);
+    mass_to = scan_add(mass, lane);
+    if (lane == 31) {
+      s->warp_count[warp] = count_to;
+      s->warp_mass[warp] = mass_to;
+    }
   }
-  cluster_sync_all();
+  __syncthreads();
+  Mass all = mass0 + s->warp_mass[0] + s->warp_mass[1];
+  for (int q = 0; q < kCtas; ++q) all += s->coarse_mass[q][kCoarse];
+  if (mass_all == 0) mass_all = all;
+  const Mass target = part_of(mass_all, share);
+  if (t < kCoarse) {
+    const uint32_t before = count0 + (warp ? s->warp_count[0] : 0u) + count_to - count;
+    const Mass before_mass = mass0 + (warp ? s->warp_mass[0] : 0ull) + mass_to - mass;
+    if (count && (want ? before < want && before + count >= want : before_mass < target && before_mass + mass >= target)) {
+      s->border.bin = t;
+      s->border.count_before = before;
+      s->border.mass_before = before_mass;
+    }
+  }
+  __syncthreads();
   Border b = s->border;
+  b.mass_all = mass_all;
+  if (b.bin < 0) return b;
+  for (int q = warp; q < kCtas; q += kWarps) {
+    const int bin = b.bin * kFine + lane;
+    const uint32_t c = peer_u32<kCtas>(&s->count[bin], q);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < Shared<kCtas>::kSums; ++i) sum += peer_u32<kCtas>(&s->sum[i][bin], q);
+    s->fine_count[q][lane] = c;
+    s->fine_mass[q][lane] = c ? mass_of(weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin), sum_of(c, sum)) : 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    count = 0;
+    mass = 0;
+    for (int q = 0; q < kCtas; ++q) {
+      count += s->fine_count[q][lane];
+      mass += s->fine_mass[q][lane];
+    }
+    const uint32_t before = b.count_before + scan_add(count, lane) - count;
+    const Mass before_mass = b.mass_before + scan_add(mass, lane) - mass;
+    // the bins were rounded one by one in either place: the sums agree
+    const unsigned here = __ballot_sync(0xffffffffu, count && (want ? before < want && before + count >= want
+                                                                    : before_mass < target && before_mass + mass >= target));
+    if (here && lane == __ffs(here) - 1) s->border = Border{b.bin * kFine + lane, before, count, before_mass, mass_all};
+  }
+  __syncthreads();
+  b = s->border;
   b.mass_all = mass_all;
   return b;
 }
 
-// Sorts s->list[0 .. n) in descending order (one CTA).
-__device__ void sort_list(Shared* s, int n) {
+__device__ __forceinline__ int power_from(int n) {
   int size = 32;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) s->list[i] = 0;
-  __syncthreads();
+  while (size < n && size < kList) size <<= 1;
+  return size;
+}
+// One step of the sort: the larger of two to the lower place where the run that
+// place e is in goes down.
+__device__ __forceinline__ uint64_t step_down(uint64_t v, uint64_t u, int e, int j, int k) {
+  return (v > u) == (((e & j) == 0) == ((e & k) == 0)) ? v : u;
+}
+__device__ __forceinline__ uint64_t sort_warp(uint64_t v, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j; j >>= 1) v = step_down(v, __shfl_xor_sync(0xffffffffu, v, j), lane, j, k);
+  return v;
+}
+// Sorts list[0 .. n) downwards, n <= kRows * kThreads, by the whole CTA: place e =
+// 512 i + t is thread t's i-th.
+template <int kRows>
+__device__ void sort_rows(uint64_t* list, int n) {
+  const int t = threadIdx.x, size = power_from(n);
+  uint64_t v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) v[i] = i * kThreads + t < n ? list[i * kThreads + t] : 0ull;
+#pragma unroll 1
   for (int k = 2; k <= size; k <<= 1)
+#pragma unroll 1
     for (int j = k >> 1; j; j >>= 1) {
-      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-        const int a = 2 * i - (i & (j - 1)), b = a + j;
-        const uint64_t x = s->list[a], y = s->list[b];
-        if ((x < y) == ((a & k) == 0)) {
-          s->list[a] = y;
-          s->list[b] = x;
+      if (j >= kThreads) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int o = i ^ (j / kThreads);
+#pragma unroll
+          for (int i2 = 0; i2 < kRows; ++i2)
+            if (i2 == o && i2 > i) {
+              const uint64_t a = v[i], b = v[i2];
+              v[i] = step_down(a, b, i * kThreads + t, j, k);
+              v[i2] = step_down(b, a, i2 * kThreads + t, j, k);
+            }
         }
+      } else if (j >= 32) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) list[i * kThreads + t] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) v[i] = step_down(v[i], list[i * kThreads + (t ^ j)], i * kThreads + t, j, k);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) v[i] = step_down(v[i], __shfl_xor_sync(0xffffffffu, v[i], j), i * kThreads + t, j, k);
       }
-      __syncthreads();
     }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) list[i * kThreads + t] = v[i];
+  __syncthreads();
+}
+__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
+  if (n <= kThreads)
+    sort_rows<1>(list, n);
+  else
+    sort_rows<kPer>(list, n);
 }
 
-// Weights of the sorted list's tokens before and up to each: this thread's four.
-__device__ void list_masses(Shared* s, const Row& w, int n, double mass0, double (&before)[kList / kThreads], double (&upto)[kList / kThreads]) {
+// A token's weight, to 2^-42 of its bin's.
+__device__ __forceinline__ Mass weight_of(const Row& w, float l) {
+  int bin;
+  float y;
+  return place(w, l, bin, y) ? __umul64hi(weight_of_bin(bin), (1ull << 42) + __float2ll_rn(y * 4398046511104.f)) : 0ull;
+}
+// Weight of the first CTA's sorted list before and up to each of this thread's
+// tokens, kPer from place kPer t on.
+template <int kCtas>
+__device__ void list_masses(Shared<kCtas>* s, const Row& w, int n, Mass mass0, Mass (&before)[kPer], Mass (&upto)[kPer]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double sum = 0;
+  Mass sum = 0;
 #pragma unroll
-  for (int j = 0; j < kList / kThreads; ++j) {
-    const int i = threadIdx.x * (kList / kThreads) + j;
-    double m = 0;
-    int bin;
-    float d;
-    if (i < n && place(w, logit_of(s->list[i]), bin, d)) m = weight_of_bin(bin) * (1.0 - static_cast<double>(d));
+  for (int j = 0; j < kPer; ++j) {
+    const int e = kPer * threadIdx.x + j;
     before[j] = sum;
-    sum += m;
+    if (e < n) sum += weight_of(w, logit_of(s->list[e]));
     upto[j] = sum;
   }
-  const double to = scan_add(sum, lane);
-  __syncthreads();
+  const Mass to = scan_add(sum, lane);
   if (lane == 31) s->warp_mass[warp] = to;
   __syncthreads();
-  double at = mass0 + to - sum;
+  Mass at = mass0 + to - sum;
   for (int i = 0; i < warp; ++i) at += s->warp_mass[i];
 #pragma unroll
-  for (int j = 0; j < kList / kThreads; ++j) {
+  for (int j = 0; j < kPer; ++j) {
     before[j] += at;
     upto[j] += at;
   }
 }
 
-// Gathers the numbers of the tokens that pass f(logit, id, number) in the first
-// CTA's list (there are kList at most); ends with a barrier of the cluster.
-template <typename T, typename F>
-__device__ void gather(Shared* s, const unsigned char* s_row, const Row& w, F f) {
-  each<T>(s_row, w, [&](float l, int id) {
-    const uint64_t number = number_of(l, id);
-    if (f(l, number)) {
-      const uint32_t at = peer_add(&s->list_n, 0, 1u);
-      if (at < kList) to_peer(&s->list[at], 0, number);
+// Gathers the numbers of the tokens with l >= least that pass f in the first
+// CTA's list and returns how many there were (kList fit). The cluster's
+// histograms are not in use any more.
+template <typename T, int kCtas, bool kGlobal, typename F>
+__device__ uint32_t gather(Shared<kCtas>* s, const Row& w, int turn, float least, F f) {
+  each_of_few<T, kCtas, kGlobal>(s, w, least, [&](float l, int id) {
+    if (l >= least) {
+      const uint64_t number = number_of(l, id);
+      if (f(l, number)) {
+        const uint32_t at = add_first<kCtas>(&s->list_n[turn], 1u);
+        if (at < kList) to_peer<kCtas>(&s->list[at], 0, number);
+      }
     }
   });
-  cluster_sync_all();
+  sync_row<kCtas>();
+  return peer_u32<kCtas>(&s->list_n[turn], 0);
 }
 
+// ------------------------------------------------------------------- the draw
+
+__device__ __forceinline__ bool ahead(float z, int id, float z0, int id0) { return z > z0 || (z == z0 && id < id0); }
 __device__ __forceinline__ void merge(Best& a, const Best& b) {
-  if (b.z1 > a.z1 || (b.z1 == a.z1 && b.id < a.id)) {
-    a.z2 = fmaxf(a.z1, b.z2);
-    a.z1 = b.z1;
-    a.id = b.id;
+  if (ahead(b.z1, b.id, a.z1, a.id)) {
+    a = Best{b.z1, fmaxf(a.z1, b.z2), b.id, b.l};
   } else {
     a.z2 = fmaxf(a.z2, b.z1);
   }
 }
 __device__ __forceinline__ Best warp_best(Best v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Best u = {__shfl_xor_sync(0xffffffffu, v.z1, o), __shfl_xor_sync(0xffffffffu, v.z2, o), __shfl_xor_sync(0xffffffffu, v.id, o)};
-    merge(v, u);
-  }
+  for (int o = 16; o; o >>= 1)
+    merge(v, Best{__shfl_xor_sync(0xffffffffu, v.z1, o), __shfl_xor_sync(0xffffffffu, v.z2, o), __shfl_xor_sync(0xffffffffu, v.id, o),
+                  __shfl_xor_sync(0xffffffffu, v.l, o)});
   return v;
 }
-__device__ Best block_best(Shared* s, Best v) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_best(v);
-  __syncthreads();
-  if (lane == 0) s->warp_best[warp] = v;
-  __syncthreads();
-  return warp_best(lane < kWarps ? s->warp_best[lane] : Best{-INFINITY, -INFINITY, 0x7FFFFFFF});
-}
+constexpr int kNoId = 0x7FFFFFFF;
 
-// Two best values that a thread has seen, with their tokens.
+// The two best values that a thread has seen, with their tokens.
 struct Two {
   float z[2], l[2];
   int id[2];
 };
+__device__ __forceinline__ Two no_two() { return Two{{-INFINITY, -INFINITY}, {0.f, 0.f}, {kNoId, kNoId}}; }
 __device__ __forceinline__ void fold(Two& t, float z, float l, int id) {
-  if (z > t.z[0] || (z == t.z[0] && id < t.id[0])) {
+  if (ahead(z, id, t.z[0], t.id[0])) {
     t.z[1] = t.z[0], t.l[1] = t.l[0], t.id[1] = t.id[0];
     t.z[0] = z, t.l[0] = l, t.id[0] = id;
-  } else if (z > t.z[1] || (z == t.z[1] && id < t.id[1])) {
+  } else if (ahead(z, id, t.z[1], t.id[1])) {
     t.z[1] = z, t.l[1] = l, t.id[1] = id;
   }
 }
-
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
+struct Key {  // of the row's noise
+  uint32_t pos, seq, k0, k1;
+};
+__device__ __forceinline__ uint4 noise4(const Key& k, int id) {
+  return philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, k.pos, k.seq, 0u), k.k0, k.k1);
+}
 // The draw's value of a token in 64 bits.
-__device__ double value64(const Params& p, const Row& w, float l, int id, uint32_t pos, uint32_t seq) {
-  const uint4 n = philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, pos, seq, 0u), p.k0, p.k1);
-  const double u = (static_cast<double>(word_of(n, id & 3) >> 9) + 0.5) * (1.0 / 8388608.0);
+__device__ __noinline__ double value64(const Row& w, const Key& k, float l, int id) {
+  const uint32_t word = word_of(noise4(k, id), id & 3);
+  const double u = (static_cast<double>(word >> 9) + 0.5) * (1.0 / 8388608.0);
   return (static_cast<double>(l) - static_cast<double>(w.top)) * static_cast<double>(w.r) - log(-log(u));
 }
+// Values within the rounding of the best, fp32's and the noise's.
+__device__ __forceinline__ float near_best(float z) { return z - (2e-5f + 1e-6f * fabsf(z)); }
 
-// From the threads' two best values to the row's token: the first CTA (of the
-// cluster, or by itself with `alone`) writes it.
-__device__ void finish(Shared* s, const Params& p, const Row& w, const Two& t, bool greedy, bool alone, int row, uint32_t pos,
-                       uint32_t seq) {
-  Best b = {t.z[0], t.z[1], t.id[0]};
-  b = block_best(s, b);
-  if (!alone) {
-    if (threadIdx.x < w.ctas) to_peer(&s->peer_best[w.rank], threadIdx.x, b);
-    cluster_sync_all();
-    b = s->peer_best[0];
-    for (int q = 1; q < w.ctas; ++q) merge(b, s->peer_best[q]);
-  }
-  // values within rounding of the best, fp32's and the noise's, are compared in fp64
-  const float near = b.z1 - (2e-5f + 1e-6f * fabsf(b.z1));
-  if (!greedy) {
+// The best of a warp's values of which several are near the best: these in fp64.
+__device__ Best near_of_warp(const Row& w, const Key& key, const Best& mine, bool near) {
+  const double z = near ? value64(w, key, mine.l, mine.id) : -INFINITY;
+  __syncwarp();
+  double best = z;
+  int id = near ? mine.id : kNoId;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (t.z[j] >= near) {
-        const uint32_t at = alone ? atomicAdd(&s->cand_n, 1u) : peer_add(&s->cand_n, 0, 1u);
-        if (at < kCand) {
-          if (alone) {
-            s->cand_l[at] = t.l[j];
-            s->cand_id[at] = t.id[j];
-          } else {
-            to_peer(&s->cand_l[at], 0, t.l[j]);
-            to_peer(&s->cand_id[at], 0, t.id[j]);
-          }
-        }
-      }
-    if (alone)
-      __syncthreads();
-    else
-      cluster_sync_all();
+  for (int o = 16; o; o >>= 1) {
+    const double u = __shfl_xor_sync(0xffffffffu, best, o);
+    const int i = __shfl_xor_sync(0xffffffffu, id, o);
+    if (u > best || (u == best && i < id)) best = u, id = i;
   }
-  if (w.rank != 0) return;
-  float gap = b.z1 - b.z2;
-  int id = b.id;
-  const int n = greedy ? 1 : static_cast<int>(s->cand_n);
-  if (n > 1 && n <= kCand) {
-    double z = -INFINITY;
-    int mine = 0x7FFFFFFF;
-    if (threadIdx.x < n) {
-      mine = s->cand_id[threadIdx.x];
-      z = value64(p, w, s->cand_l[threadIdx.x], mine, pos, seq);
-    }
-    // by one thread over the few of them
-    double* zs = reinterpret_cast<double*>(s->list);
-    __syncthreads();
-    if (threadIdx.x < n) zs[threadIdx.x] = z;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double z1 = -INFINITY, z2 = -INFINITY;
-      id = 0x7FFFFFFF;
-      for (int i = 0; i < n; ++i) {
-        if (zs[i] > z1 || (zs[i] == z1 && s->cand_id[i] < id)) {
-          z2 = z1;
-          z1 = zs[i];
-          id = s->cand_id[i];
-        } else if (zs[i] > z2) {
-          z2 = zs[i];
-        }
+  // the second best: another lane's, or the best one's own second
+  float second = near ? (mine.id == id ? mine.z2 : static_cast<float>(z)) : mine.z1;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, o));
+  return Best{static_cast<float>(best), second, id, 0.f};
+}
+
+// The block's best of its threads' two best values, near ones compared in fp64.
+template <int kCtas>
+__device__ Best block_best(Shared<kCtas>* s, const Row& w, const Key& key, const Two& t, bool exact) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncwarp();
+  Best b = warp_best(Best{t.z[0], t.z[1], t.id[0], t.l[0]});
+  if (lane == 0) s->warp_best[warp] = b;
+  if (threadIdx.x == 0) s->near_n = 0;
+  __syncthreads();
+  b = warp_best(lane < kWarps ? s->warp_best[lane] : Best{-INFINITY, -INFINITY, kNoId, 0.f});
+  // the same for all threads
+  if (exact || b.z1 == -INFINITY || !(b.z2 >= near_best(b.z1))) return b;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (t.z[j] >= near_best(b.z1)) {
+      const uint32_t at = atomicAdd(&s->near_n, 1u);
+      if (at < kThreads) {
+        s->near_l[at] = t.l[j];
+        s->near_id[at] = t.id[j];
       }
-      gap = static_cast<float>(z1 - z2);
+    }
+  __syncthreads();
+  const int n = min(s->near_n, static_cast<uint32_t>(kThreads));
+  if (static_cast<int>(threadIdx.x) < n) s->near_z[threadIdx.x] = value64(w, key, s->near_l[threadIdx.x], s->near_id[threadIdx.x]);
+  __syncthreads();
+  double z1 = -INFINITY, z2 = -INFINITY;
+  int at = 0;
+  for (int i = 0; i < n; ++i) {
+    const double z = s->near_z[i];
+    if (i == 0 || z > z1 || (z == z1 && s->near_id[i] < s->near_id[at])) {
+      z2 = z1;
+      z1 = z;
+      at = i;
+    } else if (z > z2) {
+      z2 = z;
     }
   }
-  if (threadIdx.x == 0 && GLANCE_IN_BOUNDS(row, p.M)) {
-    p.tokens[row] = id;
-    if (p.gap) p.gap[row] = gap;
+  return Best{static_cast<float>(z1), static_cast<float>(z2), s->near_id[at], s->near_l[at]};
+}
+
+__device__ __forceinline__ void write_row(const Params& p, int row, const Best& b) {
+  if (GLANCE_IN_BOUNDS(row, p.M)) {
+    p.tokens[row] = b.id;
+    if (p.gap) p.gap[row] = fmaxf(b.z1 - b.z2, 0.f);
   }
 }
 
-// The number of the last token that a prefix keeps, and the weight up to it:
-// the bin's tokens (from `floor` on) are divided until they fit the list, and
-// that is sorted.
-template <typename T>
-__device__ void refine(Shared* s, const unsigned char* s_row, const Row& w, const Border& first, uint64_t floor, uint32_t want,
-                       double share, uint64_t* cut, double* mass) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// From every CTA's best to the row's token, by the first CTA.
+template <int kCtas>
+__device__ void finish(Shared<kCtas>* s, const Params& p, const Row& w, const Key& key, const Two& t, bool exact, int row) {
+  Best b = block_best(s, w, key, t, exact);
+  if (kCtas == 1) {
+    if (threadIdx.x == 0) write_row(p, row, b);
+    return;
+  }
+  if (threadIdx.x == 0) to_peer<kCtas>(&s->peer_best[w.rank], 0, b);
+  sync_row<kCtas>();
+  if (w.rank != 0 || threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  const Best mine = lane < kCtas ? s->peer_best[lane] : Best{-INFINITY, -INFINITY, kNoId, 0.f};
+  b = warp_best(mine);
+  const bool near = mine.z1 >= near_best(b.z1);
+  if (!exact && __popc(__ballot_sync(0xffffffffu, near)) > 1) b = near_of_warp(w, key, mine, near);
+  if (lane == 0) write_row(p, row, b);
+}
+
+// The first CTA draws from its list of n tokens: the first `want` of them (0:
+// all), of these `share` of the weight (of mass_all, or of theirs if it is 0).
+template <int kCtas>
+__device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, const Key& key, int n, uint32_t want, bool all_p, Mass share,
+                               Mass mass_all, int row) {
+  const int t = threadIdx.x;
+  const int kept = want ? min(static_cast<int>(want), n) : n;
+  Two two = no_two();
+  const auto draw = [&](uint64_t number) {
+    const int id = id_of(number);
+    const float l = logit_of(number);
+    fold(two, (l - w.top) * w.r + gumbel_of(word_of(noise4(key, id), id & 3)), l, id);
+  };
+  if (n <= 32) {  // one warp's
+    if (t >= 32) return;
+    const uint64_t number = sort_warp(t < n ? s->list[t] : 0ull, t);
+    const Mass m = !all_p && t < kept ? weight_of(w, logit_of(number)) : 0ull;
+    const Mass upto = scan_add(m, t), all = mass_all ? mass_all : __shfl_sync(0xffffffffu, upto, 31);
+    if (t < kept && (all_p || upto - m < part_of(all, share))) draw(number);
+    __syncwarp();
+    const Best mine = {two.z[0], -INFINITY, two.id[0], two.l[0]};
+    Best b = warp_best(mine);
+    const bool near = mine.z1 >= near_best(b.z1);
+    if (__popc(__ballot_sync(0xffffffffu, near)) > 1) b = near_of_warp(w, key, mine, near);
+    if (t == 0) write_row(p, row, b);
+    return;
+  }
+  sort_list(s->list, n);
+  Mass before[kPer], upto[kPer], target = ~0ull;
+  if (!all_p) {
+    list_masses(s, w, kept, 0, before, upto);
+    if (mass_all == 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (kPer * t + j == kept - 1) s->cut.mass = upto[j];
+      __syncthreads();
+      mass_all = s->cut.mass;
+    }
+    target = part_of(mass_all, share);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = kPer * t + j;
+    if (e < kept && (all_p || before[j] < target)) draw(s->list[e]);
+  }
+  const Best b = block_best(s, w, key, two, false);
+  if (t == 0) write_row(p, row, b);
+}
+
+// The last token that a prefix keeps, and the weight up to it: the tokens of the
+// border's bin (from `floor` on) are divided until they fit the list, and that is
+// sorted. turn: which of the list's counters.
+template <typename T, int kCtas, bool kGlobal>
+__device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint64_t floor, uint32_t want, Mass share, int turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
   Border b = first;
   const int bin = b.bin;
+  const Mass all = b.mass_all;
   uint64_t lo = floor, hi = ~0ull;
-  const auto inside = [&](float l, uint64_t number) {
-    int at;
-    float d;
-    return number >= lo && number <= hi && place(w, l, at, d) && at == bin;
-  };
+  const float least = least_of_bin(w, bin);
   // the numbers differ and the range shrinks to the tokens' own each time: 50
   // bits are through after five divisions by 2^10 or more
   for (int level = 0; level < 8 && b.count_in > kList; ++level) {
-    uint64_t least = ~0ull, most = 0;
-    each<T>(s_row, w, [&](float l, int id) {
-      const uint64_t number = number_of(l, id);
-      if (inside(l, number)) {
-        least = min(least, number);
-        most = max(most, number);
+    uint64_t least_n = ~0ull, most_n = 0;
+    each<T, kGlobal>(w, least, [&](float l, int id) {
+      int at;
+      float y;
+      if (l >= least && place(w, l, at, y) && at == bin) {
+        const uint64_t number = number_of(l, id);
+        if (number >= lo && number <= hi) {
+          least_n = number < least_n ? number : least_n;
+          most_n = number > most_n ? number : most_n;
+        }
       }
     });
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      const uint64_t a = __shfl_xor_sync(0xffffffffu, least_n, o), c = __shfl_xor_sync(0xffffffffu, most_n, o);
+      least_n = a < least_n ? a : least_n;
+      most_n = c > most_n ? c : most_n;
     }
     if (lane == 0) {
-      s->warp_lo[warp] = least;
-      s->warp_hi[warp] = most;
+      s->warp_lo[warp] = least_n;
+      s->warp_hi[warp] = most_n;
     }
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) {
-      least = min(least, s->warp_lo[i]);
-      most = max(most, s->warp_hi[i]);
+      least_n = s->warp_lo[i] < least_n ? s->warp_lo[i] : least_n;
+      most_n = s->warp_hi[i] > most_n ? s->warp_hi[i] : most_n;
     }
-    if (threadIdx.x < w.ctas) {
-      to_peer(&s->peer_lo[w.rank], threadIdx.x, least);
-      to_peer(&s->peer_hi[w.rank], threadIdx.x, most);
+    if (t < kCtas) {
+      to_peer<kCtas>(&s->peer_lo[w.rank], t, least_n);
+      to_peer<kCtas>(&s->peer_hi[w.rank], t, most_n);
     }
+    sync_row<kCtas>();  // also: the others have read this CTA's histogram
     clear_hist(s);
-    cluster_sync_all();
-    for (int q = 0; q < w.ctas; ++q) {
-      least = min(least, s->peer_lo[q]);
-      most = max(most, s->peer_hi[q]);
+    lo = s->peer_lo[0];
+    hi = s->peer_hi[0];
+    for (int q = 1; q < kCtas; ++q) {
+      lo = s->peer_lo[q] < lo ? s->peer_lo[q] : lo;
+      hi = s->peer_hi[q] > hi ? s->peer_hi[q] : hi;
     }
-    lo = least;
-    hi = most;
-    int shift = 0;
-    while ((hi - lo) >> shift >= kBins) ++shift;
-    each<T>(s_row, w, [&](float l, int id) {
-      const uint64_t number = number_of(l, id);
+    const int shift = max(0, 64 - __clzll(hi - lo) - 11);  // the range in 2048 steps at most
+    each<T, kGlobal>(w, least, [&](float l, int id) {
       int at;
-      float d;
-      if (number >= lo && number <= hi && place(w, l, at, d) && at == bin) {
-        const int sub = static_cast<int>((hi - number) >> shift);
-        atomicAdd(&s->hist.count[sub], 1u);
-        atomicAdd(&s->hist.d[sub], __float2uint_rn(d * kUnit));
+      float y;
+      if (l >= least && place(w, l, at, y) && at == bin) {
+        const uint64_t number = number_of(l, id);
+        if (number >= lo && number <= hi) add_hist(s, static_cast<int>((hi - number) >> shift), y, !want);
       }
     });
-    const double all = b.mass_all;
-    b = find_border(s, w, want, share, all, bin, b.count_before, b.mass_before);
-    if (b.bin < 0) {  // the sum of the weights came out a rounding short of its share: the range's last token
-      *cut = lo;
-      *mass = all;
-      return;
-    }
+    b = find_border(s, w, want, share, all, 0.f, bin, b.count_before, b.mass_before);
+    // the sum of the weights came out a rounding short of its share: the range's last token
+    if (b.bin < 0) return Cut{lo, all};
     hi -= static_cast<uint64_t>(b.bin) << shift;
-    const uint64_t least_of_bin = hi - ((1ull << shift) - 1);
-    if (least_of_bin > lo) lo = least_of_bin;
+    const uint64_t last = hi - ((1ull << shift) - 1);
+    lo = last > lo ? last : lo;
   }
-  gather<T>(s, s_row, w, [&](float l, uint64_t number) { return inside(l, number); });
+  sync_row<kCtas>();  // the others have read this CTA's histogram
+  const uint32_t found = gather<T, kCtas, kGlobal>(s, w, turn, least, [&](float l, uint64_t number) {
+    int at;
+    float y;
+    return number >= lo && number <= hi && place(w, l, at, y) && at == bin;
+  });
   if (w.rank == 0) {
-    const int n = min(static_cast<int>(s->list_n), kList);
-    __syncthreads();
-    if (threadIdx.x == 0) s->list_n = 0;
-    sort_list(s, n);
-    double before[kList / kThreads], upto[kList / kThreads];
+    const int n = min(found, static_cast<uint32_t>(kList));
+    sort_list(s->list, n);
+    Mass before[kPer], upto[kPer];
     list_masses(s, w, n, b.mass_before, before, upto);
-    const double target = share * b.mass_all;
-    if (threadIdx.x == 0) {  // unless a token is found: the last one
-      s->cut = s->list[n - 1];
-      s->cut_mass = b.mass_all;
-    }
+    const Mass target = part_of(all, share);
+    if (t == 0) s->cut = Cut{s->list[max(n - 1, 0)], all};  // unless a token is found: the last one
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kList / kThreads; ++j) {
-      const int i = threadIdx.x * (kList / kThreads) + j;
-      if (i < n && (want ? b.count_before + i + 1 == want : before[j] < target && upto[j] >= target)) {
-        s->cut = s->list[i];
-        s->cut_mass = upto[j];
-      }
+    for (int j = 0; j < kPer; ++j) {
+      const int e = kPer * t + j;
+      if (e < n && (want ? b.count_before + e + 1 == want : before[j] < target && upto[j] >= target)) s->cut = Cut{s->list[e], upto[j]};
     }
     __syncthreads();
-    if (threadIdx.x < w.ctas && threadIdx.x > 0) {
-      to_peer(&s->cut, threadIdx.x, s->cut);
-      to_peer(&s->cut_mass, threadIdx.x, s->cut_mass);
-    }
+    if (t > 0 && t < kCtas) to_peer<kCtas>(&s->cut, t, s->cut);
   }
-  cluster_sync_all();
-  *cut = s->cut;
-  *mass = s->cut_mass;
+  sync_row<kCtas>();
+  return s->cut;
 }
 
-// Grid: x = row * cluster size + rank.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p, const int ctas) {
+// ------------------------------------------------------------------ the kernel
+
+// Grid: x = row * kCtas + rank. One CTA: the row stays in global memory; more:
+// in theirs.
+template <typename T, int kCtas>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
+  constexpr bool kGlobal = kCtas == 1;
   extern __shared__ __align__(16) unsigned char smem[];
-  Shared* s = reinterpret_cast<Shared*>(smem);
-  unsigned char* s_row = smem + (sizeof(Shared) + 15) / 16 * 16;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = static_cast<int>(blockIdx.x) / ctas;
+  Shared<kCtas>* s = reinterpret_cast<Shared<kCtas>*>(smem);
+  unsigned char* s_row = smem + (sizeof(Shared<kCtas>) + 15) / 16 * 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
+  const int row = static_cast<int>(blockIdx.x) / kCtas;
   Row w;
-  w.ctas = ctas;
-  w.rank = static_cast<int>(cluster_ctarank());
+  w.rank = kCtas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   w.first = w.rank * p.slice;
   w.n = max(0, min(p.slice, p.V - w.first));
+  if (kCtas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait_prior();
   pdl_launch_dependents();
   const float temperature = p.temperature ? __ldg(p.temperature + row) : 1.f;
   const int k = p.top_k ? __ldg(p.top_k + row) : 0;
   const float top_p = p.top_p ? __ldg(p.top_p + row) : 1.f, min_p = p.min_p ? __ldg(p.min_p + row) : 0.f;
-  const uint32_t pos = static_cast<uint32_t>(__ldg(p.position + row)), seq = p.seq ? static_cast<uint32_t>(__ldg(p.seq + row)) : 0u;
+  const Key key = {static_cast<uint32_t>(__ldg(p.position + row)), p.seq ? static_cast<uint32_t>(__ldg(p.seq + row)) : 0u, p.k0, p.k1};
   const bool greedy = temperature == 0.f;
   w.r = greedy ? 1.f : 1.f / temperature;
-  if (threadIdx.x == 0) {
-    s->list_n = s->cand_n = 0;
-    s->log_min_p = min_p > 0.f ? log(static_cast<double>(min_p)) : 0.0;
-  }
-  // the row's part into shared memory, its largest logit on the way
-  constexpr int kN = 16 / static_cast<int>(sizeof(T));
-  const char* src = p.logits + row * p.stride + static_cast<long long>(w.first) * static_cast<int>(sizeof(T));
-  float top = -INFINITY;
-  int done = 0;
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    const int vecs = w.n / kN;
-    done = vecs * kN;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < vecs; i += kThreads) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-      *reinterpret_cast<uint4*>(s_row + 16 * i) = v;
-      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  if (t < 3) s->list_n[t] = 0;
+  const unsigned char* src =
+      reinterpret_cast<const unsigned char*>(p.logits) + row * p.stride + static_cast<long long>(w.first) * static_cast<int>(sizeof(T));
+  w.vec = reinterpret_cast<uintptr_t>(src) % (4 * sizeof(T)) == 0;
+  float top = -INFINITY;  // of this thread's tokens
+  w.own = 0.f;
+  w.at = src;
+  each4<T, true, sizeof(T) == 4 ? 4 : 8>(
+      w, -INFINITY,
+      [&](const float(&l)[4], int id) {
+        top = max_nan(top, max_nan(max_nan(l[0], l[1]), max_nan(l[2], l[3])));
+        if (!kGlobal && id - w.first < w.n) pack4(reinterpret_cast<T*>(s_row) + (id - w.first), l);
+      },
+      [] {});
+  if (!kGlobal) w.at = s_row;
+  w.own = top;
+  // 512 maxima in all, of kCtas threads each, to every CTA
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (sizeof(T) == 4)
-          top = max_nan(top, __uint_as_float(q[j]));
-        else
-          top = max_nan(top, max_nan(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xFFFF0000u)));
-      }
-    }
-  }
-#pragma unroll 4
-  for (int i = done + threadIdx.x; i < w.n; i += kThreads) {
-    const T v = reinterpret_cast<const T*>(src)[i];
-    reinterpret_cast<T*>(s_row)[i] = v;
-    top = max_nan(top, static_cast<float>(v));
-  }
-  if (threadIdx.x < 4) reinterpret_cast<T*>(s_row)[w.n + threadIdx.x] = static_cast<T>(-INFINITY);
+  for (int o = 1; o < kCtas; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (kCtas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all have begun
+  to_peer<kCtas>(&s->group[(w.rank * kThreads + t) / kCtas], t % kCtas, top);
+  if (t == 0) s->log_min_p = min_p > 0.f && !greedy ? log(static_cast<double>(min_p)) : 0.0;
+  sync_row<kCtas>();
+  const float group = s->group[t];
+  top = group;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s->warp_f[warp] = top;
   __syncthreads();
+#pragma unroll
   for (int i = 0; i < kWarps; ++i) top = max_nan(top, s->warp_f[i]);
-  // (the barrier of the cluster that every path has after this one keeps the CTAs together)
-  cluster_sync_all();  // the other CTAs have begun: their shared memory may be written
-  if (threadIdx.x < ctas) to_peer(&s->peer_max[w.rank], threadIdx.x, top);
-  cluster_sync_all();
-  for (int q = 0; q < ctas; ++q) top = max_nan(top, s->peer_max[q]);
   w.top = top;
   const bool bad_row = !(top > -INFINITY && top < INFINITY);
   const bool bad_param = !(temperature >= 0.f && w.r < INFINITY && w.r > 0.f) || top_p != top_p || min_p != min_p;
   if (bad_row || bad_param) {
-    if (threadIdx.x == 0 && w.rank == 0 && GLANCE_IN_BOUNDS(row, p.M)) {
+    if (t == 0 && w.rank == 0 && GLANCE_IN_BOUNDS(row, p.M)) {
       p.tokens[row] = -1;
       if (p.gap) p.gap[row] = NAN;
       report(bad_row ? GLANCE_DEV_NONFINITE_LOGITS : GLANCE_DEV_BAD_SAMPLING);
@@ -685,139 +956,168 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p, con
   // the least logit with (l - top) r >= ln min_p, in fp64
   w.min_l = -INFINITY;
   if (min_p > 0.f && !greedy) {
-    if (threadIdx.x == 0) {
-      const double lg = fmin(s->log_min_p, 0.0), r = w.r, t = top;
-      float x = static_cast<float>(t + lg / r);
-      x = fminf(x, top);
-      for (int i = 0; i < 4 && x > -INFINITY && (static_cast<double>(x) - t) * r >= lg; ++i) x = nextafterf(x, -INFINITY);
-      for (int i = 0; i < 8 && (static_cast<double>(x) - t) * r < lg; ++i) x = nextafterf(x, INFINITY);
+    if (t == 0) {
+      const double lg = fmin(s->log_min_p, 0.0), r = w.r, m = top;
+      float x = fminf(static_cast<float>(m + lg / r), top);
+      for (int i = 0; i < 4 && x > -INFINITY && (static_cast<double>(x) - m) * r >= lg; ++i) x = nextafterf(x, -INFINITY);
+      for (int i = 0; i < 8 && (static_cast<double>(x) - m) * r < lg; ++i) x = nextafterf(x, INFINITY);
       s->min_l = x;
     }
     __syncthreads();
     w.min_l = s->min_l;
   }
   const uint32_t want = k > 0 && k < p.V ? k : 0u;
-  const double share = top_p < 1.f ? static_cast<double>(fmaxf(top_p, 0.f)) : 1.0;
-  uint64_t cut = 0;  // the last number that is kept
-  if (!greedy && (want || share < 1.0)) {
-    clear_hist(s);
-    __syncthreads();
-    each<T>(s_row, w, [&](float l, int) {
-      int bin;
-      float d;
-      if (place(w, l, bin, d)) {
-        atomicAdd(&s->hist.count[bin], 1u);
-        atomicAdd(&s->hist.d[bin], __float2uint_rn(d * kUnit));
-      }
-    });
-    // share 0: the first token alone, which any positive share has
-    const double least = share > 0 ? share : 1e-300;
-    Border b = find_border(s, w, want, want ? 1.0 : least, 0, -1, 0u, 0);
-    const uint32_t upto = b.bin < 0 ? 0xFFFFFFFFu : b.count_before + b.count_in;
-    if (upto <= kList) {
-      // all that may be kept fits the list: the first CTA draws from it
-      gather<T>(s, s_row, w, [&](float l, uint64_t) {
-        int bin;
-        float d;
-        return place(w, l, bin, d) && bin <= b.bin;
-      });
-      if (w.rank != 0) return;
-      const int n = min(static_cast<int>(s->list_n), kList);
-      sort_list(s, n);
-      double before[kList / kThreads], upto_mass[kList / kThreads];
-      list_masses(s, w, n, 0, before, upto_mass);
-      const int kept = want ? min(static_cast<int>(want), n) : n;
-      // the weight of the first k, or of all
-      if (want && static_cast<int>(threadIdx.x) == (kept - 1) / (kList / kThreads)) {
-#pragma unroll
-        for (int j = 0; j < kList / kThreads; ++j)
-          if ((kept - 1) % (kList / kThreads) == j) s->cut_mass = upto_mass[j];
-      }
-      __syncthreads();
-      const double target = least * (want ? s->cut_mass : b.mass_all);
-      Two t = {{-INFINITY, -INFINITY}, {0.f, 0.f}, {0x7FFFFFFF, 0x7FFFFFFF}};
-#pragma unroll
-      for (int j = 0; j < kList / kThreads; ++j) {
-        const int i = threadIdx.x * (kList / kThreads) + j;
-        if (i < kept && (share >= 1.0 || before[j] < target)) {
-          const uint64_t number = s->list[i];
-          const int id = id_of(number);
-          const float l = logit_of(number);
-          const uint4 v = philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, pos, seq, 0u), p.k0, p.k1);
-          fold(t, fmaf(l - w.top, w.r, gumbel_of(word_of(v, id & 3))), l, id);
+  // top_p in units of 2^-64 (all_p: off)
+  const bool all_p = !(top_p < 1.f);
+  const Mass share = all_p ? 0 : __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p32f * 0x1p32f);
+  uint64_t cut = 0;
+  if (!greedy && (want || !all_p)) {
+    uint32_t upto = ~0u;
+    Border b = {};
+    b.bin = -1;
+    if (want && want <= kGroupK) {
+      // k of the maxima, tokens all, are at or above a place between them that
+      // is searched for to 2^-10 of the histogram's range
+      float lo = top - kRange / w.r, hi = top;
+      if (__syncthreads_count(group >= lo) < static_cast<int>(want)) {
+        lo = -INFINITY;
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 10; ++i) {
+          const float mid = 0.5f * (lo + hi);
+          if (__syncthreads_count(group >= mid) >= static_cast<int>(want))
+            lo = mid;
+          else
+            hi = mid;
         }
       }
-      finish(s, p, w, t, false, true, row, pos, seq);
+      const float least = fmaxf(lo, w.min_l);
+      upto = gather<T, kCtas, kGlobal>(s, w, 0, least, [&](float l, uint64_t) { return __fmul_rn(w.top - l, w.r) < kRange; });
+    }
+    if (upto > kList) {
+      // Tokens with (max - l) r above `skip` need no bin: all of them together
+      // weigh less than (1 - p) / 2, and the border is not among them.
+      const float skip = want ? kRange : fminf(kRange, logf(2.f * p.V / (1.f - fmaxf(top_p, 0.f))));
+      float loose = 0.f;
+      clear_hist(s);
+      each<T, kGlobal>(w, w.min_l, [&](float l, int) {
+        const float x = __fmul_rn(w.top - l, w.r);
+        if (x < skip) {
+          int bin;
+          float y;
+          if (place(w, l, bin, y)) add_hist(s, bin, y, !want);
+        } else if (!want && l >= w.min_l) {
+          loose += ex2_approx(-kLog2e * x);
+        }
+      });
+      b = find_border(s, w, want, share, 0, loose, -1, 0u, 0);
+      upto = ~0u;
+      if (b.bin >= 0 && b.count_before + b.count_in <= kList) {
+        sync_row<kCtas>();  // the others have read this CTA's histogram
+        upto = gather<T, kCtas, kGlobal>(s, w, 1, least_of_bin(w, b.bin), [&](float l, uint64_t) {
+          int bin;
+          float y;
+          return __fmul_rn(w.top - l, w.r) < skip && place(w, l, bin, y) && bin <= b.bin;
+        });
+      }
+    }
+    if (upto <= kList) {
+      // all that may be kept is in the first CTA's list
+      __syncwarp();
+      if (kCtas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      if (w.rank == 0) {
+        draw_from_list(s, p, w, key, static_cast<int>(upto), want, all_p, share, want ? 0 : b.mass_all, row);
+        // the others have read its counter
+        __syncwarp();
+        if (kCtas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      }
       return;
     }
     if (b.bin >= 0) {
-      double mass = b.mass_all;
-      uint64_t last;
-      refine<T>(s, s_row, w, b, 0, want, want ? 1.0 : least, &last, &mass);
-      cut = last;
-      if (want && share < 1.0) {
+      cut = refine<T, kCtas, kGlobal>(s, w, b, 0, want, share, 1).number;
+      if (want && !all_p) {
         // the first k are known: the share of their weight ends at or before their last
         clear_hist(s);
-        __syncthreads();
-        each<T>(s_row, w, [&](float l, int id) {
+        each<T, kGlobal>(w, logit_of(cut), [&](float l, int id) {
           int bin;
-          float d;
-          if (place(w, l, bin, d) && number_of(l, id) >= cut) {
-            atomicAdd(&s->hist.count[bin], 1u);
-            atomicAdd(&s->hist.d[bin], __float2uint_rn(d * kUnit));
-          }
+          float y;
+          if (place(w, l, bin, y) && number_of(l, id) >= cut) add_hist(s, bin, y, true);
         });
-        b = find_border(s, w, 0u, least, mass, -1, 0u, 0);
+        b = find_border(s, w, 0u, share, 0, 0.f, -1, 0u, 0);
         if (b.bin >= 0) {
-          refine<T>(s, s_row, w, b, cut, 0u, least, &last, &mass);
-          if (last > cut) cut = last;
+          const Cut c = refine<T, kCtas, kGlobal>(s, w, b, cut, 0u, share, 2);
+          if (c.number > cut) cut = c.number;
         }
       }
-    } else if (want && share < 1.0) {
+    } else if (want && !all_p) {
       // fewer than k tokens in reach: the share is of all of them
-      b = find_border(s, w, 0u, least, 0, -1, 0u, 0);
-      if (b.bin >= 0) {
-        double mass;
-        refine<T>(s, s_row, w, b, 0, 0u, least, &cut, &mass);
-      }
+      sync_row<kCtas>();  // the others have read the sums of the search before
+      clear_hist(s);
+      each<T, kGlobal>(w, w.min_l, [&](float l, int) {
+        int bin;
+        float y;
+        if (place(w, l, bin, y)) add_hist(s, bin, y, true);
+      });
+      b = find_border(s, w, 0u, share, 0, 0.f, -1, 0u, 0);
+      if (b.bin >= 0) cut = refine<T, kCtas, kGlobal>(s, w, b, 0, 0u, share, 2).number;
     }
   }
   // every CTA looks at its part of the row
-  Two t = {{-INFINITY, -INFINITY}, {0.f, 0.f}, {0x7FFFFFFF, 0x7FFFFFFF}};
+  Two two = no_two();
   if (greedy) {
-    each<T>(s_row, w, [&](float l, int id) {
-      if (l > -INFINITY) fold(t, l, l, id);
+    // two tokens are no smaller than the second largest of the parts' maxima
+    float second = group == top ? -INFINITY : group;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, o));
+    if (lane == 0) s->warp_second[warp] = second;
+    if (__syncthreads_count(group == top) > 1) second = top;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) second = fmaxf(second, s->warp_second[i]);
+    each_of_few<T, kCtas, kGlobal>(s, w, second, [&](float l, int id) {
+      if (l > -INFINITY) fold(two, l, l, id);
     });
   } else {
-    for (int i = 4 * static_cast<int>(threadIdx.x); i < w.n; i += 4 * kThreads) {
-      float l[4];
-      Row4<T>::load(s_row, i, l);
-      const int id = w.first + i;
-      bool any[4], some = false;
+    const float cut_l = cut ? logit_of(cut) : -INFINITY;
+    const float least = fmaxf(fmaxf(cut_l, w.min_l), -3.4028234e38f);
+    const int last = cut ? id_of(cut) : kMaxV;  // of the tokens with the cut's logit
+    float second = -INFINITY;  // two of the warp's values are no less
+    float reach = least;       // tokens below cannot come to it: the noise is below 16.7
+    each4<T, kGlobal, 4>(
+        w, least,
+        [&](const float(&l)[4], int id) {
+          const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+          if (!(most >= reach)) return;
+          const uint4 v = noise4(key, id);
+          // x + g >= second asks for 1 - u <= e^(x - second); with the largest x of the
+          // four, as a bound of the noise's word, 1 - u = (2^23 - 1/2 - (word >> 9)) 2^-23
+          const float rest = ex2_approx(((most - w.top) * w.r - second) * kLog2e) * (4294967296.f * 1.0001f);
+          if (!(static_cast<float>(max(max(v.x, v.y), max(v.z, v.w))) >= 4294965248.f - rest)) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // the noise is below 16.7: a token that cannot reach this thread's second best is passed over
-        any[j] = l[j] > -INFINITY && l[j] >= w.min_l && fmaf(l[j] - w.top, w.r, 16.7f) >= t.z[1] &&
-                 (!cut || number_of(l[j], id + j) >= cut);
-        some |= any[j];
-      }
-      if (!some) continue;
-      const uint4 v = philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, pos, seq, 0u), p.k0, p.k1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (any[j]) fold(t, fmaf(l[j] - w.top, w.r, gumbel_of(word_of(v, j))), l[j], id + j);
-    }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word = word_of(v, j);
+            if (l[j] >= least && static_cast<float>(word) >= 4294965248.f - rest && (l[j] != cut_l || id + j <= last))
+              fold(two, (l[j] - w.top) * w.r + gumbel_of(word), l[j], id + j);
+          }
+        },
+        [&] {
+          const uint32_t z0 = ord_key(two.z[0]), z1 = ord_key(two.z[1]);
+          const uint32_t best = __reduce_max_sync(0xffffffffu, z0);
+          const unsigned who = __ballot_sync(0xffffffffu, z0 == best);
+          second = of_key(__reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? z1 : z0));
+          reach = fmaxf(least, w.top + (second - 16.8f) / w.r - 1e-5f * fabsf(w.top));
+        });
   }
-  finish(s, p, w, t, greedy, false, row, pos, seq);
+  finish(s, p, w, key, two, greedy, row);
 }
 
-// CTAs to a row: as few as hold it with two of them on an SM, more while the
-// rows alone would leave SMs idle and each keeps 4096 tokens.
-int cluster_size(int M, int V, int esize) {
-  int c = 1;
-  while (c < kMaxCluster && ((V + c - 1) / c > kMaxSlice || (V + c - 1) / c * esize > 77 * 1024)) c <<= 1;
-  while (c < kMaxCluster && static_cast<int64_t>(M) * c * 2 <= glance::num_sms() && V / (2 * c) >= 4096) c <<= 1;
-  return c;
+constexpr int kRowsAlone = 96;  // rows beyond which a row has one CTA
+
+// CTAs to a row: 1, or a cluster of 8 or 16 that holds it, while rows alone
+// would leave SMs idle.
+int cluster_size(int M, int V) {
+  if (M > kRowsAlone || V < 2048) return 1;
+  if (M * 16 <= glance::num_sms() && V >= 16 * 2048) return 16;
+  return 8;
 }
 
 // Clusters of 16 are beyond the portable size: allowed once per kernel and device.
@@ -840,15 +1140,16 @@ cudaError_t allow_large_clusters(const void* f) {
   return e;
 }
 
-template <typename T>
-glance_status launch(const char* who, const Params& p, int ctas, cudaStream_t stream) {
-  const void* f = reinterpret_cast<const void*>(sample_kernel<T>);
-  const int bytes = static_cast<int>((sizeof(Shared) + 15) / 16 * 16 + (static_cast<size_t>(p.slice) + 8) * sizeof(T));
+template <typename T, int kCtas>
+glance_status launch(const char* who, Params p, cudaStream_t stream) {
+  const void* f = reinterpret_cast<const void*>(sample_kernel<T, kCtas>);
+  p.slice = ((p.V + kCtas - 1) / kCtas + 63) / 64 * 64;
+  const int bytes = static_cast<int>((sizeof(Shared<kCtas>) + 15) / 16 * 16 + (kCtas > 1 ? (static_cast<size_t>(p.slice) + 8) * sizeof(T) : 0));
   cudaError_t e = glance::ensure_smem(f, bytes);
-  if (e == cudaSuccess && ctas > 8) e = allow_large_clusters(f);
+  if (e == cudaSuccess && kCtas > 8) e = allow_large_clusters(f);
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.M) * ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.M) * kCtas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
@@ -856,14 +1157,20 @@ glance_status launch(const char* who, const Params& p, int ctas, cudaStream_t st
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, sample_kernel<T>, p, ctas);
+  e = cudaLaunchKernelEx(&cfg, sample_kernel<T, kCtas>, p);
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
   return GLANCE_OK;
+}
+template <typename T>
+glance_status launch(const char* who, const Params& p, int ctas, cudaStream_t stream) {
+  return ctas == 1   ? launch<T, 1>(who, p, stream)
+         : ctas == 8 ? launch<T, 8>(who, p, stream)
+                     : launch<T, 16>(who, p, stream);
 }
 
 }  // namespace
@@ -903,8 +1210,7 @@ extern "C" glance_status glance_sample(const void* logits, int64_t row_stride, g
   p.k1 = static_cast<uint32_t>(seed >> 32);
   p.M = M;
   p.V = V;
-  const int ctas = cluster_size(M, V, esize);
-  p.slice = ((V + ctas - 1) / ctas + 63) / 64 * 64;
+  const int ctas = cluster_size(M, V);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == GLANCE_BF16 ? launch<__nv_bfloat16>(who, p, ctas, s) : launch<float>(who, p, ctas, s);
 }
