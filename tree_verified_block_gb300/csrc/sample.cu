@@ -10,17 +10,17 @@
 // = earlier. The token is argmax l_v r + g_v over the kept ones, g_v the noise of
 // the LM head's sampling mode: a draw from their renormalised softmax.
 //
-// A row is never sorted. One pass finds its maximum, and 512 maxima of disjoint
-// parts of it. Then, whichever comes first:
-// * k up to 384: at least k tokens are no smaller than the k-th largest of the
-//   parts' maxima, and seldom many more. They are gathered, sorted, summed and
-//   drawn from by one CTA.
+// Nothing is sorted. One pass finds the row's maximum, and the maxima of 2048
+// disjoint parts of it. Then, whichever comes first:
+// * k up to 1536: at least k tokens are no smaller than the k-th largest of the
+//   parts' maxima, and seldom many more. They are gathered by one CTA, which keeps
+//   them in registers, finds the last one that is kept and draws.
 // * Else a histogram of (max - l) r in steps of 1/64 holds each bin's count, or
 //   its count and weight. Where at most kList tokens lie in the bins up to the
-//   border's, these are gathered as above. Where not, the border's bin is (divided
-//   by further histograms, over ranges of the 50-bit numbers, until it fits the
-//   list, and) sorted, which gives the last token, and every CTA draws from its
-//   part of the row.
+//   border's, these are gathered as above. Where not, the tokens of the border's
+//   bin are (divided by further histograms, over ranges of the 50-bit numbers,
+//   until they fit the list, and) gathered, which gives the last token, and every
+//   CTA draws from its part of the row.
 // Within a bin weights are W (1 + y), |y| < 1/127, W a constant of the bin: the
 // sum of the y is kept as an integer in 2^-21 units, so that it does not depend
 // on the order of the additions and is good to 2^-22 of each weight. For top-p
@@ -31,13 +31,12 @@
 //
 // The draw's values are fp32 and compared in fp32 except for those that are near
 // the best: these are evaluated again in fp64, so that rounding decides nothing.
-// Most tokens need no logarithm: g >= t only if 1 - u <= e^-t, and once a warp has
+// Most tokens need no logarithm: g >= t only if 1 - u <= e^-t, and once there are
 // two values the noise's own bits decide.
 //
-// Forms of the kernel, by how many rows there are to fill the GPU: a CTA per row,
-// which reads the row again from L2 for a second pass, or a cluster that keeps
-// the row in its shared memory. Every decision that a cluster's CTAs take by
-// themselves is taken from values that all of them hold alike.
+// A row has one CTA, or a cluster of 4 or 16, by how many rows there are to fill
+// the GPU; a second pass over it reads from L2. Every decision that a cluster's
+// CTAs take by themselves is taken from values that all of them hold alike.
 #include <cstring>
 #include <mutex>
 
@@ -55,7 +54,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
 constexpr int kList = 2048;
 constexpr int kPer = kList / kThreads;
-constexpr int kGroups = kThreads;         // parts of a row whose maxima are known
+constexpr int kGroups = 2048;             // parts of a row whose maxima are known
 constexpr int kGroupK = kGroups * 3 / 4;  // so many of them are below the k-th, and the list will do
 constexpr int kIdBits = 18;
 constexpr int kMaxV = 1 << kIdBits;
@@ -141,9 +140,8 @@ struct Shared {
     struct {
       uint32_t count[kBins], sum[kSums][kBins];
     };
-    struct {
-      uint64_t list[kList];  // the first CTA's: numbers of tokens
-      int part[kThreads];    // one CTA: the threads whose tokens are looked at again
+    struct {  // of a search in the list's tokens: a bin's weight in two parts
+      uint32_t bin_count[kThreads], bin_low[kThreads], bin_high[kThreads];
     };
     struct {  // of the draw
       double near_z[kThreads];
@@ -151,16 +149,21 @@ struct Shared {
       int near_id[kThreads];
     };
   };
+  uint64_t mine[kCtas > 1 ? kList : 1];  // numbers of tokens on their way to the first CTA's list
   // written by the cluster's other CTAs
+  uint64_t list[kList];
   float group[kGroups];
   Mass coarse_mass[kCtas][kCoarse + 1];  // [kCoarse]: of tokens without a bin
   uint32_t coarse_count[kCtas][kCoarse];
   Best peer_best[kCtas];
   uint64_t peer_lo[kCtas], peer_hi[kCtas];
   Cut cut;
+  int found;
   uint32_t list_n[3];
   // this CTA's own
-  uint32_t near_n, part_n;
+  uint32_t near_n, part_n, mine_n, mine_at;
+  uint32_t second;  // key of a value that two of the draw's are no less than
+  int part[kThreads];  // the threads whose tokens are looked at again
   Border border;
   Mass fine_mass[kCtas][kFine];
   uint32_t fine_count[kCtas][kFine];
@@ -229,70 +232,79 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // The row as this CTA sees it.
 struct Row {
-  const unsigned char* at;  // its part: in shared memory, padded with -infinity, or global
-  bool vec;                 // global: four logits from a multiple of four on are aligned
+  const unsigned char* at;  // its part
+  bool vec;                 // four logits from a multiple of four on are aligned
   float own;                // the largest logit of this thread's tokens
   float top, r;             // the row's largest; 1 / T
   float min_l;              // tokens below are not kept
   int rank, first, n;       // ids first .. first + n - 1
 };
 
+// Four logits as they are stored.
 template <typename T>
-__device__ __forceinline__ void unpack4(const unsigned char* p, float (&l)[4]);
+struct Four;
 template <>
-__device__ __forceinline__ void unpack4<float>(const unsigned char* p, float (&l)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
-}
+struct Four<float> {
+  typedef float4 Raw;
+  static __device__ __forceinline__ void unpack(const Raw& v, float (&l)[4]) { l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w; }
+  static __device__ __forceinline__ Raw pack(const float (&l)[4]) { return make_float4(l[0], l[1], l[2], l[3]); }
+};
 template <>
-__device__ __forceinline__ void unpack4<__nv_bfloat16>(const unsigned char* p, float (&l)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void pack4(float* p, const float (&l)[4]) { *reinterpret_cast<float4*>(p) = make_float4(l[0], l[1], l[2], l[3]); }
-__device__ __forceinline__ void pack4(__nv_bfloat16* p, const float (&l)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3]));
-}
-template <typename T, bool kGlobal>
-__device__ __forceinline__ void load4(const Row& w, int i, float (&l)[4]) {
-  const unsigned char* p = w.at + static_cast<size_t>(i) * sizeof(T);
-  if (!kGlobal || (w.vec && i + 4 <= w.n)) {
-    unpack4<T>(p, l);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) l[j] = i + j < w.n ? static_cast<float>(reinterpret_cast<const T*>(p)[j]) : -INFINITY;
+struct Four<__nv_bfloat16> {
+  typedef uint2 Raw;
+  static __device__ __forceinline__ void unpack(const Raw& v, float (&l)[4]) {
+    l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xFFFF0000u);
   }
+  static __device__ __forceinline__ Raw pack(const float (&l)[4]) { return make_uint2(pack_bf16x2(l[0], l[1]), pack_bf16x2(l[2], l[3])); }
+};
+// From place i (a multiple of four) of this CTA's tokens on; -infinity behind them.
+template <typename T>
+__device__ __forceinline__ typename Four<T>::Raw load4(const Row& w, int i) {
+  const unsigned char* p = w.at + static_cast<size_t>(i) * sizeof(T);
+  if (w.vec && i + 4 <= w.n) return *reinterpret_cast<const typename Four<T>::Raw*>(p);
+  float l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) l[j] = i + j < w.n ? static_cast<float>(reinterpret_cast<const T*>(p)[j]) : -INFINITY;
+  return Four<T>::pack(l);
 }
 // Calls f(four logits, the first one's id) for this CTA's tokens, from a
-// multiple of four on; kBatch loads of a thread are in flight. after() follows
-// each batch, with every warp's lanes together. A thread with its largest logit
-// below `least` is passed over.
-template <typename T, bool kGlobal, int kBatch, typename F, typename G>
+// multiple of four on, with after() behind it for the warp's lanes together;
+// kAhead loads of a thread are in flight. The loop is not unrolled: a thread goes
+// through it ten to a hundred times, and the instructions of larger bodies took
+// longer to arrive than to run. A thread with its largest logit below `least` is
+// passed over.
+constexpr int kAhead = 4;
+template <typename T, typename F, typename G>
 __device__ __forceinline__ void each4(const Row& w, float least, F f, G after) {
+  typedef typename Four<T>::Raw Raw;
   const bool mine = w.own >= least;
   if (!__any_sync(0xffffffffu, mine)) return;
   const int t = threadIdx.x, warp0 = 4 * (t & ~31);
-  for (int base = 0; base + warp0 < w.n; base += 4 * kThreads * kBatch) {
-    float l[kBatch][4];
+  const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  Raw ahead[kAhead];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = base + 4 * t + u * 4 * kThreads;
-      if (mine && i < w.n) {
-        load4<T, kGlobal>(w, i, l[u]);
-      } else {
-        l[u][0] = l[u][1] = l[u][2] = l[u][3] = -INFINITY;
-      }
-    }
+  for (int d = 0; d < kAhead; ++d) {
+    ahead[d] = Four<T>::pack(none);
+    if (mine && 4 * (t + d * kThreads) < w.n) ahead[d] = load4<T>(w, 4 * (t + d * kThreads));
+  }
+#pragma unroll 1
+  for (int base = 0; base + warp0 < w.n; base += 4 * kThreads) {
+    float l[4];
+    Four<T>::unpack(ahead[0], l);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) f(l[u], w.first + base + 4 * t + u * 4 * kThreads);
+    for (int d = 0; d + 1 < kAhead; ++d) ahead[d] = ahead[d + 1];
+    const int next = base + 4 * (t + kAhead * kThreads);
+    ahead[kAhead - 1] = Four<T>::pack(none);
+    if (mine && next < w.n) ahead[kAhead - 1] = load4<T>(w, next);
+    f(l, w.first + base + 4 * t);
     __syncwarp();
     after();
   }
 }
-template <typename T, bool kGlobal, typename F>
+template <typename T, typename F>
 __device__ __forceinline__ void each(const Row& w, float least, F f) {
-  each4<T, kGlobal, 4>(
+  each4<T>(
       w, least,
       [&](const float(&l)[4], int id) {
 #pragma unroll
@@ -301,37 +313,27 @@ __device__ __forceinline__ void each(const Row& w, float least, F f) {
       [] {});
 }
 // The same, for the few threads that have a token with l >= least (others may
-// come too). A CTA that has to fetch their tokens from L2 shares them out to all.
-template <typename T, int kCtas, bool kGlobal, typename F>
+// come too): a thread's tokens come from L2, so few threads' are shared out to all.
+template <typename T, int kCtas, typename F>
 __device__ __forceinline__ void each_of_few(Shared<kCtas>* s, const Row& w, float least, F f) {
-  if constexpr (kGlobal) {
-    if (threadIdx.x == 0) s->part_n = 0;
-    __syncthreads();
-    if (w.own >= least) s->part[atomicAdd(&s->part_n, 1u)] = threadIdx.x;
-    __syncthreads();
-    const int parts = s->part_n, per = (w.n + 4 * kThreads - 1) / (4 * kThreads);  // groups of four of a thread
-    if (parts <= kThreads / 4) {
-      constexpr int kBatch = 4;
-      for (int i0 = threadIdx.x; i0 < parts * per; i0 += kThreads * kBatch) {
-        float l[kBatch][4];
-        int at[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int i = i0 + u * kThreads;
-          at[u] = i < parts * per ? 4 * (s->part[i / per] + kThreads * (i % per)) : w.n;
-          if (at[u] < w.n) load4<T, true>(w, at[u], l[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (at[u] < w.n) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f(l[u][j], w.first + at[u] + j);
-          }
-      }
-      return;
-    }
+  if (threadIdx.x == 0) s->part_n = 0;
+  __syncthreads();
+  if (w.own >= least) s->part[atomicAdd(&s->part_n, 1u)] = threadIdx.x;
+  __syncthreads();
+  const int parts = s->part_n, per = (w.n + 4 * kThreads - 1) / (4 * kThreads);  // groups of four of a thread
+  if (parts > kThreads / 4) {
+    each<T>(w, least, f);
+    return;
   }
-  each<T, kGlobal>(w, least, f);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < parts * per; i += kThreads) {
+    const int at = 4 * (s->part[i / per] + kThreads * (i % per));
+    if (at >= w.n) continue;
+    float l[4];
+    Four<T>::unpack(load4<T>(w, at), l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f(l[j], w.first + at + j);
+  }
 }
 
 // ------------------------------------------------------------- bins and sums
@@ -348,10 +350,16 @@ __device__ __forceinline__ bool place(const Row& w, float l, int& bin, float& y)
   y = d * fmaf(d, fmaf(d, fmaf(d, 1.f / 24, 1.f / 6), 0.5f), 1.f);  // to d^5 / 120 < 3e-13
   return true;
 }
-// A logit that no token of the bins up to `bin` is below.
+// Logits that no token of the bins up to `bin` is below, and none of the bins from
+// it on above.
 __device__ __forceinline__ float least_of_bin(const Row& w, int bin) {
   const float x = (static_cast<float>(bin) + 0.51f) / kBinsPerNat / w.r;
   return w.top - x - 1e-6f * (fabsf(w.top) + x);
+}
+
+__device__ __forceinline__ float most_of_bin(const Row& w, int bin) {
+  const float x = (static_cast<float>(bin) - 0.51f) / kBinsPerNat / w.r;
+  return w.top - x + 1e-6f * (fabsf(w.top) + fabsf(x));
 }
 
 template <int kCtas>
@@ -492,69 +500,16 @@ __device__ Border find_border(Shared<kCtas>* s, const Row& w, uint32_t want, Mas
   return b;
 }
 
-__device__ __forceinline__ int power_from(int n) {
-  int size = 32;
-  while (size < n && size < kList) size <<= 1;
-  return size;
-}
-// One step of the sort: the larger of two to the lower place where the run that
-// place e is in goes down.
-__device__ __forceinline__ uint64_t step_down(uint64_t v, uint64_t u, int e, int j, int k) {
-  return (v > u) == (((e & j) == 0) == ((e & k) == 0)) ? v : u;
-}
+// A warp's numbers in descending order.
 __device__ __forceinline__ uint64_t sort_warp(uint64_t v, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-    for (int j = k >> 1; j; j >>= 1) v = step_down(v, __shfl_xor_sync(0xffffffffu, v, j), lane, j, k);
-  return v;
-}
-// Sorts list[0 .. n) downwards, n <= kRows * kThreads, by the whole CTA: place e =
-// 512 i + t is thread t's i-th.
-template <int kRows>
-__device__ void sort_rows(uint64_t* list, int n) {
-  const int t = threadIdx.x, size = power_from(n);
-  uint64_t v[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) v[i] = i * kThreads + t < n ? list[i * kThreads + t] : 0ull;
-#pragma unroll 1
-  for (int k = 2; k <= size; k <<= 1)
-#pragma unroll 1
     for (int j = k >> 1; j; j >>= 1) {
-      if (j >= kThreads) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int o = i ^ (j / kThreads);
-#pragma unroll
-          for (int i2 = 0; i2 < kRows; ++i2)
-            if (i2 == o && i2 > i) {
-              const uint64_t a = v[i], b = v[i2];
-              v[i] = step_down(a, b, i * kThreads + t, j, k);
-              v[i2] = step_down(b, a, i2 * kThreads + t, j, k);
-            }
-        }
-      } else if (j >= 32) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) list[i * kThreads + t] = v[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) v[i] = step_down(v[i], list[i * kThreads + (t ^ j)], i * kThreads + t, j, k);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) v[i] = step_down(v[i], __shfl_xor_sync(0xffffffffu, v[i], j), i * kThreads + t, j, k);
-      }
+      const uint64_t u = __shfl_xor_sync(0xffffffffu, v, j);
+      v = (v > u) == (((lane & j) == 0) == ((lane & k) == 0)) ? v : u;
     }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) list[i * kThreads + t] = v[i];
-  __syncthreads();
-}
-__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
-  if (n <= kThreads)
-    sort_rows<1>(list, n);
-  else
-    sort_rows<kPer>(list, n);
+  return v;
 }
 
 // A token's weight, to 2^-42 of its bin's.
@@ -563,45 +518,134 @@ __device__ __forceinline__ Mass weight_of(const Row& w, float l) {
   float y;
   return place(w, l, bin, y) ? __umul64hi(weight_of_bin(bin), (1ull << 42) + __float2ll_rn(y * 4398046511104.f)) : 0ull;
 }
-// Weight of the first CTA's sorted list before and up to each of this thread's
-// tokens, kPer from place kPer t on.
+// The list's tokens, kPer to a thread; 0: none.
+struct Held {
+  uint64_t number[kPer];
+  Mass mass[kPer];
+};
 template <int kCtas>
-__device__ void list_masses(Shared<kCtas>* s, const Row& w, int n, Mass mass0, Mass (&before)[kPer], Mass (&upto)[kPer]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Mass sum = 0;
+__device__ __forceinline__ Held hold_list(Shared<kCtas>* s, const Row& w, int n, bool weigh) {
+  Held h;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int e = kPer * threadIdx.x + j;
-    before[j] = sum;
-    if (e < n) sum += weight_of(w, logit_of(s->list[e]));
-    upto[j] = sum;
+    const int e = static_cast<int>(threadIdx.x) + j * kThreads;
+    h.number[j] = e < n ? s->list[e] : 0ull;
+    h.mass[j] = weigh && e < n ? weight_of(w, logit_of(h.number[j])) : 0ull;
   }
-  const Mass to = scan_add(sum, lane);
-  if (lane == 31) s->warp_mass[warp] = to;
-  __syncthreads();
-  Mass at = mass0 + to - sum;
-  for (int i = 0; i < warp; ++i) at += s->warp_mass[i];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    before[j] += at;
-    upto[j] += at;
-  }
+  return h;
 }
 
-// Gathers the numbers of the tokens with l >= least that pass f in the first
-// CTA's list and returns how many there were (kList fit). The cluster's
-// histograms are not in use any more.
-template <typename T, int kCtas, bool kGlobal, typename F>
-__device__ uint32_t gather(Shared<kCtas>* s, const Row& w, int turn, float least, F f) {
-  each_of_few<T, kCtas, kGlobal>(s, w, least, [&](float l, int id) {
-    if (l >= least) {
-      const uint64_t number = number_of(l, id);
-      if (f(l, number)) {
-        const uint32_t at = add_first<kCtas>(&s->list_n[turn], 1u);
-        if (at < kList) to_peer<kCtas>(&s->list[at], 0, number);
+// The token of those held at which a prefix of `want` of them (want > 0), or of
+// the weight `target`, ends, where `mass0` lies before them: by one CTA, 512 bins
+// of the numbers' range at a time. The last one if there is none.
+template <int kCtas>
+__device__ Cut select_held(Shared<kCtas>* s, const Held& h, uint32_t want, Mass target, Mass mass0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
+  uint64_t lo = ~0ull, hi = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (h.number[j]) {
+      lo = h.number[j] < lo ? h.number[j] : lo;
+      hi = h.number[j] > hi ? h.number[j] : hi;
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const uint64_t a = __shfl_xor_sync(0xffffffffu, lo, o), c = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = a < lo ? a : lo;
+    hi = c > hi ? c : hi;
+  }
+  if (lane == 0) {
+    s->warp_lo[warp] = lo;
+    s->warp_hi[warp] = hi;
+  }
+  __syncthreads();
+  for (int i = 0; i < kWarps; ++i) {
+    lo = s->warp_lo[i] < lo ? s->warp_lo[i] : lo;
+    hi = s->warp_hi[i] > hi ? s->warp_hi[i] : hi;
+  }
+  const uint64_t least = lo;
+  uint32_t count0 = 0;
+  int shift = max(0, 64 - __clzll(hi - lo) - 9);
+  for (int level = 0; level < 8; ++level) {
+    s->bin_count[t] = s->bin_low[t] = s->bin_high[t] = 0;
+    if (t == 0) s->found = -1;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (h.number[j] >= lo && h.number[j] <= hi) {
+        const int bin = static_cast<int>((hi - h.number[j]) >> shift);
+        atomicAdd(&s->bin_count[bin], 1u);
+        if (!want) {  // (a token's weight is 2^40 at most, and there are 2^11)
+          atomicAdd(&s->bin_low[bin], static_cast<uint32_t>(h.mass[j]) & 0xFFFFFu);
+          atomicAdd(&s->bin_high[bin], static_cast<uint32_t>(h.mass[j] >> 20));
+        }
+      }
+    __syncthreads();
+    const uint32_t count = s->bin_count[t];
+    const Mass mass = (static_cast<Mass>(s->bin_high[t]) << 20) + s->bin_low[t];
+    const uint32_t count_to = scan_add(count, lane);
+    const Mass mass_to = scan_add(mass, lane);
+    if (lane == 31) {
+      s->warp_count[warp] = count_to;
+      s->warp_mass[warp] = mass_to;
+    }
+    __syncthreads();
+    uint32_t before = count0 + count_to - count;
+    Mass before_mass = mass0 + mass_to - mass;
+    for (int i = 0; i < warp; ++i) {
+      before += s->warp_count[i];
+      before_mass += s->warp_mass[i];
+    }
+    if (count && (want ? before < want && before + count >= want : before_mass < target && before_mass + mass >= target)) {
+      s->found = t;
+      s->border.count_before = before;
+      s->border.count_in = count;
+      s->border.mass_before = before_mass;
+    }
+    __syncthreads();
+    const int bin = s->found;
+    if (bin < 0) return Cut{least, target};
+    count0 = s->border.count_before;
+    mass0 = s->border.mass_before;
+    hi -= static_cast<uint64_t>(bin) << shift;
+    const uint64_t last = hi - ((1ull << shift) - 1);
+    lo = last > lo ? last : lo;
+    if (s->border.count_in == 1) break;  // numbers differ: at shift 0 at the latest
+    shift = max(0, shift - 9);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (h.number[j] >= lo && h.number[j] <= hi) s->cut = Cut{h.number[j], mass0 + h.mass[j]};
+  __syncthreads();
+  return s->cut;
+}
+
+// Gathers the numbers of the tokens with least <= l <= most that pass f in the
+// first CTA's list and returns how many there were (kList fit). Every CTA collects
+// its own first: one trip to the other CTA for all.
+template <typename T, int kCtas, typename F>
+__device__ uint32_t gather(Shared<kCtas>* s, const Row& w, int turn, float least, float most, F f) {
+  const int t = threadIdx.x;
+  if (t == 0) s->mine_n = 0;
+  uint32_t* n = kCtas == 1 ? &s->list_n[turn] : &s->mine_n;
+  uint64_t* to = kCtas == 1 ? s->list : s->mine;
+  each_of_few<T, kCtas>(s, w, least, [&](float l, int id) {
+    if (l >= least && l <= most) {
+      if (f(l, id)) {
+        const uint32_t at = atomicAdd(n, 1u);
+        if (at < kList) to[at] = number_of(l, id);
       }
     }
   });
+  if (kCtas > 1) {
+    __syncthreads();
+    const uint32_t mine = s->mine_n;
+    if (t == 0 && mine) s->mine_at = add_first<kCtas>(&s->list_n[turn], mine);
+    __syncthreads();
+    const uint32_t at = s->mine_at;
+    for (uint32_t i = t; i < mine && i < kList && at + i < kList; i += kThreads) to_peer<kCtas>(&s->list[at + i], 0, s->mine[i]);
+  }
   sync_row<kCtas>();
   return peer_u32<kCtas>(&s->list_n[turn], 0);
 }
@@ -768,24 +812,32 @@ __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, 
     if (t == 0) write_row(p, row, b);
     return;
   }
-  sort_list(s->list, n);
-  Mass before[kPer], upto[kPer], target = ~0ull;
+  Held h = hold_list(s, w, n, !all_p);
+  uint64_t cut = 1;
+  if (kept < n) {
+    cut = select_held(s, h, want, 0, 0).number;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (h.number[j] < cut) h.number[j] = 0;
+  }
   if (!all_p) {
-    list_masses(s, w, kept, 0, before, upto);
     if (mass_all == 0) {
+      Mass sum = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (kPer * t + j == kept - 1) s->cut.mass = upto[j];
+      for (int j = 0; j < kPer; ++j) sum += h.number[j] ? h.mass[j] : 0ull;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       __syncthreads();
-      mass_all = s->cut.mass;
+      if ((t & 31) == 0) s->warp_mass[t >> 5] = sum;
+      __syncthreads();
+      for (int i = 0; i < kWarps; ++i) mass_all += s->warp_mass[i];
+      __syncthreads();
     }
-    target = part_of(mass_all, share);
+    cut = select_held(s, h, 0u, part_of(mass_all, share), 0).number;
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = kPer * t + j;
-    if (e < kept && (all_p || before[j] < target)) draw(s->list[e]);
-  }
+  for (int j = 0; j < kPer; ++j)
+    if (h.number[j] >= cut) draw(h.number[j]);
   const Best b = block_best(s, w, key, two, false);
   if (t == 0) write_row(p, row, b);
 }
@@ -793,22 +845,22 @@ __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, 
 // The last token that a prefix keeps, and the weight up to it: the tokens of the
 // border's bin (from `floor` on) are divided until they fit the list, and that is
 // sorted. turn: which of the list's counters.
-template <typename T, int kCtas, bool kGlobal>
+template <typename T, int kCtas>
 __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint64_t floor, uint32_t want, Mass share, int turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
   Border b = first;
   const int bin = b.bin;
   const Mass all = b.mass_all;
   uint64_t lo = floor, hi = ~0ull;
-  const float least = least_of_bin(w, bin);
+  const float least = least_of_bin(w, bin), most = most_of_bin(w, bin);
   // the numbers differ and the range shrinks to the tokens' own each time: 50
   // bits are through after five divisions by 2^10 or more
   for (int level = 0; level < 8 && b.count_in > kList; ++level) {
     uint64_t least_n = ~0ull, most_n = 0;
-    each<T, kGlobal>(w, least, [&](float l, int id) {
+    each<T>(w, least, [&](float l, int id) {
       int at;
       float y;
-      if (l >= least && place(w, l, at, y) && at == bin) {
+      if (l >= least && l <= most && place(w, l, at, y) && at == bin) {
         const uint64_t number = number_of(l, id);
         if (number >= lo && number <= hi) {
           least_n = number < least_n ? number : least_n;
@@ -845,10 +897,10 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
       hi = s->peer_hi[q] > hi ? s->peer_hi[q] : hi;
     }
     const int shift = max(0, 64 - __clzll(hi - lo) - 11);  // the range in 2048 steps at most
-    each<T, kGlobal>(w, least, [&](float l, int id) {
+    each<T>(w, least, [&](float l, int id) {
       int at;
       float y;
-      if (l >= least && place(w, l, at, y) && at == bin) {
+      if (l >= least && l <= most && place(w, l, at, y) && at == bin) {
         const uint64_t number = number_of(l, id);
         if (number >= lo && number <= hi) add_hist(s, static_cast<int>((hi - number) >> shift), y, !want);
       }
@@ -860,27 +912,17 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
     const uint64_t last = hi - ((1ull << shift) - 1);
     lo = last > lo ? last : lo;
   }
-  sync_row<kCtas>();  // the others have read this CTA's histogram
-  const uint32_t found = gather<T, kCtas, kGlobal>(s, w, turn, least, [&](float l, uint64_t number) {
+  const uint32_t found = gather<T, kCtas>(s, w, turn, least, most, [&](float l, int id) {
     int at;
     float y;
+    const uint64_t number = number_of(l, id);
     return number >= lo && number <= hi && place(w, l, at, y) && at == bin;
   });
   if (w.rank == 0) {
     const int n = min(found, static_cast<uint32_t>(kList));
-    sort_list(s->list, n);
-    Mass before[kPer], upto[kPer];
-    list_masses(s, w, n, b.mass_before, before, upto);
-    const Mass target = part_of(all, share);
-    if (t == 0) s->cut = Cut{s->list[max(n - 1, 0)], all};  // unless a token is found: the last one
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = kPer * t + j;
-      if (e < n && (want ? b.count_before + e + 1 == want : before[j] < target && upto[j] >= target)) s->cut = Cut{s->list[e], upto[j]};
-    }
-    __syncthreads();
-    if (t > 0 && t < kCtas) to_peer<kCtas>(&s->cut, t, s->cut);
+    const Held h = hold_list(s, w, n, !want);
+    const Cut c = select_held(s, h, want ? want - b.count_before : 0u, part_of(all, share), b.mass_before);
+    if (t < kCtas) to_peer<kCtas>(&s->cut, t, c);
   }
   sync_row<kCtas>();
   return s->cut;
@@ -888,14 +930,11 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
 
 // ------------------------------------------------------------------ the kernel
 
-// Grid: x = row * kCtas + rank. One CTA: the row stays in global memory; more:
-// in theirs.
+// Grid: x = row * kCtas + rank.
 template <typename T, int kCtas>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
-  constexpr bool kGlobal = kCtas == 1;
   extern __shared__ __align__(16) unsigned char smem[];
   Shared<kCtas>* s = reinterpret_cast<Shared<kCtas>*>(smem);
-  unsigned char* s_row = smem + (sizeof(Shared<kCtas>) + 15) / 16 * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
   const int row = static_cast<int>(blockIdx.x) / kCtas;
   Row w;
@@ -915,27 +954,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
   const unsigned char* src =
       reinterpret_cast<const unsigned char*>(p.logits) + row * p.stride + static_cast<long long>(w.first) * static_cast<int>(sizeof(T));
   w.vec = reinterpret_cast<uintptr_t>(src) % (4 * sizeof(T)) == 0;
-  float top = -INFINITY;  // of this thread's tokens
-  w.own = 0.f;
   w.at = src;
-  each4<T, true, sizeof(T) == 4 ? 4 : 8>(
-      w, -INFINITY,
-      [&](const float(&l)[4], int id) {
-        top = max_nan(top, max_nan(max_nan(l[0], l[1]), max_nan(l[2], l[3])));
-        if (!kGlobal && id - w.first < w.n) pack4(reinterpret_cast<T*>(s_row) + (id - w.first), l);
-      },
-      [] {});
-  if (!kGlobal) w.at = s_row;
-  w.own = top;
-  // 512 maxima in all, of kCtas threads each, to every CTA
+  // the maxima of four parts of this thread's tokens; with more CTAs it is
+  // kCtas / 4 threads' that are one part
+  float group[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  constexpr int kBatch = sizeof(T) == 4 ? 4 : 8;
+  for (int base = 4 * t; base < w.n; base += 4 * kThreads * kBatch) {
+    typename Four<T>::Raw raw[kBatch];
 #pragma unroll
-  for (int o = 1; o < kCtas; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (kCtas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all have begun
-  to_peer<kCtas>(&s->group[(w.rank * kThreads + t) / kCtas], t % kCtas, top);
+    for (int u = 0; u < kBatch; ++u)
+      if (base + u * 4 * kThreads < w.n) raw[u] = load4<T>(w, base + u * 4 * kThreads);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (base + u * 4 * kThreads < w.n) {
+        float l[4];
+        Four<T>::unpack(raw[u], l);
+        group[u & 3] = max_nan(group[u & 3], max_nan(max_nan(l[0], l[1]), max_nan(l[2], l[3])));
+      }
+  }
+  __syncwarp();
+  w.own = max_nan(max_nan(group[0], group[1]), max_nan(group[2], group[3]));
+  if (kCtas > 1) {
+    float part = w.own;
+#pragma unroll
+    for (int o = 1; o < kCtas / 4; o <<= 1) part = max_nan(part, __shfl_xor_sync(0xffffffffu, part, o));
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all have begun
+    constexpr int kOne = kCtas >= 4 ? kCtas / 4 : 1;  // threads of a part
+#pragma unroll
+    for (int j = 0; j < 4; ++j) to_peer<kCtas>(&s->group[(w.rank * kThreads + t) / kOne], t % kOne * 4 + j, part);
+  }
   if (t == 0) s->log_min_p = min_p > 0.f && !greedy ? log(static_cast<double>(min_p)) : 0.0;
   sync_row<kCtas>();
-  const float group = s->group[t];
-  top = group;
+  if (kCtas > 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) group[j] = s->group[t + j * kThreads];
+  }
+  float top = max_nan(max_nan(group[0], group[1]), max_nan(group[2], group[3]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s->warp_f[warp] = top;
@@ -976,23 +1030,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
     Border b = {};
     b.bin = -1;
     if (want && want <= kGroupK) {
-      // k of the maxima, tokens all, are at or above a place between them that
-      // is searched for to 2^-10 of the histogram's range
-      float lo = top - kRange / w.r, hi = top;
-      if (__syncthreads_count(group >= lo) < static_cast<int>(want)) {
-        lo = -INFINITY;
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < 10; ++i) {
-          const float mid = 0.5f * (lo + hi);
-          if (__syncthreads_count(group >= mid) >= static_cast<int>(want))
-            lo = mid;
-          else
-            hi = mid;
-        }
+      // k of the maxima, tokens all, are at or above the upper one of 512 steps of
+      // the histogram's range that the k-th is in
+      s->part[t] = 0;  // (not the histogram's place: another CTA may write to the list there)
+      if (t == 0) s->found = -1;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __fmul_rn(top - group[j], w.r);
+        if (x < kRange) atomicAdd(&s->part[static_cast<int>(x * (kThreads / 32.f))], 1);
       }
+      __syncthreads();
+      const uint32_t count = s->part[t], count_to = scan_add(count, lane);
+      if (lane == 31) s->warp_count[warp] = count_to;
+      __syncthreads();
+      uint32_t before = count_to - count;
+      for (int i = 0; i < warp; ++i) before += s->warp_count[i];
+      if (before < want && before + count >= want) s->found = t;
+      __syncthreads();
+      const float x = (static_cast<float>(s->found) + 1.01f) * (32.f / kThreads) / w.r;
+      const float lo = s->found < 0 ? -INFINITY : top - x - 1e-6f * (fabsf(top) + x);
       const float least = fmaxf(lo, w.min_l);
-      upto = gather<T, kCtas, kGlobal>(s, w, 0, least, [&](float l, uint64_t) { return __fmul_rn(w.top - l, w.r) < kRange; });
+      upto = gather<T, kCtas>(s, w, 0, least, INFINITY, [&](float l, int) { return __fmul_rn(w.top - l, w.r) < kRange; });
     }
     if (upto > kList) {
       // Tokens with (max - l) r above `skip` need no bin: all of them together
@@ -1000,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       const float skip = want ? kRange : fminf(kRange, logf(2.f * p.V / (1.f - fmaxf(top_p, 0.f))));
       float loose = 0.f;
       clear_hist(s);
-      each<T, kGlobal>(w, w.min_l, [&](float l, int) {
+      each<T>(w, w.min_l, [&](float l, int) {
         const float x = __fmul_rn(w.top - l, w.r);
         if (x < skip) {
           int bin;
@@ -1013,8 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       b = find_border(s, w, want, share, 0, loose, -1, 0u, 0);
       upto = ~0u;
       if (b.bin >= 0 && b.count_before + b.count_in <= kList) {
-        sync_row<kCtas>();  // the others have read this CTA's histogram
-        upto = gather<T, kCtas, kGlobal>(s, w, 1, least_of_bin(w, b.bin), [&](float l, uint64_t) {
+        upto = gather<T, kCtas>(s, w, 1, least_of_bin(w, b.bin), INFINITY, [&](float l, int) {
           int bin;
           float y;
           return __fmul_rn(w.top - l, w.r) < skip && place(w, l, bin, y) && bin <= b.bin;
@@ -1034,18 +1092,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       return;
     }
     if (b.bin >= 0) {
-      cut = refine<T, kCtas, kGlobal>(s, w, b, 0, want, share, 1).number;
+      cut = refine<T, kCtas>(s, w, b, 0, want, share, 1).number;
       if (want && !all_p) {
         // the first k are known: the share of their weight ends at or before their last
         clear_hist(s);
-        each<T, kGlobal>(w, logit_of(cut), [&](float l, int id) {
+        each<T>(w, logit_of(cut), [&](float l, int id) {
           int bin;
           float y;
           if (place(w, l, bin, y) && number_of(l, id) >= cut) add_hist(s, bin, y, true);
         });
         b = find_border(s, w, 0u, share, 0, 0.f, -1, 0u, 0);
         if (b.bin >= 0) {
-          const Cut c = refine<T, kCtas, kGlobal>(s, w, b, cut, 0u, share, 2);
+          const Cut c = refine<T, kCtas>(s, w, b, cut, 0u, share, 2);
           if (c.number > cut) cut = c.number;
         }
       }
@@ -1053,36 +1111,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       // fewer than k tokens in reach: the share is of all of them
       sync_row<kCtas>();  // the others have read the sums of the search before
       clear_hist(s);
-      each<T, kGlobal>(w, w.min_l, [&](float l, int) {
+      each<T>(w, w.min_l, [&](float l, int) {
         int bin;
         float y;
         if (place(w, l, bin, y)) add_hist(s, bin, y, true);
       });
       b = find_border(s, w, 0u, share, 0, 0.f, -1, 0u, 0);
-      if (b.bin >= 0) cut = refine<T, kCtas, kGlobal>(s, w, b, 0, 0u, share, 2).number;
+      if (b.bin >= 0) cut = refine<T, kCtas>(s, w, b, 0, 0u, share, 2).number;
     }
   }
   // every CTA looks at its part of the row
   Two two = no_two();
   if (greedy) {
     // two tokens are no smaller than the second largest of the parts' maxima
-    float second = group == top ? -INFINITY : group;
+    float second = -INFINITY;
+    int tops = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tops += group[j] == top;
+      if (group[j] != top) second = fmaxf(second, group[j]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, o));
     if (lane == 0) s->warp_second[warp] = second;
-    if (__syncthreads_count(group == top) > 1) second = top;
+    if (__syncthreads_count(tops > 0) > 1 || __syncthreads_or(tops > 1)) second = top;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) second = fmaxf(second, s->warp_second[i]);
-    each_of_few<T, kCtas, kGlobal>(s, w, second, [&](float l, int id) {
+    each_of_few<T, kCtas>(s, w, second, [&](float l, int id) {
       if (l > -INFINITY) fold(two, l, l, id);
     });
   } else {
     const float cut_l = cut ? logit_of(cut) : -INFINITY;
     const float least = fmaxf(fmaxf(cut_l, w.min_l), -3.4028234e38f);
     const int last = cut ? id_of(cut) : kMaxV;  // of the tokens with the cut's logit
-    float second = -INFINITY;  // two of the warp's values are no less
+    float second = -INFINITY;  // two of the CTA's values are no less
+    if (t == 0) s->second = 0;
+    __syncthreads();
     float reach = least;       // tokens below cannot come to it: the noise is below 16.7
-    each4<T, kGlobal, 4>(
+    each4<T>(
         w, least,
         [&](const float(&l)[4], int id) {
           const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
@@ -1103,21 +1169,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
           const uint32_t z0 = ord_key(two.z[0]), z1 = ord_key(two.z[1]);
           const uint32_t best = __reduce_max_sync(0xffffffffu, z0);
           const unsigned who = __ballot_sync(0xffffffffu, z0 == best);
-          second = of_key(__reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? z1 : z0));
+          const uint32_t next = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? z1 : z0);
+          const uint32_t shared = *const_cast<volatile uint32_t*>(&s->second);
+          if (lane == 0 && next > shared) atomicMax(&s->second, next);
+          second = of_key(max(next, shared));
           reach = fmaxf(least, w.top + (second - 16.8f) / w.r - 1e-5f * fabsf(w.top));
         });
   }
   finish(s, p, w, key, two, greedy, row);
 }
 
-constexpr int kRowsAlone = 96;  // rows beyond which a row has one CTA
-
-// CTAs to a row: 1, or a cluster of 8 or 16 that holds it, while rows alone
-// would leave SMs idle.
+// CTAs to a row: 16 while two such clusters' CTAs have an SM each, 4 beyond, as
+// long as each has enough of the row.
 int cluster_size(int M, int V) {
-  if (M > kRowsAlone || V < 2048) return 1;
-  if (M * 16 <= glance::num_sms() && V >= 16 * 2048) return 16;
-  return 8;
+  if (M * 16 <= 2 * glance::num_sms() && V >= 16 * 2048) return 16;
+  return V >= 4 * 2048 ? 4 : 1;
 }
 
 // Clusters of 16 are beyond the portable size: allowed once per kernel and device.
@@ -1144,7 +1210,7 @@ template <typename T, int kCtas>
 glance_status launch(const char* who, Params p, cudaStream_t stream) {
   const void* f = reinterpret_cast<const void*>(sample_kernel<T, kCtas>);
   p.slice = ((p.V + kCtas - 1) / kCtas + 63) / 64 * 64;
-  const int bytes = static_cast<int>((sizeof(Shared<kCtas>) + 15) / 16 * 16 + (kCtas > 1 ? (static_cast<size_t>(p.slice) + 8) * sizeof(T) : 0));
+  const int bytes = static_cast<int>(sizeof(Shared<kCtas>));
   cudaError_t e = glance::ensure_smem(f, bytes);
   if (e == cudaSuccess && kCtas > 8) e = allow_large_clusters(f);
   if (e != cudaSuccess) return glance::cuda_fail(e, who);
@@ -1169,7 +1235,7 @@ glance_status launch(const char* who, Params p, cudaStream_t stream) {
 template <typename T>
 glance_status launch(const char* who, const Params& p, int ctas, cudaStream_t stream) {
   return ctas == 1   ? launch<T, 1>(who, p, stream)
-         : ctas == 8 ? launch<T, 8>(who, p, stream)
+         : ctas == 4 ? launch<T, 4>(who, p, stream)
                      : launch<T, 16>(who, p, stream);
 }
 
