@@ -18,9 +18,9 @@
 //   share of the rows. The first weight stages are on their way before the
 //   kernel waits for the one before it.
 // * Many rows (q8_linear_wide_kernel): bound by the products. A pair of SMs
-//   works on 256 x 256 outputs (each holds half of both operands), persistent
-//   over the tiles, with two accumulators so that one tile's epilogue runs under
-//   the next one's products.
+//   works on 256 x 256 outputs (each holds half of both operands; 256 x 128 where
+//   these would not fill half of the pairs), persistent over the tiles, with two
+//   accumulators so that one tile's epilogue runs under the next one's products.
 #include <mutex>
 
 #include "q8_internal.cuh"
@@ -46,7 +46,8 @@ struct Params {
   const char* residual;   // null: none
   char* out;
   long long r_stride, o_stride;  // bytes
-  int tiles_n, tiles_m, tiles;   // wide: tiles of 256 x 256
+  int tiles_n, tiles_m;  // wide
+  int64_t tiles;
 };
 
 // ------------------------------------------------------------------- epilogue
@@ -95,6 +96,61 @@ __device__ __forceinline__ void store8(const Params& p, int64_t row, int n, floa
   }
 }
 
+// The residual of 32 outputs of this thread's row from column n on (those that
+// are there: N is a multiple of eight). A sector's second half comes from L1.
+__device__ __forceinline__ void add_residual(const Params& p, int64_t row, int n, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    if (n + j >= p.N) continue;
+    if (p.out_f32) {
+      const float4* r = reinterpret_cast<const float4*>(p.residual + row * p.r_stride + 4ll * (n + j));
+      const float4 a = r[0], b = r[1];
+      v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w, v[j + 4] += b.x, v[j + 5] += b.y, v[j + 6] += b.z, v[j + 7] += b.w;
+    } else {
+      const uint4 r = *reinterpret_cast<const uint4*>(p.residual + row * p.r_stride + 2ll * (n + j));
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[j + 2 * i] += __uint_as_float(w[i] << 16);
+        v[j + 2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// A warp's 32 rows of 64 bytes, a row a thread, to out rows row0 .. from byte
+// `at` of a row on: through shared memory (16-byte pieces exchanged so that neither
+// side meets a bank twice), so that four threads write a row's two sectors whole.
+__device__ __forceinline__ void store_rows(const Params& p, unsigned char* buf, const uint32_t (&word)[16], int64_t row0, int64_t at) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + (c ^ ((lane >> 1) & 3)) * 16) =
+        make_uint4(word[4 * c], word[4 * c + 1], word[4 * c + 2], word[4 * c + 3]);
+  __syncwarp();
+  const int piece = lane & 3;
+  const bool in = at + 16 * piece < static_cast<int64_t>(p.N) * (p.out_f32 ? 4 : 2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
+    if (in && row0 + r < p.M && GLANCE_IN_BOUNDS(row0 + r, p.M))
+      *reinterpret_cast<uint4*>(p.out + (row0 + r) * p.o_stride + at + 16 * piece) = v;
+  }
+}
+
+// One output.
+__device__ __forceinline__ void store1(const Params& p, int64_t row, int n, float v) {
+  if (p.out_f32) {
+    if (p.residual) v += *reinterpret_cast<const float*>(p.residual + row * p.r_stride + 4ll * n);
+    *reinterpret_cast<float*>(p.out + row * p.o_stride + 4ll * n) = v;
+  } else {
+    if (p.residual) v += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p.residual + row * p.r_stride + 2ll * n));
+    *reinterpret_cast<__nv_bfloat16*>(p.out + row * p.o_stride + 2ll * n) = __float2bfloat16_rn(v);
+  }
+}
+
 // ---------------------------------------------------------------------- waits
 
 __device__ __forceinline__ bool aborted(const int* flag) { return *reinterpret_cast<const volatile int*>(flag) != 0; }
@@ -122,6 +178,8 @@ __device__ __forceinline__ void settle() {
 
 constexpr int kFewThreads = 256;
 constexpr int kMaxSplit = 8;
+constexpr int kMaxRows = 128;  // of a block
+constexpr uint32_t kFewMisc = 2048;
 
 template <int kRows>
 struct Few {
@@ -130,7 +188,7 @@ struct Few {
   // two CTAs to an SM
   static constexpr int kStages = kRows <= 16 ? 6 : kRows <= 32 ? 5 : kRows <= 64 ? 4 : 3;
   static constexpr uint32_t kArea = kStages * kStage;
-  static constexpr uint32_t kSmem = 1024 + kArea + 1024;
+  static constexpr uint32_t kSmem = 1024 + kArea + kFewMisc;
   static constexpr uint32_t kCols = kRows < 32 ? 32 : kRows;  // of tensor memory
   static_assert((kRows + kMaxSplit) * kTile * 4 <= kArea, "received partials take the stages' place");
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -142,8 +200,10 @@ struct FewBars {
   uint32_t tmem;
   int abort;
   int failed;  // read by the cluster's other CTAs
+  float scale[kTile], bias[kTile];  // of the tile's weight rows
+  float x_scale[kMaxRows];
 };
-static_assert(sizeof(FewBars) <= 1024, "barriers");
+static_assert(sizeof(FewBars) <= kFewMisc, "barriers and scales");
 
 __device__ __forceinline__ int dsmem_ld_s32(uint32_t addr) {
   int v;
@@ -240,6 +300,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if (ok) mma_commit(&bars->done);
     }
   }
+  const int M = min(kRows, p.M - m0);  // rows of this block
+  if (warp >= 2) {  // what the epilogue needs, while the products run
+    const int i = static_cast<int>(threadIdx.x) - 64;
+    if (i < kTile) {
+      const int n = p.gated ? tile * 64 + (i & 63) : tile * kTile + i, w = i < 64 ? w0 + i : w1 + i - 64;
+      bars->scale[i] = n < p.N ? __ldg(p.w_scale + w) : 0.f;
+      bars->bias[i] = n < p.N && p.bias ? __ldg(p.bias + w) : 0.f;
+    }
+    for (int m = i; m < M; m += kFewThreads - 64) bars->x_scale[m] = __ldg(p.x_scale + m0 + m);
+  }
   __syncwarp();
   if (ok) ok = wait_or_abort(&bars->done, 0, &bars->abort);
   if (!ok) give_up(&bars->abort);
@@ -254,8 +324,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (threadIdx.x < S) peer = dsmem_ld_s32(dsmem_addr(&bars->failed, threadIdx.x)) != 0;
     bad = __syncthreads_or(peer) != 0;
   }
-  const int M = min(kRows, p.M - m0);  // rows of this block
-  const int per = (M + S - 1) / S;     // rows that a CTA finishes
+  const int per = (M + S - 1) / S;  // rows that a CTA finishes
+  const bool direct = S == 1 && !p.gated;  // a thread has all of its outputs' sums
   if (!bad) {
     // D: lane = weight row of the tile, column = row. Row m's partial goes to
     // the CTA that finishes it, [source][row][128].
@@ -281,6 +351,21 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(tmem + lanes + m));
       tmem_ld_wait();
+      if (direct) {
+        const int n = tile * kTile + ch;
+        if (n < p.N) {
+          const float ws = bars->scale[ch], b = bars->bias[ch];
+          float v[kChunk];
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) v[j] = fmaf(__uint_as_float(r[j]) * bars->x_scale[m + j], ws, b);
+          activate(v, p.act);
+          // a warp's 32 outputs of a row lie next to each other
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j)
+            if (m + j < M && GLANCE_IN_BOUNDS(m0 + m + j, p.M)) store1(p, m0 + m + j, n, v[j]);
+        }
+        continue;
+      }
       int owner = m / per, local = m - owner * per;
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) {
@@ -302,14 +387,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     tmem_dealloc(tmem, C::kCols);
   }
   if (S > 1) cluster_sync_all();  // every partial has reached its owner
-  if (bad) return;
+  if (bad || direct) return;
   const int first = rank * per, mine = min(per, M - first);
   const int cols = p.gated ? 64 : kTile, groups = cols / 8;
   for (int i = threadIdx.x; i < mine * groups; i += kFewThreads) {
     const int local = i / groups, c = i % groups * 8, n = tile * cols + c;
     if (n >= p.N) continue;
     const int64_t row = m0 + first + local;
-    const float xs = __ldg(p.x_scale + row);
+    const float xs = bars->x_scale[first + local];
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -322,12 +407,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         b.x += b1.x, b.y += b1.y, b.z += b1.z, b.w += b1.w;
       }
       const float sum[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      const int w = n + (h ? p.N : 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[h][j] = sum[j] * xs * __ldg(p.w_scale + w + j);
-        if (p.bias) v[h][j] += __ldg(p.bias + w + j);
-      }
+      for (int j = 0; j < 8; ++j) v[h][j] = fmaf(sum[j] * xs, bars->scale[c + 64 * h + j], bars->bias[c + 64 * h + j]);
     }
     activate(v[0], p.act);
     if (p.gated) {
@@ -342,11 +423,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 constexpr int kWideThreads = 384;  // a warp each for copies, products, tensor memory; one idle; eight for the epilogue
 constexpr int kWideStages = 6;
-constexpr uint32_t kWideStage = 2 * kTileBytes;  // a CTA's 128 rows and 128 weight rows
-constexpr uint32_t kWideArea = kWideStages * kWideStage;
+// kN: weight rows of a tile. A stage is a CTA's 128 rows and half of the weight rows.
+__host__ __device__ constexpr uint32_t wide_stage(int kN) { return kTileBytes + kN / 2 * kBK; }
+constexpr uint32_t kWideArea = kWideStages * wide_stage(256);
 constexpr uint32_t kWideVec = 2 * 2 * 256 * 4;  // two tiles' weight scales and biases
-constexpr uint32_t kWideSmem = 1024 + kWideArea + kWideVec + 1024;
 constexpr int kEpilogueWarps = 8;
+constexpr uint32_t kWideOut = kEpilogueWarps * 32 * 64;  // a warp's 32 rows of 64 bytes on their way out
+constexpr uint32_t kWideSmem = 1024 + kWideArea + kWideOut + kWideVec + 1024;
 constexpr int kGroupM = 8;  // tiles of the row axis that are taken together, for L2
 
 struct WideBars {
@@ -359,20 +442,25 @@ static_assert(sizeof(WideBars) <= 1024, "barriers");
 static_assert(kWideSmem <= 227 * 1024, "shared memory");
 
 // Tile i: groups of kGroupM row tiles go through all column tiles.
-__device__ __forceinline__ void wide_tile(const Params& p, int i, int& tm, int& tn) {
-  const int per_group = kGroupM * p.tiles_n, g = i / per_group, in = i - g * per_group;
+__device__ __forceinline__ void wide_tile(const Params& p, int64_t i, int& tm, int& tn) {
+  const int64_t per_group = static_cast<int64_t>(kGroupM) * p.tiles_n;
+  const int g = static_cast<int>(i / per_group), in = static_cast<int>(i - g * per_group);
   const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
   tm = g * kGroupM + in % rows;
   tn = in / rows;
 }
 
+template <int kN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     q8_linear_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Params p) {
+  constexpr uint32_t kStage = wide_stage(kN);
+  constexpr int kHalf = kN / 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* s_vec = reinterpret_cast<float*>(smem + kWideArea);  // [2 tiles][scale, bias][256]
-  WideBars* bars = reinterpret_cast<WideBars*>(smem + kWideArea + kWideVec);
+  unsigned char* s_out = smem + kWideArea;
+  float* s_vec = reinterpret_cast<float*>(smem + kWideArea + kWideOut);  // [2 tiles][scale, bias][256]
+  WideBars* bars = reinterpret_cast<WideBars*>(smem + kWideArea + kWideOut + kWideVec);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
@@ -389,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     fence_barrier_init();
   }
   if (warp == 2) {
-    tmem_alloc_pair(&bars->tmem, 512);
+    tmem_alloc_pair(&bars->tmem, 2 * kN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -403,23 +491,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_last();
-      const int w_of = p.gated ? 128 : 256;  // outputs of a tile
+      const int w_of = p.gated ? kHalf : kN;  // outputs of a tile
       int it = 0;
-      for (int i = pair; i < p.tiles && ok; i += pairs) {
+      for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
         int tm, tn;
         wide_tile(p, i, tm, tn);
         const int x0 = tm * 256 + rank * 128;
-        // the pair's second CTA holds the tile's second half: columns 128 .., or the up rows
-        const int w0 = tn * w_of + (rank ? (p.gated ? p.N : 128) : 0);
+        // the pair's second CTA holds the tile's second half: the later columns, or the up rows
+        const int w0 = tn * w_of + (rank ? (p.gated ? p.N : kHalf) : 0);
         for (int kb = 0; kb < p.n_kb; ++kb, ++it) {
           const int st = it % kWideStages;
           if (it >= kWideStages && !wait_or_abort(&bars->empty[st], (it / kWideStages - 1) & 1, &bars->abort)) {
             ok = false;
             break;
           }
-          unsigned char* at = smem + st * kWideStage;
+          unsigned char* at = smem + st * kStage;
           const uint32_t full = dsmem_addr(&bars->full[st], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * kWideStage);
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * kStage);
           tma_load_2d_pair(at, &map_x, full, kb * kBK, x0, pol);
           tma_load_2d_pair(at + kTileBytes, &map_w, full, kb * kBK, w0, pol);
         }
@@ -427,10 +515,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+      constexpr uint32_t idesc = idesc_e4m3_f32(256, kN);
       const uint32_t a0 = smem_u32(smem);
       int it = 0, n = 0;
-      for (int i = pair; i < p.tiles && ok; i += pairs, ++n) {
+      for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
         const int acc = n & 1;
         if (n >= 2 && !wait_or_abort(&bars->acc_empty[acc], (n / 2 - 1) & 1, &bars->abort)) {
           ok = false;
@@ -444,10 +532,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a = a0 + st * kWideStage, b = a + kTileBytes;
+          const uint32_t a = a0 + st * kStage, b = a + kTileBytes;
 #pragma unroll
           for (int k = 0; k < kBK / 32; ++k)
-            mma_f8_ss_pair(tmem + acc * 256, sdesc_sw128(a + k * 32, 16, 1024), sdesc_sw128(b + k * 32, 16, 1024), idesc,
+            mma_f8_ss_pair(tmem + acc * kN, sdesc_sw128(a + k * 32, 16, 1024), sdesc_sw128(b + k * 32, 16, 1024), idesc,
                            (kb | k) ? 1u : 0u);
           mma_commit_pair(&bars->empty[st]);
         }
@@ -459,16 +547,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int te = static_cast<int>(threadIdx.x) - 128;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int n = 0;
-    for (int i = pair; i < p.tiles && ok; i += pairs, ++n) {
+    for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
       const int acc = n & 1;
       int tm, tn;
       wide_tile(p, i, tm, tn);
-      const int out0 = tn * (p.gated ? 128 : 256);
+      const int out0 = tn * (p.gated ? kHalf : kN);
       // this tile's weight scales and biases; the other buffer may still be read
       float* vec = s_vec + (n & 1) * 512;
-      {
-        const int w = p.gated ? (te < 128 ? out0 + te : p.N + out0 + te - 128) : out0 + te;
-        const bool in = p.gated ? out0 + (te & 127) < p.N : w < p.N;
+      if (te < kN) {
+        const int w = p.gated ? (te < kHalf ? out0 + te : p.N + out0 + te - kHalf) : out0 + te;
+        const bool in = p.gated ? out0 + te % kHalf < p.N : w < p.N;
         vec[te] = in ? __ldg(p.w_scale + w) : 0.f;
         vec[256 + te] = in && p.bias ? __ldg(p.bias + w) : 0.f;
       }
@@ -478,8 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       ok = !named_bar_or(1, 32 * kEpilogueWarps, !wait_or_abort(&bars->acc_full[acc], (n / 2) & 1, &bars->abort));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + lanes + acc * 256;
-      const int width = p.gated ? 64 : 128;  // this warp's outputs
+      const uint32_t d = tmem + lanes + acc * kN;
+      const int width = p.gated ? kHalf / 2 : kHalf;  // this warp's outputs
 #pragma unroll 1
       for (int c = half * width; c < (half + 1) * width; c += 32) {
         uint32_t r[32];
@@ -496,12 +584,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         activate(v, p.act);
         if (p.gated) {
-          tmem_ld32(d + 128 + c, r);
+          tmem_ld32(d + kHalf + c, r);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(vec + 128 + c + j),
-                         b = *reinterpret_cast<const float4*>(vec + 384 + c + j);
+            const float4 s = *reinterpret_cast<const float4*>(vec + kHalf + c + j),
+                         b = *reinterpret_cast<const float4*>(vec + 256 + kHalf + c + j);
             v[j] *= fmaf(__uint_as_float(r[j]) * xs, s.x, b.x);
             v[j + 1] *= fmaf(__uint_as_float(r[j + 1]) * xs, s.y, b.y);
             v[j + 2] *= fmaf(__uint_as_float(r[j + 2]) * xs, s.z, b.z);
@@ -513,16 +601,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(dsmem_addr(&bars->acc_empty[acc], 0));
         }
-        if (row < p.M) {
+        if (p.residual && row < p.M) add_residual(p, row, out0 + c, v);
+        if (p.out_f32) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (out0 + c + j < p.N && GLANCE_IN_BOUNDS(row, p.M)) {
-              float o[8];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t word[16];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = v[j + q];
-              store8(p, row, out0 + c + j, o);
-            }
+            for (int j = 0; j < 16; ++j) word[j] = __float_as_uint(v[16 * h + j]);
+            store_rows(p, s_out + e * 2048, word, row - lane, (out0 + c + 16 * h) * 4);
           }
+        } else {
+          uint32_t word[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) word[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+          store_rows(p, s_out + e * 2048, word, row - lane, (out0 + c) * 2);
         }
       }
     }
@@ -534,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   cluster_sync_all();  // the pair is done with both CTAs' memory
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * kN);
   }
 }
 
@@ -546,13 +638,44 @@ cudaError_t raise(F* f, int bytes) {
   return glance::ensure_smem(reinterpret_cast<const void*>(f), bytes);
 }
 
-// How many CTAs split K: with two CTAs to an SM the grid should come near
-// 2 x SMs, and a CTA should keep at least two stages.
+// Clusters of `size` CTAs of the few-rows kernel that the device holds at once
+// (asked once per device, form and size).
+template <int kRows>
+int max_clusters(int size) {
+  static int known[64][kMaxSplit + 1] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev][size];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size * glance::num_sms()));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = Few<kRows>::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, q8_linear_few_kernel<kRows>, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      n = -1;
+    }
+  }
+  return n;
+}
+
+// How many CTAs split K: as many as the device holds at once (a cluster that has
+// to wait for another's end doubles the time), each with two stages at least.
+template <int kRows>
 int choose_split(int tiles, int blocks_m, int n_kb) {
-  const int room = 2 * glance::num_sms() / (tiles * blocks_m > 0 ? tiles * blocks_m : 1);
-  int s = room < 1 ? 1 : room > kMaxSplit ? kMaxSplit : room;
-  while (s > 1 && n_kb / s < 2) --s;
-  return s;
+  int best = 1;
+  for (int s = 2; s <= kMaxSplit && n_kb / s >= 2; ++s)
+    if (max_clusters<kRows>(s) >= static_cast<int64_t>(tiles) * blocks_m) best = s;
+  return best;
 }
 
 template <int kRows>
@@ -561,7 +684,7 @@ cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const Param
   cudaError_t e = raise(q8_linear_few_kernel<kRows>, C::kSmem);
   if (e != cudaSuccess) return e;
   const int per = p.gated ? 64 : kTile, tiles = (p.N + per - 1) / per, blocks_m = (p.M + kRows - 1) / kRows;
-  const int S = choose_split(tiles, blocks_m, p.n_kb);
+  const int S = choose_split<kRows>(tiles, blocks_m, p.n_kb);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * S), static_cast<unsigned>(blocks_m));
   cfg.blockDim = dim3(kFewThreads);
@@ -579,14 +702,15 @@ cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const Param
   return cudaLaunchKernelEx(&cfg, q8_linear_few_kernel<kRows>, mw, mx, p, S);
 }
 
+template <int kN>
 cudaError_t launch_wide(const CUtensorMap& mw, const CUtensorMap& mx, Params p, cudaStream_t s) {
-  cudaError_t e = raise(q8_linear_wide_kernel, kWideSmem);
+  cudaError_t e = raise(q8_linear_wide_kernel<kN>, kWideSmem);
   if (e != cudaSuccess) return e;
-  const int per = p.gated ? 128 : 256;
+  const int per = p.gated ? kN / 2 : kN;
   p.tiles_n = (p.N + per - 1) / per;
   p.tiles_m = (p.M + 255) / 256;
-  p.tiles = p.tiles_n * p.tiles_m;
-  const int pairs = glance::num_sms() / 2;
+  p.tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
+  const int64_t pairs = glance::num_sms() / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * static_cast<unsigned>(p.tiles < pairs ? p.tiles : pairs));
   cfg.blockDim = dim3(kWideThreads);
@@ -597,10 +721,19 @@ cudaError_t launch_wide(const CUtensorMap& mw, const CUtensorMap& mx, Params p, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_linear_wide_kernel, mw, mx, p);
+  return cudaLaunchKernelEx(&cfg, q8_linear_wide_kernel<kN>, mw, mx, p);
 }
 
-constexpr int kFewLimit = 256;  // rows up to which the few-rows kernel runs
+// 256 x 256 tiles of the many-rows kernel.
+int64_t wide_tiles(const Params& p) {
+  const int64_t per = p.gated ? 128 : 256;
+  return (p.N + per - 1) / per * ((p.M + 255) / 256);
+}
+// The few-rows kernel: up to a block of rows, and up to two while the other's
+// tiles would leave half of the SM pairs without work.
+bool takes_few(const Params& p) { return p.M <= kMaxRows || (p.M <= 2 * kMaxRows && 4 * wide_tiles(p) <= glance::num_sms()); }
+// Many rows: tiles half as wide while the wide ones leave half of the pairs without work.
+bool takes_narrow(const Params& p) { return 4 * wide_tiles(p) <= glance::num_sms(); }
 
 }  // namespace
 
@@ -650,14 +783,16 @@ extern "C" glance_status glance_q8_linear(const void* x, int64_t x_stride, const
   p.out = static_cast<char*>(out);
   p.r_stride = rs;
   p.o_stride = os;
-  const bool few = M <= kFewLimit;
+  const bool few = takes_few(p);
+  const bool narrow = !few && takes_narrow(p);
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   CUtensorMap mw, mx;
-  glance_status st = glance::make_map_u8(&mw, w, K, rows_w, w_stride, few ? kTile / 2 : kTile, who);
+  glance_status st = glance::make_map_u8(&mw, w, K, rows_w, w_stride, few || narrow ? kTile / 2 : kTile, who);
   if (st == GLANCE_OK) st = glance::make_map_u8(&mx, x, K, M, x_stride, few ? rows : kTile, who);
   if (st != GLANCE_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = !few         ? launch_wide(mw, mx, p, s)
+  const cudaError_t e = narrow       ? launch_wide<128>(mw, mx, p, s)
+                        : !few       ? launch_wide<256>(mw, mx, p, s)
                         : rows == 16 ? launch_few<16>(mw, mx, p, s)
                         : rows == 32 ? launch_few<32>(mw, mx, p, s)
                         : rows == 64 ? launch_few<64>(mw, mx, p, s)
