@@ -29,7 +29,10 @@
  * glance_row_sumsq), query / key norm with rotary positions of several axes
  * for any number of rows (glance_qk_norm_rope), and the round on K/V caches
  * held in 4 bits (glance_kv4_write_rows, glance_kv4_read_rows,
- * glance_kv4_tree_attention, glance_kv4_accept_commit).
+ * glance_kv4_tree_attention, glance_kv4_accept_commit), the target's dense
+ * layers in 8 bits (glance_q8_norm_rows, glance_q8_rows, glance_q8_read_rows,
+ * glance_q8_linear), and a sampled verify with top-k, top-p and min-p from rows
+ * of logits (glance_sample).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -85,7 +88,8 @@ typedef enum { GLANCE_F32 = 0, GLANCE_BF16 = 1 } glance_dtype;
 
 /* Device status word values (glance_device_status). */
 #define GLANCE_DEV_OK 0
-#define GLANCE_DEV_NONFINITE_LOGITS 1 /* a draft logit row held NaN or +-inf */
+#define GLANCE_DEV_NONFINITE_LOGITS 1 /* a draft logit row held NaN or +-inf, or a row of
+                                        glance_sample NaN, +inf or nothing but -inf */
 #define GLANCE_DEV_TREE_CAPACITY 2    /* the rows' K/V slots do not fit: T + rows > t_cap */
 #define GLANCE_DEV_BAD_TREE 3         /* a tree array was inconsistent */
 #define GLANCE_DEV_PIPELINE_TIMEOUT 4 /* a pipeline wait ran out of time (2 s) */
@@ -773,9 +777,9 @@ typedef enum {
  * of out_dtype, strides in elements; out may be the residual itself (with its
  * stride) and must overlap no other input.
  * The products are exact and summed in fp32, the epilogue is fp32, out is
- * rounded once. The results do not change from call to call, nor with the other
- * rows of the call for as long as M stays in one of the ranges 1 to 16, 17 to
- * 32, 33 to 64, 65 to 128 and so on of the kernels (the order of the sums does).
+ * rounded once. The results do not change from call to call. A row's result does
+ * not depend on the other rows, but the order of its sums may change with M, N
+ * and K.
  * A row of x (a weight row) with a code that is not a number or such a scale
  * makes NaN of that row (column) of out alone.
  * Limits: 1 <= M <= 2^24, N a multiple of 8 up to 2^22, K a multiple of 16 up
@@ -783,8 +787,9 @@ typedef enum {
  * multiples of 16 bytes, scales and bias 4-byte aligned.
  * The call is a programmatic dependent of the previous kernel in the stream: it
  * may read w (nothing else) before that kernel has finished, when that kernel
- * lets dependents start early (this library's attention and dense calls do; the
- * row calls above do not, so they may write w).
+ * lets dependents start early (this library's attention, dense, product and
+ * sampling calls do, none of which writes codes; the row calls above do not, so
+ * they may write w).
  */
 glance_status glance_q8_linear(const void* x, int64_t x_stride, const float* x_scale, int M,
                                const void* w, int64_t w_stride, const float* w_scale, int N, int K,
@@ -854,8 +859,8 @@ glance_status glance_reset_device_status(void);
  * into status_out[1..5] (tree build, tree attention, LM head, walk + commit,
  * dense layers) and a one-thread kernel that stores the first non-zero of
  * them in status_out[0] (0 if none). The 4-bit attention reports with tree
- * attention, the other 4-bit calls with walk + commit, glance_qk_norm_rope
- * with the dense layers. status_out: GLANCE_STATUS_WORDS int32,
+ * attention, the other 4-bit calls with walk + commit, glance_qk_norm_rope and
+ * the 8-bit calls with the dense layers, glance_sample with the LM head. status_out: GLANCE_STATUS_WORDS int32,
  * device memory or pinned / managed host memory (the caller reads it once
  * the stream has reached this point). No host or device-wide synchronisation,
  * so a serving loop can append it to every captured round. The words are not

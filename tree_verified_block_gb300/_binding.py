@@ -796,21 +796,34 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 
-def _matrix(x, dtypes, what, dev, shape=None):
+def _bad(what):
+    return ValueError("glance: " + what)
+
+
+def _matrix(x, shape, what, dev):
     """(address, elements between rows) of a matrix whose rows lie in one piece each."""
-    if x.dtype not in dtypes or x.dim() != 2 or x.stride(1) != 1 and x.shape[1] > 1 or shape is not None and x.shape != shape:
-        raise ValueError(f"glance: {what}")
+    if x.shape != shape:
+        raise _bad(what)
+    step, unit = x.stride()
+    if unit != 1:
+        raise _bad(what)
     if x.get_device() != dev:
         raise _elsewhere()
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return x.data_ptr(), step if shape[0] > 1 else shape[1]
 
 
 def _floats(x, n, what, dev):
     if x.dtype is not _F32T or x.numel() != n or not x.is_contiguous():
-        raise ValueError(f"glance: {what}")
+        raise _bad(what)
     if x.get_device() != dev:
         raise _elsewhere()
     return x.data_ptr()
+
+
+def _codes(x, shape, what, dev):
+    if x.dtype not in _CODES:
+        raise _bad(what)
+    return _matrix(x, shape, what, dev)
 
 
 _CODES_TEXT = "codes must be uint8 or float8_e4m3fn of the rows' shape"
@@ -818,49 +831,69 @@ _SCALES_TEXT = "scales must be contiguous float32, one per row"
 _ROWS_TEXT = "x, residual and total must be float32 or bfloat16 [M, d], all of one type"
 
 
+def _rows_of(x, what):
+    """(shape, type's number) of a matrix of floats."""
+    shape, dtype = x.shape, _DTYPES.get(x.dtype)
+    if dtype is None or len(shape) != 2:
+        raise _bad(what)
+    return shape, dtype
+
+
 def q8_rows(x, codes, scales, stream=None):
     """codes (uint8 or float8_e4m3fn [M, d]), scales (float32 [M]) <- rows of x [M, d]: e4m3 with a power-of-two scale per row."""
-    dev, (M, d) = x.get_device(), x.shape
-    (xp, xs), (cp, cs) = _matrix(x, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, x.shape)
-    _check(lib().glance_q8_rows(xp, xs, _DTYPES[x.dtype], M, d, cp, cs, _floats(scales, M, _SCALES_TEXT, dev), _on(stream, dev)))
+    dev, (shape, dtype) = x.get_device(), _rows_of(x, _ROWS_TEXT)
+    (xp, xs), (cp, cs) = _matrix(x, shape, _ROWS_TEXT, dev), _codes(codes, shape, _CODES_TEXT, dev)
+    _check(lib().glance_q8_rows(xp, xs, dtype, shape[0], shape[1], cp, cs, _floats(scales, shape[0], _SCALES_TEXT, dev), _on(stream, dev)))
 
 
 def q8_norm_rows(x, residual, weight, eps, total, codes, scales, stream=None):
     """total <- x + residual (either None; total may be x or residual), codes and scales <- its RMS-normed rows times weight
     (float32 [d] or None), in e4m3 with a power-of-two scale per row."""
-    dev, (M, d) = x.get_device(), x.shape
-    one = (x.dtype,)
-    (xp, xs), (cp, cs) = _matrix(x, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, x.shape)
-    rp, rs = (None, 0) if residual is None else _matrix(residual, one, _ROWS_TEXT, dev, x.shape)
-    tp, ts = (None, 0) if total is None else _matrix(total, one, _ROWS_TEXT, dev, x.shape)
-    wp = None if weight is None else _floats(weight, d, "weight must be contiguous float32 [d]", dev)
-    _check(lib().glance_q8_norm_rows(xp, xs, rp, rs, _DTYPES[x.dtype], M, d, wp, eps, tp, ts, cp, cs,
-                                     _floats(scales, M, _SCALES_TEXT, dev), _on(stream, dev)))
+    dev, (shape, dtype) = x.get_device(), _rows_of(x, _ROWS_TEXT)
+    (M, d), one = shape, x.dtype
+    (xp, xs), (cp, cs) = _matrix(x, shape, _ROWS_TEXT, dev), _codes(codes, shape, _CODES_TEXT, dev)
+    rp, rs, tp, ts = None, 0, None, 0
+    if residual is not None:
+        if residual.dtype is not one:
+            raise _bad(_ROWS_TEXT)
+        rp, rs = _matrix(residual, shape, _ROWS_TEXT, dev)
+    if total is not None:
+        if total.dtype is not one:
+            raise _bad(_ROWS_TEXT)
+        tp, ts = _matrix(total, shape, _ROWS_TEXT, dev)
+    _check(lib().glance_q8_norm_rows(xp, xs, rp, rs, dtype, M, d,
+                                     None if weight is None else _floats(weight, d, "weight must be contiguous float32 [d]", dev),
+                                     eps, tp, ts, cp, cs, _floats(scales, M, _SCALES_TEXT, dev), _on(stream, dev)))
 
 
 def q8_read_rows(codes, scales, out, stream=None):
     """out [M, d] (float32 or bfloat16) = code * scale."""
-    dev, (M, d) = out.get_device(), out.shape
-    (op, os_), (cp, cs) = _matrix(out, _DTYPES, _ROWS_TEXT, dev), _matrix(codes, _CODES, _CODES_TEXT, dev, out.shape)
-    _check(lib().glance_q8_read_rows(cp, cs, _floats(scales, M, _SCALES_TEXT, dev), _DTYPES[out.dtype], M, d, op, os_,
+    dev, (shape, dtype) = out.get_device(), _rows_of(out, _ROWS_TEXT)
+    (op, os_), (cp, cs) = _matrix(out, shape, _ROWS_TEXT, dev), _codes(codes, shape, _CODES_TEXT, dev)
+    _check(lib().glance_q8_read_rows(cp, cs, _floats(scales, shape[0], _SCALES_TEXT, dev), dtype, shape[0], shape[1], op, os_,
                                      _on(stream, dev)))
 
 
 def q8_linear(x, x_scale, w, w_scale, out, bias=None, act="none", gated=False, residual=None, stream=None):
     """out [M, N] (float32 or bfloat16) = act(x_scale x . w w_scale + bias) + residual: x [M, K] and w [N, K] codes of the row
     calls (or any e4m3), w_scale and bias float32 [N]. gated: w [2 N, K], gate rows then up rows, out = act(gate) * up."""
-    dev, (M, N), K = out.get_device(), out.shape, x.shape[1]
-    rows = 2 * N if gated else N
-    if act not in ACTS:
-        raise ValueError("glance: act must be one of " + ", ".join(ACTS))
-    (op, os_), (xp, xs) = _matrix(out, _DTYPES, "out must be float32 or bfloat16 [M, N]", dev), _matrix(
-        x, _CODES, "x must be uint8 or float8_e4m3fn [M, K]", dev, (M, K))
-    wp, wst = _matrix(w, _CODES, "w must be uint8 or float8_e4m3fn [N, K] (gated: [2 N, K])", dev, (rows, K))
-    rp, rs = (None, 0) if residual is None else _matrix(residual, (out.dtype,), "residual must be of out's shape and type", dev, out.shape)
+    dev, (shape, dtype) = out.get_device(), _rows_of(out, "out must be float32 or bfloat16 [M, N]")
+    (M, N), K = shape, x.shape[-1]
+    rows, kind = 2 * N if gated else N, ACTS.get(act)
+    if kind is None:
+        raise _bad("act must be one of " + ", ".join(ACTS))
+    (op, os_), (xp, xs) = _matrix(out, shape, "out must have its rows in one piece each", dev), _codes(
+        x, (M, K), "x must be uint8 or float8_e4m3fn [M, K]", dev)
+    wp, wst = _codes(w, (rows, K), "w must be uint8 or float8_e4m3fn [N, K] (gated: [2 N, K])", dev)
+    rp, rs = None, 0
+    if residual is not None:
+        if residual.dtype is not out.dtype:
+            raise _bad("residual must be of out's shape and type")
+        rp, rs = _matrix(residual, shape, "residual must be of out's shape and type", dev)
     _check(lib().glance_q8_linear(xp, xs, _floats(x_scale, M, "x_scale must be contiguous float32 [M]", dev), M, wp, wst,
-                                  _floats(w_scale, rows, "w_scale must be contiguous float32, one per row of w", dev), N, K, bool(gated),
-                                  ACTS[act], None if bias is None else _floats(bias, rows, "bias must be contiguous float32, one per row of w", dev),
-                                  rp, rs, op, os_, _DTYPES[out.dtype], _on(stream, dev)))
+                                  _floats(w_scale, rows, "w_scale must be contiguous float32, one per row of w", dev), N, K, 1 if gated else 0,
+                                  kind, None if bias is None else _floats(bias, rows, "bias must be contiguous float32, one per row of w", dev),
+                                  rp, rs, op, os_, dtype, _on(stream, dev)))
 
 
 def _per_row(x, dtype, M, dev):
@@ -877,11 +910,11 @@ def _per_row(x, dtype, M, dev):
 def sample(logits, temperature, top_k, top_p, min_p, seed, position, seq, tokens, gap=None, stream=None):
     """tokens (int32 [M]) drawn from rows of logits [M, V] (float32 or bfloat16) with each row's temperature (0: argmax), top_k,
     top_p and min_p (tensors [M] or None), the noise keyed by (seed, position[row], seq[row]) as in lmhead_sample."""
-    dev, (M, V) = logits.get_device(), logits.shape
-    lp, ls = _matrix(logits, _DTYPES, "logits must be float32 or bfloat16 [M, V]", dev)
+    dev, (shape, dtype) = logits.get_device(), _rows_of(logits, "logits must be float32 or bfloat16 [M, V]")
+    (M, V), (lp, ls) = shape, _matrix(logits, shape, "logits must have their rows in one piece each", dev)
     if position is None or tokens is None:
         raise ValueError("glance: position and tokens are required")
-    _check(lib().glance_sample(lp, ls, _DTYPES[logits.dtype], M, V, _per_row(temperature, _F32T, M, dev), _per_row(top_k, _I32, M, dev),
+    _check(lib().glance_sample(lp, ls, dtype, M, V, _per_row(temperature, _F32T, M, dev), _per_row(top_k, _I32, M, dev),
                                _per_row(top_p, _F32T, M, dev), _per_row(min_p, _F32T, M, dev), int(seed) & ((1 << 64) - 1),
                                _per_row(position, _I32, M, dev), _per_row(seq, _I32, M, dev), _per_row(tokens, _I32, M, dev),
                                _per_row(gap, _F32T, M, dev), _on(stream, dev)))

@@ -29,8 +29,9 @@
 // are outside the histogram: 2^18 of them hold 4e-9 of the sum, under what an
 // fp32 top_p can name.
 //
-// The draw's values are fp32 and compared in fp32 except for those that are near
-// the best: these are evaluated again in fp64, so that rounding decides nothing.
+// The draw's values are fp32 and compared in fp32 but for the foremost two and what
+// comes near the second: these are evaluated again in fp64, so that rounding
+// decides next to nothing, and the gap, which may be small, is good to 1e-9.
 // Most tokens need no logarithm: g >= t only if 1 - u <= e^-t, and once there are
 // two values the noise's own bits decide.
 //
@@ -122,10 +123,9 @@ struct Border {  // the bin in which a prefix ends
   uint32_t count_before, count_in;
   Mass mass_before, mass_all;
 };
-struct Best {
-  float z1, z2;  // the two best values, of
-  int id;        // the best one's token
-  float l;       // and its logit
+struct Entry {  // a token, its logit and its value in the draw
+  float z, l;
+  int id;
 };
 struct Cut {
   uint64_t number;  // the last token that is kept
@@ -143,11 +143,6 @@ struct Shared {
     struct {  // of a search in the list's tokens: a bin's weight in two parts
       uint32_t bin_count[kThreads], bin_low[kThreads], bin_high[kThreads];
     };
-    struct {  // of the draw
-      double near_z[kThreads];
-      float near_l[kThreads];
-      int near_id[kThreads];
-    };
   };
   uint64_t mine[kCtas > 1 ? kList : 1];  // numbers of tokens on their way to the first CTA's list
   // written by the cluster's other CTAs
@@ -155,13 +150,13 @@ struct Shared {
   float group[kGroups];
   Mass coarse_mass[kCtas][kCoarse + 1];  // [kCoarse]: of tokens without a bin
   uint32_t coarse_count[kCtas][kCoarse];
-  Best peer_best[kCtas];
+  Entry peer_best[2 * kCtas];
   uint64_t peer_lo[kCtas], peer_hi[kCtas];
   Cut cut;
   int found;
   uint32_t list_n[3];
   // this CTA's own
-  uint32_t near_n, part_n, mine_n, mine_at;
+  uint32_t part_n, mine_n, mine_at;
   uint32_t second;  // key of a value that two of the draw's are no less than
   int part[kThreads];  // the threads whose tokens are looked at again
   Border border;
@@ -171,7 +166,7 @@ struct Shared {
   uint32_t warp_count[kWarps];
   float warp_f[kWarps], warp_second[kWarps];
   uint64_t warp_lo[kWarps], warp_hi[kWarps];
-  Best warp_best[kWarps];
+  Entry warp_best[2 * kWarps];
   float min_l;
   double log_min_p;
 };
@@ -359,7 +354,8 @@ __device__ __forceinline__ float least_of_bin(const Row& w, int bin) {
 
 __device__ __forceinline__ float most_of_bin(const Row& w, int bin) {
   const float x = (static_cast<float>(bin) - 0.51f) / kBinsPerNat / w.r;
-  return w.top - x + 1e-6f * (fabsf(w.top) + fabsf(x));
+  const float most = w.top - x + 1e-6f * (fabsf(w.top) + fabsf(x));
+  return most == most ? most : INFINITY;  // (x beyond fp32's range: no bound)
 }
 
 template <int kCtas>
@@ -653,35 +649,36 @@ __device__ uint32_t gather(Shared<kCtas>* s, const Row& w, int turn, float least
 // ------------------------------------------------------------------- the draw
 
 __device__ __forceinline__ bool ahead(float z, int id, float z0, int id0) { return z > z0 || (z == z0 && id < id0); }
-__device__ __forceinline__ void merge(Best& a, const Best& b) {
-  if (ahead(b.z1, b.id, a.z1, a.id)) {
-    a = Best{b.z1, fmaxf(a.z1, b.z2), b.id, b.l};
-  } else {
-    a.z2 = fmaxf(a.z2, b.z1);
-  }
-}
-__device__ __forceinline__ Best warp_best(Best v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    merge(v, Best{__shfl_xor_sync(0xffffffffu, v.z1, o), __shfl_xor_sync(0xffffffffu, v.z2, o), __shfl_xor_sync(0xffffffffu, v.id, o),
-                  __shfl_xor_sync(0xffffffffu, v.l, o)});
-  return v;
-}
 constexpr int kNoId = 0x7FFFFFFF;
+__device__ __forceinline__ Entry no_entry() { return Entry{-INFINITY, 0.f, kNoId}; }
+// The foremost of a warp's entries, and whose it is.
+__device__ __forceinline__ Entry warp_first(const Entry& e, int& lane) {
+  const uint32_t key = ord_key(e.z), most = __reduce_max_sync(0xffffffffu, key);
+  const uint32_t id = __reduce_min_sync(0xffffffffu, key == most ? static_cast<uint32_t>(e.id) : ~0u);
+  lane = __ffs(__ballot_sync(0xffffffffu, key == most && static_cast<uint32_t>(e.id) == id)) - 1;
+  return Entry{__shfl_sync(0xffffffffu, e.z, lane), __shfl_sync(0xffffffffu, e.l, lane), static_cast<int>(id)};
+}
 
 // The two best values that a thread has seen, with their tokens.
 struct Two {
-  float z[2], l[2];
-  int id[2];
+  Entry e[2];
 };
-__device__ __forceinline__ Two no_two() { return Two{{-INFINITY, -INFINITY}, {0.f, 0.f}, {kNoId, kNoId}}; }
+__device__ __forceinline__ Two no_two() { return Two{{no_entry(), no_entry()}}; }
 __device__ __forceinline__ void fold(Two& t, float z, float l, int id) {
-  if (ahead(z, id, t.z[0], t.id[0])) {
-    t.z[1] = t.z[0], t.l[1] = t.l[0], t.id[1] = t.id[0];
-    t.z[0] = z, t.l[0] = l, t.id[0] = id;
-  } else if (ahead(z, id, t.z[1], t.id[1])) {
-    t.z[1] = z, t.l[1] = l, t.id[1] = id;
+  if (ahead(z, id, t.e[0].z, t.e[0].id)) {
+    t.e[1] = t.e[0];
+    t.e[0] = Entry{z, l, id};
+  } else if (ahead(z, id, t.e[1].z, t.e[1].id)) {
+    t.e[1] = Entry{z, l, id};
   }
+}
+// A warp's two best of its threads' two best.
+__device__ __forceinline__ Two warp_two(const Two& t) {
+  int lane;
+  Two b;
+  b.e[0] = warp_first(t.e[0], lane);
+  b.e[1] = warp_first((threadIdx.x & 31) == static_cast<unsigned>(lane) ? t.e[1] : t.e[0], lane);
+  return b;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
@@ -691,99 +688,81 @@ struct Key {  // of the row's noise
 __device__ __forceinline__ uint4 noise4(const Key& k, int id) {
   return philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, k.pos, k.seq, 0u), k.k0, k.k1);
 }
-// The draw's value of a token in 64 bits.
+// ln a of a normal a > 0, to about 1e-11: a = 2^e m, m in [sqrt 1/2, sqrt 2), ln m =
+// 2 artanh s with s = (m - 1) / (m + 1) as the sum of two floats, its terms from s^5
+// on in fp32 (below 4e-5). Few operations are fp64: an SM has two such units, and
+// the general logarithm's chain took 1.3 us of a call with one row.
+__device__ __forceinline__ double ln_of(float a) {
+  const uint32_t bits = __float_as_uint(a);
+  const int e = (static_cast<int>(bits) - 0x3F3504F3) >> 23;
+  const float m = __uint_as_float(bits - (static_cast<uint32_t>(e) << 23));
+  const float num = m - 1.f, den = m + 1.f, den_low = m - (den - 1.f);  // num and den + den_low are exact
+  const float q = num / den, low = fmaf(-q, den_low, fmaf(-q, den, num)) / den, q2 = q * q;
+  const float tail = q2 * q2 * q * fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 0.2f);
+  const double s = static_cast<double>(q) + static_cast<double>(low);
+  return fma(static_cast<double>(e), 0.69314718055994530942, 2.0 * (s + fma(s * s * s, 1.0 / 3, static_cast<double>(tail))));
+}
+// The draw's value of a token, to 1e-9.
 __device__ __noinline__ double value64(const Row& w, const Key& k, float l, int id) {
   const uint32_t word = word_of(noise4(k, id), id & 3);
-  const double u = (static_cast<double>(word >> 9) + 0.5) * (1.0 / 8388608.0);
-  return (static_cast<double>(l) - static_cast<double>(w.top)) * static_cast<double>(w.r) - log(-log(u));
+  const double y = -ln_of((static_cast<float>(word >> 9) + 0.5f) * (1.f / 8388608.f));
+  const float high = static_cast<float>(y), low = static_cast<float>(y - static_cast<double>(high));
+  const double ln_y = ln_of(high) + static_cast<double>(low / high);
+  return fma(static_cast<double>(l) - static_cast<double>(w.top), static_cast<double>(w.r), -ln_y);
 }
-// Values within the rounding of the best, fp32's and the noise's.
-__device__ __forceinline__ float near_best(float z) { return z - (2e-5f + 1e-6f * fabsf(z)); }
-
-// The best of a warp's values of which several are near the best: these in fp64.
-__device__ Best near_of_warp(const Row& w, const Key& key, const Best& mine, bool near) {
-  const double z = near ? value64(w, key, mine.l, mine.id) : -INFINITY;
-  __syncwarp();
-  double best = z;
-  int id = near ? mine.id : kNoId;
+// The row's token, by a warp that holds the entries that it can be: the two best
+// and what comes within the rounding of the second (fp32's and the noise's) are
+// evaluated again in fp64, which decides between them and gives the gap.
+__device__ void decide(const Params& p, const Row& w, const Key& key, const Entry& e, bool exact, int row) {
+  const int lane = threadIdx.x & 31;
+  int at, next;
+  const Entry a = warp_first(e, at), b = warp_first(lane == at ? no_entry() : e, next);
+  int id = a.id;
+  float gap = a.z - b.z;
+  if (!exact && b.z > -INFINITY) {
+    const float near = b.z - (2e-5f + 1e-6f * fabsf(b.z));
+    const double z = e.z >= near ? value64(w, key, e.l, e.id) : -INFINITY;
+    __syncwarp();
+    double best = z;
+    id = e.z >= near ? e.id : kNoId;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const double u = __shfl_xor_sync(0xffffffffu, best, o);
-    const int i = __shfl_xor_sync(0xffffffffu, id, o);
-    if (u > best || (u == best && i < id)) best = u, id = i;
+    for (int o = 16; o; o >>= 1) {
+      const double u = __shfl_xor_sync(0xffffffffu, best, o);
+      const int i = __shfl_xor_sync(0xffffffffu, id, o);
+      if (u > best || (u == best && i < id)) best = u, id = i;
+    }
+    double second = e.id == id ? -INFINITY : z;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) second = fmax(second, __shfl_xor_sync(0xffffffffu, second, o));
+    gap = static_cast<float>(best - second);
   }
-  // the second best: another lane's, or the best one's own second
-  float second = near ? (mine.id == id ? mine.z2 : static_cast<float>(z)) : mine.z1;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, o));
-  return Best{static_cast<float>(best), second, id, 0.f};
+  if (lane == 0 && GLANCE_IN_BOUNDS(row, p.M)) {
+    p.tokens[row] = id;
+    if (p.gap) p.gap[row] = gap;
+  }
 }
 
-// The block's best of its threads' two best values, near ones compared in fp64.
+// From the threads' two best values to the row's token. alone: the first CTA's
+// threads have all that counts.
 template <int kCtas>
-__device__ Best block_best(Shared<kCtas>* s, const Row& w, const Key& key, const Two& t, bool exact) {
+__device__ void finish(Shared<kCtas>* s, const Params& p, const Row& w, const Key& key, const Two& t, bool exact, bool alone, int row) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncwarp();
-  Best b = warp_best(Best{t.z[0], t.z[1], t.id[0], t.l[0]});
-  if (lane == 0) s->warp_best[warp] = b;
-  if (threadIdx.x == 0) s->near_n = 0;
+  Two b = warp_two(t);
+  if (lane < 2) s->warp_best[2 * warp + lane] = lane ? b.e[1] : b.e[0];
   __syncthreads();
-  b = warp_best(lane < kWarps ? s->warp_best[lane] : Best{-INFINITY, -INFINITY, kNoId, 0.f});
-  // the same for all threads
-  if (exact || b.z1 == -INFINITY || !(b.z2 >= near_best(b.z1))) return b;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (t.z[j] >= near_best(b.z1)) {
-      const uint32_t at = atomicAdd(&s->near_n, 1u);
-      if (at < kThreads) {
-        s->near_l[at] = t.l[j];
-        s->near_id[at] = t.id[j];
-      }
-    }
-  __syncthreads();
-  const int n = min(s->near_n, static_cast<uint32_t>(kThreads));
-  if (static_cast<int>(threadIdx.x) < n) s->near_z[threadIdx.x] = value64(w, key, s->near_l[threadIdx.x], s->near_id[threadIdx.x]);
-  __syncthreads();
-  double z1 = -INFINITY, z2 = -INFINITY;
-  int at = 0;
-  for (int i = 0; i < n; ++i) {
-    const double z = s->near_z[i];
-    if (i == 0 || z > z1 || (z == z1 && s->near_id[i] < s->near_id[at])) {
-      z2 = z1;
-      z1 = z;
-      at = i;
-    } else if (z > z2) {
-      z2 = z;
-    }
-  }
-  return Best{static_cast<float>(z1), static_cast<float>(z2), s->near_id[at], s->near_l[at]};
-}
-
-__device__ __forceinline__ void write_row(const Params& p, int row, const Best& b) {
-  if (GLANCE_IN_BOUNDS(row, p.M)) {
-    p.tokens[row] = b.id;
-    if (p.gap) p.gap[row] = fmaxf(b.z1 - b.z2, 0.f);
-  }
-}
-
-// From every CTA's best to the row's token, by the first CTA.
-template <int kCtas>
-__device__ void finish(Shared<kCtas>* s, const Params& p, const Row& w, const Key& key, const Two& t, bool exact, int row) {
-  Best b = block_best(s, w, key, t, exact);
-  if (kCtas == 1) {
-    if (threadIdx.x == 0) write_row(p, row, b);
+  if (kCtas == 1 || alone) {
+    if (warp == 0) decide(p, w, key, s->warp_best[lane], exact, row);
     return;
   }
-  if (threadIdx.x == 0) to_peer<kCtas>(&s->peer_best[w.rank], 0, b);
+  if (warp == 0) {
+    b = warp_two(Two{{s->warp_best[lane], no_entry()}});
+    if (lane < 2) to_peer<kCtas>(&s->peer_best[2 * w.rank + lane], 0, lane ? b.e[1] : b.e[0]);
+  }
   sync_row<kCtas>();
-  if (w.rank != 0 || threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  const Best mine = lane < kCtas ? s->peer_best[lane] : Best{-INFINITY, -INFINITY, kNoId, 0.f};
-  b = warp_best(mine);
-  const bool near = mine.z1 >= near_best(b.z1);
-  if (!exact && __popc(__ballot_sync(0xffffffffu, near)) > 1) b = near_of_warp(w, key, mine, near);
-  if (lane == 0) write_row(p, row, b);
+  if (w.rank == 0 && warp == 0) decide(p, w, key, lane < 2 * kCtas ? s->peer_best[lane] : no_entry(), exact, row);
 }
+static_assert(2 * kWarps == 32, "a block's entries are a warp's");
 
 // The first CTA draws from its list of n tokens: the first `want` of them (0:
 // all), of these `share` of the weight (of mass_all, or of theirs if it is 0).
@@ -805,11 +784,7 @@ __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, 
     const Mass upto = scan_add(m, t), all = mass_all ? mass_all : __shfl_sync(0xffffffffu, upto, 31);
     if (t < kept && (all_p || upto - m < part_of(all, share))) draw(number);
     __syncwarp();
-    const Best mine = {two.z[0], -INFINITY, two.id[0], two.l[0]};
-    Best b = warp_best(mine);
-    const bool near = mine.z1 >= near_best(b.z1);
-    if (__popc(__ballot_sync(0xffffffffu, near)) > 1) b = near_of_warp(w, key, mine, near);
-    if (t == 0) write_row(p, row, b);
+    decide(p, w, key, two.e[0], false, row);
     return;
   }
   Held h = hold_list(s, w, n, !all_p);
@@ -838,8 +813,7 @@ __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, 
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
     if (h.number[j] >= cut) draw(h.number[j]);
-  const Best b = block_best(s, w, key, two, false);
-  if (t == 0) write_row(p, row, b);
+  finish(s, p, w, key, two, false, true, row);
 }
 
 // The last token that a prefix keeps, and the weight up to it: the tokens of the
@@ -1166,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
           }
         },
         [&] {
-          const uint32_t z0 = ord_key(two.z[0]), z1 = ord_key(two.z[1]);
+          const uint32_t z0 = ord_key(two.e[0].z), z1 = ord_key(two.e[1].z);
           const uint32_t best = __reduce_max_sync(0xffffffffu, z0);
           const unsigned who = __ballot_sync(0xffffffffu, z0 == best);
           const uint32_t next = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? z1 : z0);
@@ -1176,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
           reach = fmaxf(least, w.top + (second - 16.8f) / w.r - 1e-5f * fabsf(w.top));
         });
   }
-  finish(s, p, w, key, two, greedy, row);
+  finish(s, p, w, key, two, greedy, false, row);
 }
 
 // CTAs to a row: 16 while two such clusters' CTAs have an SM each, 4 beyond, as
