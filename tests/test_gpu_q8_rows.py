@@ -96,7 +96,7 @@ def test_rows_of_any_magnitude(dev, clean_status):
         for i, f in enumerate((1.0, 2.0 ** 70, 2.0 ** 120, 2.0 ** -70, 2.0 ** -100, 0.0, 2.0 ** 64)):
             x[i] *= f
         codes, scales = empty8(7, d, 0, dev), torch.zeros(7, device=dev)
-        for eps in (1e-6, 1e-30):
+        for eps in (1e-6, 1e-30, 1e-36):
             g.q8_norm_rows(x, None, None, eps, None, codes, scales)
             check_values(q8.norm_rows(f64(x), None, float(np.float32(eps))), q8.code_values(codes.cpu().numpy()) * f64(scales)[:, None], f64(scales))
             assert torch.all(codes[5] & 127 == 0) and scales[5] == 1

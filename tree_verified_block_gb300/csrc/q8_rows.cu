@@ -63,17 +63,23 @@ struct Vec<float> {
   }
 };
 
-// What a row's threads reduce: the sum of squares and the largest magnitudes
-// (as bits: in the order of the magnitudes, NaN above infinity) of s and of s w.
+// What a row's threads reduce: the sum of squares, and the largest magnitude of
+// s w (NaN if one is).
 struct Stats {
-  float ss;
-  uint32_t top_s, top_p;
+  float ss, top;
 };
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+template <bool kNorm>
 __device__ __forceinline__ Stats warp_stats(Stats v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v.ss += __shfl_xor_sync(0xffffffffu, v.ss, o);
-  v.top_s = __reduce_max_sync(0xffffffffu, v.top_s);
-  v.top_p = __reduce_max_sync(0xffffffffu, v.top_p);
+  for (int o = 16; o; o >>= 1) {
+    if (kNorm) v.ss += __shfl_xor_sync(0xffffffffu, v.ss, o);
+    v.top = max_nan(v.top, __shfl_xor_sync(0xffffffffu, v.top, o));
+  }
   return v;
 }
 
@@ -135,65 +141,67 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) q8_rows_
       }
     }
   };
-  Stats st = {0.f, 0u, 0u};
+  const auto stats = [&] {
+    Stats st = {0.f, 0.f};
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    float w[kN];
-    if (kNorm) weights(t + v * nt, w);
+    for (int v = 0; v < kVecs; ++v) {
+      float w[kN];
+      if (kNorm) weights(t + v * nt, w);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      st.top_s = max(st.top_s, __float_as_uint(s[v][i]) & 0x7FFFFFFFu);
-      if (kNorm) {
-        st.ss = fmaf(s[v][i], s[v][i], st.ss);
-        st.top_p = max(st.top_p, __float_as_uint(s[v][i] * w[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < kN; ++i) {
+        if (kNorm) st.ss = fmaf(s[v][i], s[v][i], st.ss);
+        st.top = max_nan(st.top, fabsf(kNorm ? s[v][i] * w[i] : s[v][i]));
       }
     }
-  }
+    return st;
+  };
   int phase = 0;
   const auto reduce = [&](Stats v) {
-    v = warp_stats(v);
+    v = warp_stats<kNorm>(v);
     if (kWarp) return v;
     if (lane == 0) s_stats[phase][warp] = v;
     __syncthreads();
-    v = {0.f, 0u, 0u};
+    v = {0.f, 0.f};
     if (lane < nt / 32) v = s_stats[phase][lane];
     phase ^= 1;
-    return warp_stats(v);
+    return warp_stats<kNorm>(v);
   };
-  st = reduce(st);
-  const bool finite = st.top_s < 0x7F800000u;
+  Stats st = reduce(stats());
   float factor = 1.f;  // y = s w factor
-  float pre = 1.f;     // a power of two that s is multiplied by first
-  uint32_t top = st.top_s;
   if (kNorm) {
-    // squares beyond fp32's range, or lost below it: once more with the row's
-    // largest magnitude brought to [1, 2)
-    if (finite && !(st.ss <= 1e37f && (st.ss >= 1e-18f || p.eps >= 1e-12f)) && st.top_s >= 0x00800000u) {
-      const int e = static_cast<int>(st.top_s >> 23) - 127;
-      pre = __uint_as_float(static_cast<uint32_t>(min(126, max(-126, -e)) + 127) << 23);
-      st = {0.f, st.top_s, 0u};
+    float eps = p.eps;
+    // squares beyond fp32's range, or lost below it where eps does not outweigh
+    // them: once more with the row's largest magnitude brought to [1, 2), or up by
+    // 2^100 (eps then stays in range)
+    if (!(st.ss <= 1e37f && (st.ss >= 1e-18f || eps >= 1e-30f))) {
+      float top = 0.f;
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        float w[kN];
-        weights(t + v * nt, w);
+      for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float z = s[v][i] * pre;
-          st.ss = fmaf(z, z, st.ss);
-          st.top_p = max(st.top_p, __float_as_uint(z * w[i]) & 0x7FFFFFFFu);
-        }
+        for (int i = 0; i < kN; ++i) top = max_nan(top, fabsf(s[v][i]));
+      top = reduce(Stats{0.f, top}).top;
+      if (top >= 1.17549435e-38f && top < INFINITY) {
+        const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        const float pre = __uint_as_float(static_cast<uint32_t>(min(100, max(-126, -e)) + 127) << 23);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) s[v][i] *= pre;
+        eps = eps * pre * pre;
+        st = reduce(stats());
       }
-      st = reduce(st);
     }
-    factor = 1.f / sqrtf(fmaf(st.ss, p.inv_d, p.eps * pre * pre));
-    top = __float_as_uint(__uint_as_float(st.top_p) * factor);
+    factor = 1.f / sqrtf(fmaf(st.ss, p.inv_d, eps));
   }
   // e from the bits of the largest magnitude: 448 = 1.75 * 2^8
+  const float most = st.top * factor;
+  const uint32_t top = __float_as_uint(most);
   int e = static_cast<int>(top >> 23) - 135 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   e = top == 0u ? 0 : max(e, -126);
-  const bool valid = finite && top < 0x7F800000u;
+  const bool valid = most < INFINITY;  // (not NaN)
   if (t == 0 && GLANCE_IN_BOUNDS(row, p.M)) p.scales[row] = valid ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : NAN;
   const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const float scaled = factor * down;  // a power of two: s w scaled rounds where s w factor does
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     const int at = t + v * nt;
@@ -204,11 +212,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) q8_rows_
     for (int i = 0; i < kN; i += 4) {
       float y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = kNorm ? s[v][i + j] * pre * w[i + j] * factor * down : s[v][i + j] * down;
-        if (!valid) y[j] = 0.f;
-      }
-      c[i / 4] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
+      for (int j = 0; j < 4; ++j) y[j] = kNorm ? s[v][i + j] * w[i + j] * scaled : s[v][i + j] * down;
+      c[i / 4] = valid ? pack_e4m3x4(y[0], y[1], y[2], y[3]) : 0u;
     }
     if (at >= p.vecs || !GLANCE_IN_BOUNDS(row, p.M)) continue;
     unsigned char* dst = p.codes + r * p.c_stride + static_cast<int64_t>(at) * kN;
