@@ -4,9 +4,9 @@ Tokens have to be the oracle's, also where two values are close (the kernel
 compares those in 64 bits). Where a token's place at top_p's border is nearer to
 it than weights are good to, 2^-21 of the sum (a weight to 2^-23 and its step's
 rounding, sums in 64 bits), it is the oracle's draw with the border to either
-side. The gap is the difference of two values that are good to 1e-9 (logarithms
-of a series with terms below 4e-5 in fp32, 4e-5 * 2^-21, over -ln u; products in
-64 bits), rounded to fp32."""
+side. The gap is the difference of two values that are good to 1e-9 each (pairs
+of floats; logarithms to 1e-10, of -ln u relatively: over 0.35 at the least where
+its series is longest), rounded to fp32."""
 import numpy as np
 import pytest
 import torch

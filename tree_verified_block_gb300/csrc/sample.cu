@@ -30,8 +30,8 @@
 // fp32 top_p can name.
 //
 // The draw's values are fp32 and compared in fp32 but for the foremost two and what
-// comes near the second: these are evaluated again in fp64, so that rounding
-// decides next to nothing, and the gap, which may be small, is good to 1e-9.
+// comes near the second: these are evaluated again as sums of two floats, so that
+// rounding decides next to nothing, and the gap, which may be small, is good to 1e-9.
 // Most tokens need no logarithm: g >= t only if 1 - u <= e^-t, and once there are
 // two values the noise's own bits decide.
 //
@@ -168,7 +168,6 @@ struct Shared {
   uint64_t warp_lo[kWarps], warp_hi[kWarps];
   Entry warp_best[2 * kWarps];
   float min_l;
-  double log_min_p;
 };
 
 // ------------------------------------------------- the cluster, if it is one
@@ -688,31 +687,50 @@ struct Key {  // of the row's noise
 __device__ __forceinline__ uint4 noise4(const Key& k, int id) {
   return philox4x32_10(make_uint4(static_cast<uint32_t>(id) / 4, k.pos, k.seq, 0u), k.k0, k.k1);
 }
-// ln a of a normal a > 0, to about 1e-11: a = 2^e m, m in [sqrt 1/2, sqrt 2), ln m =
-// 2 artanh s with s = (m - 1) / (m + 1) as the sum of two floats, its terms from s^5
-// on in fp32 (below 4e-5). Few operations are fp64: an SM has two such units, and
-// the general logarithm's chain took 1.3 us of a call with one row.
-__device__ __forceinline__ double ln_of(float a) {
+// A number as the sum of two floats, the second at most half a step of the first
+// (arithmetic on such pairs after Dekker, 1971, and Knuth): 48 bits without the
+// fp64 units, whose chains of a few dozen operations took 2.4 us of a call with
+// one row.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair sum_of_two(float a, float b) {
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+// ln a of a normal a > 0 to 1e-10: a = 2^e m, m in [sqrt 1/2, sqrt 2), ln m = 2
+// artanh s with s = (m - 1) / (m + 1); s and s^3 / 3 as pairs, the terms from s^5
+// on (below 4e-5) in fp32.
+__device__ __forceinline__ Pair ln_of(float a) {
   const uint32_t bits = __float_as_uint(a);
   const int e = (static_cast<int>(bits) - 0x3F3504F3) >> 23;
   const float m = __uint_as_float(bits - (static_cast<uint32_t>(e) << 23));
   const float num = m - 1.f, den = m + 1.f, den_low = m - (den - 1.f);  // num and den + den_low are exact
-  const float q = num / den, low = fmaf(-q, den_low, fmaf(-q, den, num)) / den, q2 = q * q;
-  const float tail = q2 * q2 * q * fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 0.2f);
-  const double s = static_cast<double>(q) + static_cast<double>(low);
-  return fma(static_cast<double>(e), 0.69314718055994530942, 2.0 * (s + fma(s * s * s, 1.0 / 3, static_cast<double>(tail))));
+  const float q = __fdiv_rn(num, den), low = __fdividef(fmaf(-q, den_low, fmaf(-q, den, num)), den);
+  const float q2 = __fmul_rn(q, q), q2_low = fmaf(q, q, -q2), cube = __fmul_rn(q2, q), cube_low = fmaf(q2_low, q, fmaf(q2, q, -cube));
+  constexpr float kThird = 1.f / 3, kThirdLow = -9.934107e-9f;
+  const float third = __fmul_rn(cube, kThird), third_low = fmaf(cube_low, kThird, fmaf(cube, kThirdLow, fmaf(cube, kThird, -third)));
+  const float tail = cube * q2 * fmaf(q2, fmaf(q2, fmaf(q2, fmaf(q2, 1.f / 13, 1.f / 11), 1.f / 9), 1.f / 7), 0.2f);
+  // ln 2 as 0.693145751953125, which e times is exact, and the rest
+  const Pair x = sum_of_two(static_cast<float>(e) * 0.693145751953125f, 2.f * q), y = sum_of_two(x.h, 2.f * third);
+  const float rest = 2.f * (fmaf(q2, low, low) + (third_low + tail)) + static_cast<float>(e) * 1.42860682e-6f;
+  return sum_of_two(y.h, y.l + (x.l + rest));
 }
 // The draw's value of a token, to 1e-9.
-__device__ __noinline__ double value64(const Row& w, const Key& k, float l, int id) {
+__device__ __noinline__ Pair value_pair(const Row& w, const Key& k, float l, int id) {
   const uint32_t word = word_of(noise4(k, id), id & 3);
-  const double y = -ln_of((static_cast<float>(word >> 9) + 0.5f) * (1.f / 8388608.f));
-  const float high = static_cast<float>(y), low = static_cast<float>(y - static_cast<double>(high));
-  const double ln_y = ln_of(high) + static_cast<double>(low / high);
-  return fma(static_cast<double>(l) - static_cast<double>(w.top), static_cast<double>(w.r), -ln_y);
+  const Pair y = ln_of((static_cast<float>(word >> 9) + 0.5f) * (1.f / 8388608.f)), ln_y = ln_of(-y.h);  // ln u < 0
+  const Pair d = sum_of_two(l, -w.top);
+  const float x = __fmul_rn(d.h, w.r);
+  const Pair z = sum_of_two(x, -ln_y.h);
+  return sum_of_two(z.h, z.l + (fmaf(d.l, w.r, fmaf(d.h, w.r, -x)) - (ln_y.l + __fdividef(y.l, y.h))));
 }
+// Pairs by their bits: larger is larger.
+__device__ __forceinline__ uint64_t key_of(const Pair& z) { return static_cast<uint64_t>(ord_key(z.h)) << 32 | ord_key(z.l); }
+
 // The row's token, by a warp that holds the entries that it can be: the two best
 // and what comes within the rounding of the second (fp32's and the noise's) are
-// evaluated again in fp64, which decides between them and gives the gap.
+// evaluated again as pairs, which decides between them and gives the gap.
 __device__ void decide(const Params& p, const Row& w, const Key& key, const Entry& e, bool exact, int row) {
   const int lane = threadIdx.x & 31;
   int at, next;
@@ -720,21 +738,25 @@ __device__ void decide(const Params& p, const Row& w, const Key& key, const Entr
   int id = a.id;
   float gap = a.z - b.z;
   if (!exact && b.z > -INFINITY) {
-    const float near = b.z - (2e-5f + 1e-6f * fabsf(b.z));
-    const double z = e.z >= near ? value64(w, key, e.l, e.id) : -INFINITY;
+    const bool near = e.z >= b.z - (2e-5f + 1e-6f * fabsf(b.z));
+    const uint64_t z = near ? key_of(value_pair(w, key, e.l, e.id)) : 0ull;
     __syncwarp();
-    double best = z;
-    id = e.z >= near ? e.id : kNoId;
+    uint64_t best = z;
+    id = near ? e.id : kNoId;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      const double u = __shfl_xor_sync(0xffffffffu, best, o);
+      const uint64_t u = __shfl_xor_sync(0xffffffffu, best, o);
       const int i = __shfl_xor_sync(0xffffffffu, id, o);
       if (u > best || (u == best && i < id)) best = u, id = i;
     }
-    double second = e.id == id ? -INFINITY : z;
+    uint64_t second = e.id == id ? 0ull : z;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) second = fmax(second, __shfl_xor_sync(0xffffffffu, second, o));
-    gap = static_cast<float>(best - second);
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t u = __shfl_xor_sync(0xffffffffu, second, o);
+      second = u > second ? u : second;
+    }
+    gap = (of_key(static_cast<uint32_t>(best >> 32)) - of_key(static_cast<uint32_t>(second >> 32))) +
+          (of_key(static_cast<uint32_t>(best)) - of_key(static_cast<uint32_t>(second)));
   }
   if (lane == 0 && GLANCE_IN_BOUNDS(row, p.M)) {
     p.tokens[row] = id;
@@ -957,7 +979,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) to_peer<kCtas>(&s->group[(w.rank * kThreads + t) / kOne], t % kOne * 4 + j, part);
   }
-  if (t == 0) s->log_min_p = min_p > 0.f && !greedy ? log(static_cast<double>(min_p)) : 0.0;
   sync_row<kCtas>();
   if (kCtas > 1) {
 #pragma unroll
@@ -981,14 +1002,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
     }
     return;
   }
-  // the least logit with (l - top) r >= ln min_p, in fp64
+  // the least logit with (l - top) r >= ln min_p: near it in fp32, then by the
+  // comparison in fp64
   w.min_l = -INFINITY;
   if (min_p > 0.f && !greedy) {
     if (t == 0) {
-      const double lg = fmin(s->log_min_p, 0.0), r = w.r, m = top;
-      float x = fminf(static_cast<float>(m + lg / r), top);
-      for (int i = 0; i < 4 && x > -INFINITY && (static_cast<double>(x) - m) * r >= lg; ++i) x = nextafterf(x, -INFINITY);
-      for (int i = 0; i < 8 && (static_cast<double>(x) - m) * r < lg; ++i) x = nextafterf(x, INFINITY);
+      const Pair ln = ln_of(fminf(fmaxf(min_p, 1.17549435e-38f), 1.f));
+      const double lg = static_cast<double>(ln.h) + static_cast<double>(ln.l), r = w.r, m = top;
+      float x = fminf(fmaf(ln.h, temperature, top), top);
+      for (int i = 0; i < 8 && x > -INFINITY && (static_cast<double>(x) - m) * r >= lg; ++i) x = nextafterf(x, -INFINITY);
+      for (int i = 0; i < 16 && x < top && (static_cast<double>(x) - m) * r < lg; ++i) x = nextafterf(x, INFINITY);
       s->min_l = x;
     }
     __syncthreads();
