@@ -15,6 +15,8 @@ It is a plain, slow restatement of what the pages define, in numpy float64:
 * ``lmhead``     LM-head projection with per-row greedy argmax and top-2 gap
   (the gap gamma_k of Theorem 1's full statement, Appendix B.1).
 * ``walk``       the acceptance walk, A(S) in its set form, and the KV commit.
+* ``q8``         rows in 8 bits (e4m3 with a power-of-two scale), their products.
+* ``truncated_sampling``  top-k, min-p and top-p before the draw of ``sampling``.
 * ``toy``        a small random-init decoder target with greedy autoregression
   and GLANCE rounds, for Theorem 1 (Section 4.2, Appendix B.1).
 

@@ -15,6 +15,10 @@ launch per step; the LM head takes the B requests' rows stacked.
                     or several for image and video tokens), k and v cached
 * ``kv4_*``         the round on K/V caches held in 4 bits: rows written and
                     read, tree attention (one row: decoding), walk + commit
+* ``q8_*``          the target's dense layers in 8 bits: residual + RMS norm +
+                    e4m3 rows, rows quantised and read, products with bias,
+                    activation (plain or gated) and residual fused
+* ``sample``        tokens from rows of logits: temperature, top-k, min-p, top-p
 """
 from ._binding import (STATUS_WORDS, BF16, EXPORTS, F32, LIB_PATH, GlanceError, KVLayer, Tree, accept_commit,
                        accept_commit_batched, accept_commit_batched_workspace_bytes,

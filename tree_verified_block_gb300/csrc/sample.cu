@@ -38,6 +38,13 @@
 // A row has one CTA, or a cluster of 4 or 16, by how many rows there are to fill
 // the GPU; a second pass over it reads from L2. Every decision that a cluster's
 // CTAs take by themselves is taken from values that all of them hold alike.
+//
+// Measured (V = 151936): one row, k 20, p 0.8, 7.9 us; 64 bf16 rows at p 0.95, most
+// of which keep 10^4 to 10^5 tokens, 68 us (issue slots 58 %: a token has a bin, a
+// comparison and a noise word); 512 fp32 rows with parameters of their own 139 to
+// 149 us (2.1 to 2.2 TB/s; a cluster's steps one after the other, at two CTAs per
+// SM). Clusters of 16, 4, 1: one row 7.9, 8.6, 14 us; 64 rows 146, 68, 122; 512 rows
+// 355, 149, 200.
 #include <cstring>
 #include <mutex>
 
@@ -1176,8 +1183,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
   finish(s, p, w, key, two, greedy, false, row);
 }
 
-// CTAs to a row: 16 while two such clusters' CTAs have an SM each, 4 beyond, as
-// long as each has enough of the row.
+// CTAs to a row: 16 while all of them are on the device at once (two per SM), 4
+// beyond, as long as each has enough of the row.
 int cluster_size(int M, int V) {
   if (M * 16 <= 2 * glance::num_sms() && V >= 16 * 2048) return 16;
   return V >= 4 * 2048 ? 4 : 1;
