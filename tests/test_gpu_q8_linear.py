@@ -185,3 +185,30 @@ def test_captured_replayed_and_overlapping_calls(dev, clean_status):
     torch.cuda.synchronize()
     for _, out, want in sets:
         assert torch.equal(out, want)
+
+
+def test_weights_written_just_before(dev, clean_status):
+    """Weights may be read before the previous kernel has ended, but not before a row call has: nor through a product between."""
+    import tree_verified_block_gb300 as g
+    gen = torch.Generator(device=dev).manual_seed(8)
+    for M in (1, 64, 300):
+        (x, xs), (w0, ws0) = codes(M, 4096, gen, dev), codes(2048, 4096, gen, dev)
+        src = [torch.randn(2048, 4096, generator=gen, device=dev).to(BF) for _ in range(3)]
+        w, ws = torch.zeros_like(w0), torch.zeros(2048, device=dev)
+        want, other = [], torch.zeros(M, 2048, device=dev)
+        for s in src:
+            g.q8_rows(s, w, ws)
+            torch.cuda.synchronize()
+            want.append(torch.zeros(M, 2048, device=dev))
+            g.q8_linear(x, xs, w, ws, want[-1])
+            torch.cuda.synchronize()
+        outs = [torch.zeros(M, 2048, device=dev) for _ in range(24)]
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            g.q8_rows(src[i % 3], w, ws)
+            if i % 2:
+                g.q8_linear(x, xs, w0, ws0, other)
+            g.q8_linear(x, xs, w, ws, o)
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            assert torch.equal(o, want[i % 3]), (M, i)

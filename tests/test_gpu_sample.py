@@ -195,3 +195,28 @@ def test_no_gap_captured_and_two_streams(dev, clean_status):
     torch.cuda.synchronize()
     for o in outs:
         assert np.array_equal(o.cpu().numpy(), tok)
+
+
+@pytest.mark.parametrize("M", [1, 10, 19, 20, 300])
+def test_row_counts_and_clustered_tokens(dev, clean_status, M):
+    """Every cluster size; the likely tokens next to each other, so that one CTA has them all."""
+    V = 40000
+    gen = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn(M, V, generator=gen, device=dev) - 4
+    x[:, 300:2900] += 9
+    pick = lambda *v: [v[i % len(v)] for i in range(M)]
+    check(dev, x, pick(1.0, 0.6, 1.4), pick(1500, 0, 20, 1537), pick(0.9, 0.99, 1.0, 0.7, 0.95), pick(0.0, 0.01))
+    check(dev, x.to(BF), pick(1.0, 1.4), pick(0, 1200), pick(0.97, 0.6, 0.999), None)
+
+
+def test_the_same_row_gives_the_same_token_in_any_batch(dev, clean_status):
+    import tree_verified_block_gb300 as g
+    V = 50000
+    x = rows(dev, 1, V, F32, 4)
+    seen = []
+    for M in (1, 19, 40, 200):
+        t = lambda v, dt=F32: torch.full((M,), v, dtype=dt, device=dev)
+        tokens, gap = t(0, torch.int32), t(0.0)
+        g.sample(x.expand(M, V).contiguous(), t(1.1), t(0, torch.int32), t(0.98), None, 3, t(77, torch.int32), None, tokens, gap)
+        seen += [tokens, gap]
+    assert all(int(a) == int(seen[0][0]) for t in seen[::2] for a in t) and all(float(a) == float(seen[1][0]) for t in seen[1::2] for a in t)

@@ -43,8 +43,8 @@
 // of which keep 10^4 to 10^5 tokens, 68 us (issue slots 58 %: a token has a bin, a
 // comparison and a noise word); 512 fp32 rows with parameters of their own 139 to
 // 149 us (2.1 to 2.2 TB/s; a cluster's steps one after the other, at two CTAs per
-// SM). Clusters of 16, 4, 1: one row 7.9, 8.6, 14 us; 64 rows 146, 68, 122; 512 rows
-// 355, 149, 200.
+// SM). Clusters of 16, 4, 1 (timed by eager calls): one row 10.3, 12.7, 16.2 us; 64 rows
+// 146, 68, 122; 512 rows 355, 149, 200.
 #include <cstring>
 #include <mutex>
 
@@ -388,6 +388,15 @@ __device__ __forceinline__ X scan_add(X v, int lane) {
   }
   return v;
 }
+// What the warps before this one have, of each warp's amount (weights: below 2^54).
+__device__ __forceinline__ uint32_t sum_before(const uint32_t* of_warp, int lane, int warp) {
+  return __reduce_add_sync(0xffffffffu, lane < warp ? of_warp[lane] : 0u);
+}
+__device__ __forceinline__ Mass sum_before(const Mass* of_warp, int lane, int warp) {
+  const Mass v = lane < warp ? of_warp[lane] : 0ull;
+  return (static_cast<Mass>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 26))) << 26) +
+         __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3FFFFFFu);
+}
 __device__ __forceinline__ Mass sum_of(uint32_t count, uint64_t sum) { return static_cast<Mass>(count) * kUnitOff + sum; }
 
 // The bin of the row's histogram in which the prefix of `want` tokens (want > 0)
@@ -592,12 +601,8 @@ __device__ Cut select_held(Shared<kCtas>* s, const Held& h, uint32_t want, Mass 
       s->warp_mass[warp] = mass_to;
     }
     __syncthreads();
-    uint32_t before = count0 + count_to - count;
-    Mass before_mass = mass0 + mass_to - mass;
-    for (int i = 0; i < warp; ++i) {
-      before += s->warp_count[i];
-      before_mass += s->warp_mass[i];
-    }
+    const uint32_t before = count0 + count_to - count + sum_before(s->warp_count, lane, warp);
+    const Mass before_mass = mass0 + mass_to - mass + (want ? 0 : sum_before(s->warp_mass, lane, warp));
     if (count && (want ? before < want && before + count >= want : before_mass < target && before_mass + mass >= target)) {
       s->found = t;
       s->border.count_before = before;
@@ -1048,8 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       const uint32_t count = s->part[t], count_to = scan_add(count, lane);
       if (lane == 31) s->warp_count[warp] = count_to;
       __syncthreads();
-      uint32_t before = count_to - count;
-      for (int i = 0; i < warp; ++i) before += s->warp_count[i];
+      const uint32_t before = count_to - count + sum_before(s->warp_count, lane, warp);
       if (before < want && before + count >= want) s->found = t;
       __syncthreads();
       const float x = (static_cast<float>(s->found) + 1.01f) * (32.f / kThreads) / w.r;
