@@ -219,12 +219,7 @@ __device__ __forceinline__ uint32_t add_first(uint32_t* local, uint32_t v) {  //
 
 // -------------------------------------------------------------------- the row
 
-__device__ __forceinline__ uint64_t number_of(float l, int id) {
-  return static_cast<uint64_t>(ord_key(l)) << kIdBits | static_cast<uint32_t>(kMaxV - 1 - id);
-}
-__device__ __forceinline__ int id_of(uint64_t number) { return kMaxV - 1 - static_cast<int>(number & (kMaxV - 1)); }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
-__device__ __forceinline__ float logit_of(uint64_t number) { return of_key(static_cast<uint32_t>(number >> kIdBits)); }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -240,6 +235,22 @@ struct Row {
   float min_l;              // tokens below are not kept
   int rank, first, n;       // ids first .. first + n - 1
 };
+
+// A bf16 logit's key is its upper half: the lower says only the sign, and a search
+// by numbers would go through its bits as well (64 rows of the nucleus case: 67.5
+// us with the whole key, 66.0 without).
+template <typename T>
+constexpr int kShortBy = sizeof(T) == 4 ? 0 : 16;
+template <typename T>
+__device__ __forceinline__ uint64_t number_of(float l, int id) {
+  return static_cast<uint64_t>(ord_key(l) >> kShortBy<T>) << kIdBits | static_cast<uint32_t>(kMaxV - 1 - id);
+}
+__device__ __forceinline__ int id_of(uint64_t number) { return kMaxV - 1 - static_cast<int>(number & (kMaxV - 1)); }
+template <typename T>
+__device__ __forceinline__ float logit_of(uint64_t number) {
+  const uint32_t k = static_cast<uint32_t>(number >> kIdBits) << kShortBy<T>;
+  return of_key(k & 0x80000000u ? k : k | ((1u << kShortBy<T>) - 1u));
+}
 
 // Four logits as they are stored.
 template <typename T>
@@ -275,10 +286,10 @@ __device__ __forceinline__ typename Four<T>::Raw load4(const Row& w, int i) {
 // through it ten to a hundred times, and the instructions of larger bodies took
 // longer to arrive than to run. A thread with its largest logit below `least` is
 // passed over.
-constexpr int kAhead = 4;
 template <typename T, typename F, typename G>
 __device__ __forceinline__ void each4(const Row& w, float least, F f, G after) {
   typedef typename Four<T>::Raw Raw;
+  constexpr int kAhead = 4;
   const bool mine = w.own >= least;
   if (!__any_sync(0xffffffffu, mine)) return;
   const int t = threadIdx.x, warp0 = 4 * (t & ~31);
@@ -534,14 +545,14 @@ struct Held {
   uint64_t number[kPer];
   Mass mass[kPer];
 };
-template <int kCtas>
+template <typename T, int kCtas>
 __device__ __forceinline__ Held hold_list(Shared<kCtas>* s, const Row& w, int n, bool weigh) {
   Held h;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = static_cast<int>(threadIdx.x) + j * kThreads;
     h.number[j] = e < n ? s->list[e] : 0ull;
-    h.mass[j] = weigh && e < n ? weight_of(w, logit_of(h.number[j])) : 0ull;
+    h.mass[j] = weigh && e < n ? weight_of(w, logit_of<T>(h.number[j])) : 0ull;
   }
   return h;
 }
@@ -641,7 +652,7 @@ __device__ uint32_t gather(Shared<kCtas>* s, const Row& w, int turn, float least
     if (l >= least && l <= most) {
       if (f(l, id)) {
         const uint32_t at = atomicAdd(n, 1u);
-        if (at < kList) to[at] = number_of(l, id);
+        if (at < kList) to[at] = number_of<T>(l, id);
       }
     }
   });
@@ -800,7 +811,7 @@ static_assert(2 * kWarps == 32, "a block's entries are a warp's");
 
 // The first CTA draws from its list of n tokens: the first `want` of them (0:
 // all), of these `share` of the weight (of mass_all, or of theirs if it is 0).
-template <int kCtas>
+template <typename T, int kCtas>
 __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, const Key& key, int n, uint32_t want, bool all_p, Mass share,
                                Mass mass_all, int row) {
   const int t = threadIdx.x;
@@ -808,20 +819,20 @@ __device__ void draw_from_list(Shared<kCtas>* s, const Params& p, const Row& w, 
   Two two = no_two();
   const auto draw = [&](uint64_t number) {
     const int id = id_of(number);
-    const float l = logit_of(number);
+    const float l = logit_of<T>(number);
     fold(two, (l - w.top) * w.r + gumbel_of(word_of(noise4(key, id), id & 3)), l, id);
   };
   if (n <= 32) {  // one warp's
     if (t >= 32) return;
     const uint64_t number = sort_warp(t < n ? s->list[t] : 0ull, t);
-    const Mass m = !all_p && t < kept ? weight_of(w, logit_of(number)) : 0ull;
+    const Mass m = !all_p && t < kept ? weight_of(w, logit_of<T>(number)) : 0ull;
     const Mass upto = scan_add(m, t), all = mass_all ? mass_all : __shfl_sync(0xffffffffu, upto, 31);
     if (t < kept && (all_p || upto - m < part_of(all, share))) draw(number);
     __syncwarp();
     decide(p, w, key, two.e[0], false, row);
     return;
   }
-  Held h = hold_list(s, w, n, !all_p);
+  Held h = hold_list<T, kCtas>(s, w, n, !all_p);
   uint64_t cut = 1;
   if (kept < n) {
     cut = select_held(s, h, want, 0, 0).number;
@@ -869,7 +880,7 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
       int at;
       float y;
       if (l >= least && l <= most && place(w, l, at, y) && at == bin) {
-        const uint64_t number = number_of(l, id);
+        const uint64_t number = number_of<T>(l, id);
         if (number >= lo && number <= hi) {
           least_n = number < least_n ? number : least_n;
           most_n = number > most_n ? number : most_n;
@@ -909,7 +920,7 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
       int at;
       float y;
       if (l >= least && l <= most && place(w, l, at, y) && at == bin) {
-        const uint64_t number = number_of(l, id);
+        const uint64_t number = number_of<T>(l, id);
         if (number >= lo && number <= hi) add_hist(s, static_cast<int>((hi - number) >> shift), y, !want);
       }
     });
@@ -923,12 +934,12 @@ __device__ Cut refine(Shared<kCtas>* s, const Row& w, const Border& first, uint6
   const uint32_t found = gather<T, kCtas>(s, w, turn, least, most, [&](float l, int id) {
     int at;
     float y;
-    const uint64_t number = number_of(l, id);
+    const uint64_t number = number_of<T>(l, id);
     return number >= lo && number <= hi && place(w, l, at, y) && at == bin;
   });
   if (w.rank == 0) {
     const int n = min(found, static_cast<uint32_t>(kList));
-    const Held h = hold_list(s, w, n, !want);
+    const Held h = hold_list<T, kCtas>(s, w, n, !want);
     const Cut c = select_held(s, h, want ? want - b.count_before : 0u, part_of(all, share), b.mass_before);
     if (t < kCtas) to_peer<kCtas>(&s->cut, t, c);
   }
@@ -1092,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       __syncwarp();
       if (kCtas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
       if (w.rank == 0) {
-        draw_from_list(s, p, w, key, static_cast<int>(upto), want, all_p, share, want ? 0 : b.mass_all, row);
+        draw_from_list<T, kCtas>(s, p, w, key, static_cast<int>(upto), want, all_p, share, want ? 0 : b.mass_all, row);
         // the others have read its counter
         __syncwarp();
         if (kCtas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1104,10 +1115,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       if (want && !all_p) {
         // the first k are known: the share of their weight ends at or before their last
         clear_hist(s);
-        each<T>(w, logit_of(cut), [&](float l, int id) {
+        each<T>(w, logit_of<T>(cut), [&](float l, int id) {
           int bin;
           float y;
-          if (place(w, l, bin, y) && number_of(l, id) >= cut) add_hist(s, bin, y, true);
+          if (place(w, l, bin, y) && number_of<T>(l, id) >= cut) add_hist(s, bin, y, true);
         });
         b = find_border(s, w, 0u, share, 0, 0.f, -1, 0u, 0);
         if (b.bin >= 0) {
@@ -1149,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Params p) {
       if (l > -INFINITY) fold(two, l, l, id);
     });
   } else {
-    const float cut_l = cut ? logit_of(cut) : -INFINITY;
+    const float cut_l = cut ? logit_of<T>(cut) : -INFINITY;
     const float least = fmaxf(fmaxf(cut_l, w.min_l), -3.4028234e38f);
     const int last = cut ? id_of(cut) : kMaxV;  // of the tokens with the cut's logit
     float second = -INFINITY;  // two of the CTA's values are no less
