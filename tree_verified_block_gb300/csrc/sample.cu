@@ -39,12 +39,12 @@
 // the GPU; a second pass over it reads from L2. Every decision that a cluster's
 // CTAs take by themselves is taken from values that all of them hold alike.
 //
-// Measured (V = 151936): one row, k 20, p 0.8, 7.9 us; 64 bf16 rows at p 0.95, most
-// of which keep 10^4 to 10^5 tokens, 68 us (issue slots 58 %: a token has a bin, a
+// Measured (V = 151936): one row, k 20, p 0.8, 7.8 us; 64 bf16 rows at p 0.95, most
+// of which keep 10^4 to 10^5 tokens, 66 us (issue slots 58 %: a token has a bin, a
 // comparison and a noise word); 512 fp32 rows with parameters of their own 139 to
-// 149 us (2.1 to 2.2 TB/s; a cluster's steps one after the other, at two CTAs per
+// 146 us (2.1 to 2.2 TB/s; a cluster's steps one after the other, at two CTAs per
 // SM). Clusters of 16, 4, 1 (timed by eager calls): one row 10.3, 12.7, 16.2 us; 64 rows
-// 146, 68, 122; 512 rows 355, 149, 200.
+// 146, 68, 122; 512 rows 355, 149, 200. 4096 rows of 8191 bf16 at p 0.95: 251 us.
 #include <cstring>
 #include <mutex>
 
@@ -141,11 +141,9 @@ struct Cut {
 
 template <int kCtas>
 struct Shared {
-  // a CTA with a whole row adds its warps' sums to four places: 2^16 tokens each at most
-  static constexpr int kSums = kCtas == 1 ? 4 : 1;
   union {
     struct {
-      uint32_t count[kBins], sum[kSums][kBins];
+      uint32_t count[kBins], sum[kBins];  // (of 2^16 tokens at most: a CTA has no more)
     };
     struct {  // of a search in the list's tokens: a bin's weight in two parts
       uint32_t bin_count[kThreads], bin_low[kThreads], bin_high[kThreads];
@@ -378,7 +376,7 @@ __device__ __forceinline__ float most_of_bin(const Row& w, int bin) {
 template <int kCtas>
 __device__ __forceinline__ void clear_hist(Shared<kCtas>* s) {
   uint4* h = reinterpret_cast<uint4*>(s->count);
-  for (int i = threadIdx.x; i < kBins * (1 + Shared<kCtas>::kSums) / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < 2 * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 }
 template <int kCtas>
@@ -387,7 +385,7 @@ __device__ __forceinline__ void add_hist(Shared<kCtas>* s, int bin, float y, boo
   if (!weigh) return;
   // (1 + y) 2^21 rounded, from the low bits of a float, less the base
   const uint32_t f = (__float_as_uint(fmaf(y, 2097152.f, 2097152.f + 8388608.f)) & 0x7FFFFFu) - kUnitOff;
-  atomicAdd(&s->sum[(threadIdx.x >> 5) & (Shared<kCtas>::kSums - 1)][bin], f);
+  atomicAdd(&s->sum[bin], f);
 }
 
 template <typename X>
@@ -408,7 +406,7 @@ __device__ __forceinline__ Mass sum_before(const Mass* of_warp, int lane, int wa
   return (static_cast<Mass>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 26))) << 26) +
          __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3FFFFFFu);
 }
-__device__ __forceinline__ Mass sum_of(uint32_t count, uint64_t sum) { return static_cast<Mass>(count) * kUnitOff + sum; }
+__device__ __forceinline__ Mass sum_of(uint32_t count, uint32_t sum) { return static_cast<Mass>(count) * kUnitOff + sum; }
 
 // The bin of the row's histogram in which the prefix of `want` tokens (want > 0)
 // or else of `share` of the weight (of mass_all if given, else of what there is)
@@ -429,11 +427,8 @@ __device__ Border find_border(Shared<kCtas>* s, const Row& w, uint32_t want, Mas
     const int bin = t * kEach + j;
     const uint32_t c = s->count[bin];
     if (c) {
-      uint64_t sum = 0;
-#pragma unroll
-      for (int i = 0; i < Shared<kCtas>::kSums; ++i) sum += s->sum[i][bin];
       count += c;
-      mass += mass_of(weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin), sum_of(c, sum));
+      mass += mass_of(weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin), sum_of(c, s->sum[bin]));
     }
   }
 #pragma unroll
@@ -494,10 +489,7 @@ __device__ Border find_border(Shared<kCtas>* s, const Row& w, uint32_t want, Mas
   if (b.bin < 0) return b;
   for (int q = warp; q < kCtas; q += kWarps) {
     const int bin = b.bin * kFine + lane;
-    const uint32_t c = peer_u32<kCtas>(&s->count[bin], q);
-    uint64_t sum = 0;
-#pragma unroll
-    for (int i = 0; i < Shared<kCtas>::kSums; ++i) sum += peer_u32<kCtas>(&s->sum[i][bin], q);
+    const uint32_t c = peer_u32<kCtas>(&s->count[bin], q), sum = peer_u32<kCtas>(&s->sum[bin], q);
     s->fine_count[q][lane] = c;
     s->fine_mass[q][lane] = c ? mass_of(weight_of_bin(fixed_bin >= 0 ? fixed_bin : bin), sum_of(c, sum)) : 0;
   }
