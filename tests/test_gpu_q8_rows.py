@@ -155,3 +155,25 @@ def test_captured_and_on_another_stream(dev, clean_status):
     g.q8_norm_rows(x, r, None, 1e-6, total, codes, scales, stream=side)
     side.synchronize()
     assert torch.equal(codes, want[0])
+
+
+def test_middles_of_normed_fp32_rows(dev, clean_status):
+    """A value lands on the other side of the middle of two codes where y's error e, relative, reaches past it: one of
+    2 e 2^3.5 values (middles are 2^-3 to 2^-4 of a value apart). What three products, root and quotient round (2^-24 in all)
+    would make 16 of 2^24 values; with their remainders the sum of squares is left, whose first five levels 4 to 16 warps round
+    by themselves (2^-25 each at most, 2^-27 in the mean, on the root half): 2 of 2^24. Up to 7 is within three times the root."""
+    import tree_verified_block_gb300 as g
+    gen = torch.Generator(device=dev).manual_seed(5)
+    off = 0
+    for M, d in ((2048, 2048), (1024, 4096), (4096, 1024), (512, 8192)):
+        x, r = (torch.randn(M, d, generator=gen, device=dev) for _ in range(2))
+        w = 1 + 0.3 * torch.randn(d, generator=gen, device=dev)
+        codes, scales = empty8(M, d, 0, dev), torch.zeros(M, device=dev)
+        g.q8_norm_rows(x, r, w, 1e-6, None, codes, scales)
+        s = (x + r).double()
+        y = s / torch.sqrt(s.pow(2).mean(1, keepdim=True) + float(np.float32(1e-6))) * w.double() / scales.double()[:, None]
+        step = torch.exp2(torch.floor(torch.log2(y.abs())).clamp(min=-6) - 3)
+        near = torch.round(y / step) * step  # to even where two are as near
+        values = codes.view(torch.float8_e4m3fn).double()
+        off += int((values != near)[y.abs() >= 2.0 ** -6].sum())
+    assert off <= 7, off
